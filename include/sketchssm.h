@@ -326,6 +326,102 @@ ssm_status ssm_recurrent_decode_step(const ssm_dims* d,
                                      float* y, void* stream);
 
 /*
+ * Whole sequences at once: prompt processing, which makes the states that the
+ * decode calls above start from, and its gradients. (Not on the pages, which
+ * start at the decode: agihunt.info summary, "Confirmed", background bullet, on
+ * the recurrent state; the recurrence is the one above.) A packed batch holds
+ * d->batch sequences one after another:
+ *   q, k        in    [total_tokens][H][d_k]       v  in  [total_tokens][H][d_v]
+ *   decay       fp32  [total_tokens][H] or [total_tokens][H][d_k] (KDA)
+ *   beta        fp32  [total_tokens][H] (GDN, KDA); NULL for Mamba-2
+ *   y, dy       fp32  [total_tokens][H][d_v]
+ *   plan        int32, as ssm_scan_plan writes it from the sequences' lengths:
+ *               [seq_start (n + 1) | chunk_start (n + 1) | chunk_seq (total_tokens/64 + n)]
+ *               with n = d->batch: sequence s owns tokens seq_start[s] .. seq_start[s+1] and
+ *               the 64-token chunks chunk_start[s] .. chunk_start[s+1]; chunk_seq names a
+ *               chunk's sequence, -1 past the last chunk. One plan serves every layer.
+ * Sequences may be empty. Tokens behind the last sequence are neither read nor
+ * written. A plan's entries are DEVICE data and are not read on the host; whatever
+ * they hold, no token outside [0, total_tokens) is touched (an entry that no plan
+ * has skips its chunk or sequence). Gates are meant to be in [0, 1]; 0 and 1 are exact.
+ * Scalar decays, beta, their gradients and the plan need 4-byte alignment only.
+ * A non-finite value of a token may reach outputs of its own sequence up to 15
+ * tokens before it (tokens are taken 16 at a time), never another sequence or head.
+ * Sums and states are fp32. d->window and d->rank are checked but not used.
+ * (total_tokens/64 + batch)*heads < 2^22. Results do not depend on the batch's
+ * other sequences and are the same bits from run to run.
+ */
+
+/* Sizes for a packed batch: int32 elements of the plan, and the bytes of the
+ * workspace of ssm_scan_forward and ssm_scan_backward. Any output may be NULL. */
+ssm_status ssm_scan_sizes(const ssm_dims* d, int32_t total_tokens, int64_t* plan_ints,
+                          int64_t* forward_bytes, int64_t* backward_bytes);
+
+/*
+ * The plan of a packed batch, built on the device from the sequences' lengths
+ * (DEVICE int32 [n_seqs], 0 <= n_seqs < 2^24). A negative length counts as 0;
+ * sequences are cut where the arrays end (total_tokens). plan: int32, the size
+ * that ssm_scan_sizes gives for batch = n_seqs. Both need 4-byte alignment.
+ * n_seqs = 0 is a no-op. One launch.
+ */
+ssm_status ssm_scan_plan(const int32_t* lengths, int32_t n_seqs, int32_t total_tokens,
+                         int32_t* plan, void* stream);
+
+/*
+ * For every sequence and head: S <- M_t S + b_t k_t v_t^T and y_t = S^T q_t over
+ * its tokens, from the state in state_in (NULL: from zero), which ends in state.
+ * Both states are pools [num_slots][H][d_k][d_v] indexed by slot[s] (DEVICE int32
+ * [batch], NULL: slot s); state_in may be state itself, which continues a prompt
+ * in place. A sequence whose slot is outside [0, num_slots) is skipped (its y and
+ * state are not written); the sequences must map to distinct slots. An empty
+ * sequence's state is its state_in. The workspace (16-byte aligned, at least
+ * ssm_scan_sizes' forward_bytes) holds nothing between calls; calls that may run
+ * at the same time, captured graphs among them, need one each.
+ * Outputs: state, y, workspace.
+ */
+ssm_status ssm_scan_forward(const ssm_dims* d, int32_t total_tokens, const int32_t* plan,
+                            int32_t num_slots, const int32_t* slot, const float* state_in,
+                            const void* q, const void* k, const void* v, const float* decay,
+                            const float* beta, float* state, float* y, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of ssm_scan_forward (slots 0 .. batch-1) for a loss whose gradients
+ * with respect to y and the final states are dy and dstate ([batch][H][d_k][d_v],
+ * NULL: zero). dq, dk, dv have the inputs' type (bf16: rounded once, to nearest);
+ * dbeta (NULL for Mamba-2) and dstate_in (NULL: not wanted) are fp32;
+ * dlog_decay is fp32 in decay's shape and holds decay * dL/d(decay), the gradient
+ * with respect to ln(decay), which stays finite at decay = 0 (where it is 0). The
+ * states are computed again from the inputs: nothing is kept from the forward call.
+ * Gradients of tokens behind the last sequence are not written. The workspace as
+ * in ssm_scan_forward, with backward_bytes.
+ * Outputs: dq, dk, dv, dlog_decay, dbeta, dstate_in, workspace.
+ */
+ssm_status ssm_scan_backward(const ssm_dims* d, int32_t total_tokens, const int32_t* plan,
+                             const float* state_in, const void* q, const void* k, const void* v,
+                             const float* decay, const float* beta, const float* dy,
+                             const float* dstate, void* dq, void* dk, void* dv,
+                             float* dlog_decay, float* dbeta, float* dstate_in, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/*
+ * The index arrays of ssm_decode_step_varlen, built on the device (so a serving
+ * loop needs no host arithmetic per step and can be captured into a graph). For
+ * every row n, from lengths[n] = the number of tokens the row has decoded before
+ * this step (its prompt not counted; negative: a padding row):
+ *   tau[n]    = lengths[n] mod W + 1   (0 for a padding row, which the step skips)
+ *   parity[n] = (lengths[n] / W) mod 2 (0 for a padding row)
+ *   update_rows: the rows with tau = W, in ascending order, then -1; *n_update of them.
+ * d->batch rows; W = d->window; the other dims are checked but not used. All arrays
+ * DEVICE int32 [batch] (n_update: one element), 4-byte aligned. A step that takes
+ * n_update = d->batch with these update_rows updates exactly the listed rows: the
+ * entries of -1 are skipped. One launch.
+ */
+ssm_status ssm_window_plan(const ssm_dims* d, const int32_t* lengths, int32_t* tau,
+                           int32_t* parity, int32_t* update_rows, int32_t* n_update,
+                           void* stream);
+
+/*
  * Offline basis fit on the device. The pages fix the query basis offline
  * (readsearch.ai listing, Abstract; agihunt.info "Confirmed", mechanism bullet:
  * queries are compressed onto a small low-rank basis); the Mamba-2 workload's

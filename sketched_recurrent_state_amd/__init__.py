@@ -23,8 +23,8 @@ __all__ = [
     "full_read_decode_step", "recurrent_decode_step", "window_update_refresh_ranked",
     "sketch_decode_step_ranked", "rank_offsets", "window_update_refresh_varlen",
     "sketch_decode_step_varlen", "decode_step_varlen", "window_update_refresh_ls",
-    "sketch_decode_step_ls",
-    "fit_basis", "stream_probe", "SKETCH_F32", "SKETCH_BF16", "LIB_PATH", "HEADER",
+    "sketch_decode_step_ls", "scan_sizes", "scan_plan", "scan_forward", "scan_backward",
+    "window_plan", "fit_basis", "stream_probe", "SKETCH_F32", "SKETCH_BF16", "LIB_PATH", "HEADER",
     "declared_symbols", "numel", "library",
 ]
 
@@ -113,6 +113,17 @@ def _load():
     lib.ssm_sketch_decode_step_ls.argtypes = [dp] + [vp] * 11 + [i32, vp, vp]
     lib.ssm_fit_basis.restype = i32
     lib.ssm_fit_basis.argtypes = [dp, vp, i32, vp, vp]
+    i64 = ctypes.c_int64
+    lib.ssm_scan_sizes.restype = i32
+    lib.ssm_scan_sizes.argtypes = [dp, i32] + [ctypes.POINTER(i64)] * 3
+    lib.ssm_scan_plan.restype = i32
+    lib.ssm_scan_plan.argtypes = [vp, i32, i32, vp, vp]
+    lib.ssm_scan_forward.restype = i32
+    lib.ssm_scan_forward.argtypes = [dp, i32, vp, i32] + [vp] * 10 + [i64, vp]
+    lib.ssm_scan_backward.restype = i32
+    lib.ssm_scan_backward.argtypes = [dp, i32] + [vp] * 16 + [i64, vp]
+    lib.ssm_window_plan.restype = i32
+    lib.ssm_window_plan.argtypes = [dp] + [vp] * 6
     lib.ssm_stream_probe.restype = i32
     lib.ssm_stream_probe.argtypes = [vp, ctypes.c_int64, i32, vp]
     return lib
@@ -524,3 +535,123 @@ def sketch_decode_step_ls(d: Dims, sketch_q, read_map, q, k_buf, v_buf, decay_bu
         _addr(decay_buf, "decay_buf", f32, n["decay_buf"]),
         _addr(beta_buf, "beta_buf", f32, n["beta_buf"]), int(tau), _addr(y, "y", f32, n["y"]),
         _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# whole sequences and serving plans
+# ----------------------------------------------------------------------------
+def _on_device(args, stream, call) -> None:
+    """call(stream address) on the device that the tensors among args share: their device
+    becomes the current one for the call, and its current stream is the default."""
+    devs = {a.device for a in args if a is not None and not isinstance(a, int)}
+    if len(devs) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    if not devs or not next(iter(devs)).type == "cuda":
+        return call(_stream(stream))  # raw addresses (a CPU tensor was refused before)
+    import torch
+    with torch.cuda.device(devs.pop()):
+        call(_stream(stream))
+
+
+def scan_sizes(d: Dims, total_tokens: int) -> tuple:
+    """(int32 elements of the plan, workspace bytes of scan_forward, of scan_backward)."""
+    got = [ctypes.c_int64() for _ in range(3)]
+    _check(_lib.ssm_scan_sizes(ctypes.byref(d), int(total_tokens), *map(ctypes.byref, got)))
+    return tuple(int(x.value) for x in got)
+
+
+def scan_plan(lengths, total_tokens: int, plan, *, n_seqs: Optional[int] = None,
+              stream=None) -> None:
+    """ssm_scan_plan: the plan of a packed batch from its sequences' lengths (int32 [n]).
+    plan: int32, 2 (n + 1) + total_tokens // 64 + n elements. n_seqs is needed with raw addresses."""
+    n = int(lengths.numel() if n_seqs is None else n_seqs)
+    raw = isinstance(lengths, int) or isinstance(plan, int)
+    i32 = None if raw else _i32()
+    args = (_addr(lengths, "lengths", i32, n),
+            _addr(plan, "plan", i32, 2 * (n + 1) + int(total_tokens) // 64 + n))
+    _on_device((lengths, plan), stream, lambda s: _check(
+        _lib.ssm_scan_plan(args[0], n, int(total_tokens), args[1], s)))
+
+
+def _packed(d: Dims, total_tokens: int, plan, q, k, v, decay, beta):
+    """Addresses of a packed batch's arrays."""
+    rows = int(total_tokens) * d.heads
+    gate = rows * (d.d_k if d.rule == KDA else 1)
+    tin, f32 = _types(d, (plan, q, k, v, decay, beta))
+    i32 = None if tin is None else _i32()
+    return (_addr(plan, "plan", i32, scan_sizes(d, total_tokens)[0]),
+            _addr(q, "q", tin, rows * d.d_k), _addr(k, "k", tin, rows * d.d_k),
+            _addr(v, "v", tin, rows * d.d_v), _addr(decay, "decay", f32, gate),
+            _addr(beta, "beta", f32, rows))
+
+
+def _scan_workspace(workspace, nbytes: int, args, stream):
+    """A workspace of nbytes: the caller's, or one of its own from PyTorch."""
+    import torch
+    if isinstance(workspace, int):
+        raise ValueError("workspace: expected a device tensor or None")
+    if workspace is not None:
+        _addr(workspace, "workspace")
+        have = workspace.numel() * workspace.element_size()
+        return workspace, have
+    dev = next((a.device for a in args if a is not None and not isinstance(a, int)), None)
+    if dev is None:
+        raise ValueError("workspace: raw addresses need a workspace tensor")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if stream is not None and nbytes:  # used there, allocated on the current stream
+        ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=dev)
+                         if isinstance(stream, int) else stream)
+    return ws, nbytes
+
+
+def scan_forward(d: Dims, total_tokens: int, plan, q, k, v, decay, beta, state, y, *,
+                 state_in=None, slot=None, num_slots: Optional[int] = None, workspace=None,
+                 stream=None) -> None:
+    """ssm_scan_forward: a packed batch of d.batch sequences through the recurrence; y
+    [total_tokens][H][d_v] and the final states [num_slots][H][d_k][d_v] (num_slots defaults to
+    d.batch), from state_in (None: zero; may be `state` itself). workspace: a device tensor of
+    scan_sizes(...)[1] bytes, or None to take one from PyTorch for the call."""
+    ns = d.batch if num_slots is None else int(num_slots)
+    args = (plan, q, k, v, decay, beta, state, y, state_in, slot)
+    packed = _packed(d, total_tokens, plan, q, k, v, decay, beta)
+    f32 = None if all(a is None or isinstance(a, int) for a in args) else _f32()
+    states = ns * d.heads * d.d_k * d.d_v
+    at = (_addr(slot, "slot", None if f32 is None else _i32(), d.batch),
+          _addr(state_in, "state_in", f32, states), *packed[1:],
+          _addr(state, "state", f32, states),
+          _addr(y, "y", f32, int(total_tokens) * d.heads * d.d_v))
+    ws, have = _scan_workspace(workspace, scan_sizes(d, total_tokens)[1], args, stream)
+    _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_scan_forward(
+        ctypes.byref(d), int(total_tokens), packed[0], ns, *at, ws.data_ptr(), have, s)))
+
+
+def scan_backward(d: Dims, total_tokens: int, plan, q, k, v, decay, beta, dy, dq, dk, dv,
+                  dlog_decay, dbeta, *, state_in=None, dstate=None, dstate_in=None,
+                  workspace=None, stream=None) -> None:
+    """ssm_scan_backward: the gradients of scan_forward (dlog_decay is decay * dL/d(decay)).
+    workspace: a device tensor of scan_sizes(...)[2] bytes, or None."""
+    args = (plan, q, k, v, decay, beta, dy, dq, dk, dv, dlog_decay, dbeta, state_in, dstate,
+            dstate_in)
+    packed = _packed(d, total_tokens, plan, q, k, v, decay, beta)
+    tin, f32 = _types(d, args)
+    rows = int(total_tokens) * d.heads
+    states = d.batch * d.heads * d.d_k * d.d_v
+    at = (_addr(dy, "dy", f32, rows * d.d_v), _addr(dstate, "dstate", f32, states),
+          _addr(dq, "dq", tin, rows * d.d_k), _addr(dk, "dk", tin, rows * d.d_k),
+          _addr(dv, "dv", tin, rows * d.d_v),
+          _addr(dlog_decay, "dlog_decay", f32, rows * (d.d_k if d.rule == KDA else 1)),
+          _addr(dbeta, "dbeta", f32, rows), _addr(dstate_in, "dstate_in", f32, states))
+    ws, have = _scan_workspace(workspace, scan_sizes(d, total_tokens)[2], args, stream)
+    _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_scan_backward(
+        ctypes.byref(d), int(total_tokens), packed[0],
+        _addr(state_in, "state_in", f32, states), *packed[1:], *at, ws.data_ptr(), have, s)))
+
+
+def window_plan(d: Dims, lengths, tau, parity, update_rows, n_update, stream=None) -> None:
+    """ssm_window_plan: tau, parity, update_rows (int32 [d.batch] each) and n_update (one int32)
+    of a serving step from the tokens each row has decoded (int32 [d.batch], negative: padding)."""
+    args = (lengths, tau, parity, update_rows, n_update)
+    i32 = None if all(isinstance(a, int) or a is None for a in args) else _i32()
+    names = ("lengths", "tau", "parity", "update_rows", "n_update")
+    at = [_addr(a, x, i32, 1 if x == "n_update" else d.batch) for a, x in zip(args, names)]
+    _on_device(args, stream, lambda s: _check(_lib.ssm_window_plan(ctypes.byref(d), *at, s)))

@@ -24,7 +24,8 @@ SOURCES = ["abi.hip", "update_refresh.hip", "update_refresh_mamba2.hip", "update
            "update_refresh_kda.hip", "decode.hip", "sketch_decode_mamba2.hip",
            "sketch_decode_gdn.hip", "sketch_decode_kda.hip", "decode_step_mamba2.hip",
            "decode_step_gdn.hip", "decode_step_kda.hip", "append.hip", "recurrent.hip",
-           "fit_basis.hip", "stream_probe.hip"]
+           "fit_basis.hip", "stream_probe.hip", "plan.hip", "scan_mamba2.hip", "scan_gdn.hip",
+           "scan_kda.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

@@ -8,6 +8,7 @@
 #include <string>
 
 #include "launch.hpp"
+#include "scan.hpp"
 #include "sketchssm.h"
 
 namespace {
@@ -195,6 +196,69 @@ Sizes pool_sizes(const ssm_dims& d, int32_t num_slots) {
   z.dbuf = zp.dbuf;
   z.bbuf = zp.bbuf;
   return z;
+}
+
+// Whole-sequence calls: the cells (chunk, head) of a packed batch bound every grid of the scan
+// (at most 512 threads a cell), so this keeps them below 2^32 threads.
+constexpr long long kMaxCells = 1LL << 22;
+
+ssm_status check_scan(const ssm_dims* d, int32_t total_tokens, const char* fn) {
+  ssm_status st = check_dims(d, fn);
+  if (st != SSM_OK) return st;
+  if (total_tokens < 0) return fail(SSM_E_SHAPE, "%s: total_tokens %d < 0", fn, total_tokens);
+  const long long cells =
+      ((long long)total_tokens / ssm::CT + d->batch) * d->heads;
+  if (cells >= kMaxCells)
+    return fail(SSM_E_SHAPE, "%s: (total_tokens/64 + batch)*heads = %lld >= %lld", fn, cells,
+                kMaxCells);
+  return SSM_OK;
+}
+
+// The token arrays of a packed batch; they may be NULL when it holds no token.
+ssm_status check_packed(const ssm_dims& d, int32_t total_tokens, const int32_t* plan,
+                        const void* q, const void* k, const void* v, const void* decay,
+                        const void* beta, const char* fn) {
+  if (plan == nullptr) return fail(SSM_E_NULL, "%s: plan is NULL", fn);
+  if (total_tokens == 0) return SSM_OK;
+  if (q == nullptr) return fail(SSM_E_NULL, "%s: q is NULL", fn);
+  if (k == nullptr) return fail(SSM_E_NULL, "%s: k is NULL", fn);
+  if (v == nullptr) return fail(SSM_E_NULL, "%s: v is NULL", fn);
+  if (decay == nullptr) return fail(SSM_E_NULL, "%s: decay is NULL", fn);
+  return check_beta(d, beta, "beta", fn);
+}
+
+ssm_status check_workspace(const void* workspace, int64_t bytes, size_t need, const char* fn) {
+  if (need > 0 && workspace == nullptr) return fail(SSM_E_NULL, "%s: workspace is NULL", fn);
+  if (bytes < 0 || (size_t)bytes < need)
+    return fail(SSM_E_RANGE, "%s: workspace of %lld bytes, %zu needed", fn, (long long)bytes, need);
+  return SSM_OK;
+}
+
+struct PackedSizes {
+  size_t plan, qk, v, gate, beta, y;
+  unsigned gate_align;  // one value per token is read alone, KDA's channels four at a time
+};
+
+PackedSizes packed_sizes(const ssm_dims& d, int32_t total_tokens) {
+  const size_t rows = (size_t)total_tokens * d.heads, e = d.in_dtype == SSM_IN_BF16 ? 2 : 4;
+  PackedSizes z;
+  z.plan = (2 * ((size_t)d.batch + 1) + ssm::scan_capacity(total_tokens, d.batch)) * 4;
+  z.qk = rows * d.d_k * e;
+  z.v = rows * d.d_v * e;
+  z.gate = rows * (d.rule == SSM_KDA ? d.d_k : 1) * 4;
+  z.gate_align = d.rule == SSM_KDA ? 16 : 4;
+  z.beta = rows * 4;
+  z.y = rows * d.d_v * 4;
+  return z;
+}
+
+hipError_t launch_scan(const ssm_dims& d, const ssm::ScanArgs& a, bool backward, void* stream) {
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  switch (d.rule) {
+    case SSM_MAMBA2: return ssm::launch_scan_rule<ssm::MAMBA2>(d, a, backward, s);
+    case SSM_GDN: return ssm::launch_scan_rule<ssm::GDN>(d, a, backward, s);
+  }
+  return ssm::launch_scan_rule<ssm::KDA>(d, a, backward, s);
 }
 
 ssm_status launched(hipError_t e, const char* fn) {
@@ -595,6 +659,163 @@ ssm_status ssm_decode_step_varlen(const ssm_dims* d, int32_t num_slots, const in
                                           v_t, decay_t, beta_t, k_buf, v_buf, decay_buf,
                                           beta_buf, y, reinterpret_cast<hipStream_t>(stream)),
                   fn);
+}
+
+ssm_status ssm_scan_sizes(const ssm_dims* d, int32_t total_tokens, int64_t* plan_ints,
+                          int64_t* forward_bytes, int64_t* backward_bytes) {
+  static const char* fn = "ssm_scan_sizes";
+  const ssm_status st = check_scan(d, total_tokens, fn);
+  if (st != SSM_OK) return st;
+  if (plan_ints != nullptr) *plan_ints = (int64_t)(packed_sizes(*d, total_tokens).plan / 4);
+  if (forward_bytes != nullptr)
+    *forward_bytes = (int64_t)ssm::scan_work(*d, total_tokens, false, nullptr).bytes;
+  if (backward_bytes != nullptr)
+    *backward_bytes = (int64_t)ssm::scan_work(*d, total_tokens, true, nullptr).bytes;
+  return ok();
+}
+
+ssm_status ssm_scan_plan(const int32_t* lengths, int32_t n_seqs, int32_t total_tokens,
+                         int32_t* plan, void* stream) {
+  static const char* fn = "ssm_scan_plan";
+  if (n_seqs < 0 || n_seqs >= kMaxUnits)
+    return fail(SSM_E_SHAPE, "%s: n_seqs %d not in [0, 2^24)", fn, n_seqs);
+  if (total_tokens < 0) return fail(SSM_E_SHAPE, "%s: total_tokens %d < 0", fn, total_tokens);
+  if (n_seqs == 0) return ok();
+  if (lengths == nullptr) return fail(SSM_E_NULL, "%s: lengths is NULL", fn);
+  if (plan == nullptr) return fail(SSM_E_NULL, "%s: plan is NULL", fn);
+  const size_t ints = 2 * ((size_t)n_seqs + 1) + ssm::scan_capacity(total_tokens, n_seqs);
+  const ssm_status st = check_arrays(fn, {{lengths, (size_t)n_seqs * 4, false, "lengths", 4},
+                                          {plan, ints * 4, true, "plan", 4}});
+  if (st != SSM_OK) return st;
+  (void)hipGetLastError();
+  return launched(ssm::launch_scan_plan(lengths, n_seqs, total_tokens, plan,
+                                        reinterpret_cast<hipStream_t>(stream)),
+                  fn);
+}
+
+ssm_status ssm_window_plan(const ssm_dims* d, const int32_t* lengths, int32_t* tau,
+                           int32_t* parity, int32_t* update_rows, int32_t* n_update,
+                           void* stream) {
+  static const char* fn = "ssm_window_plan";
+  ssm_status st = check_dims(d, fn);
+  if (st != SSM_OK) return st;
+  if (d->batch == 0) return ok();
+  if (lengths == nullptr) return fail(SSM_E_NULL, "%s: lengths is NULL", fn);
+  if (tau == nullptr) return fail(SSM_E_NULL, "%s: tau is NULL", fn);
+  if (parity == nullptr) return fail(SSM_E_NULL, "%s: parity is NULL", fn);
+  if (update_rows == nullptr) return fail(SSM_E_NULL, "%s: update_rows is NULL", fn);
+  if (n_update == nullptr) return fail(SSM_E_NULL, "%s: n_update is NULL", fn);
+  const size_t rows = (size_t)d->batch * 4;
+  st = check_arrays(fn, {{lengths, rows, false, "lengths", 4}, {tau, rows, true, "tau", 4},
+                         {parity, rows, true, "parity", 4},
+                         {update_rows, rows, true, "update_rows", 4},
+                         {n_update, 4, true, "n_update", 4}});
+  if (st != SSM_OK) return st;
+  (void)hipGetLastError();
+  return launched(ssm::launch_window_plan(lengths, d->batch, d->window, tau, parity, update_rows,
+                                          n_update, reinterpret_cast<hipStream_t>(stream)),
+                  fn);
+}
+
+ssm_status ssm_scan_forward(const ssm_dims* d, int32_t total_tokens, const int32_t* plan,
+                            int32_t num_slots, const int32_t* slot, const float* state_in,
+                            const void* q, const void* k, const void* v, const float* decay,
+                            const float* beta, float* state, float* y, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
+  static const char* fn = "ssm_scan_forward";
+  ssm_status st = check_scan(d, total_tokens, fn);
+  if (st != SSM_OK) return st;
+  if (d->batch == 0) return ok();
+  if ((st = check_packed(*d, total_tokens, plan, q, k, v, decay, beta, fn)) != SSM_OK) return st;
+  if ((st = check_pool(*d, num_slots, slot, plan, "plan", fn)) != SSM_OK) return st;
+  if (state == nullptr) return fail(SSM_E_NULL, "%s: state is NULL", fn);
+  if (y == nullptr && total_tokens > 0) return fail(SSM_E_NULL, "%s: y is NULL", fn);
+  const ssm::ScanWork w = ssm::scan_work(*d, total_tokens, false, workspace);
+  if ((st = check_workspace(workspace, workspace_bytes, w.bytes, fn)) != SSM_OK) return st;
+  const PackedSizes z = packed_sizes(*d, total_tokens);
+  const size_t states = pool_sizes(*d, num_slots).state;
+  st = check_arrays(
+      fn, {{plan, z.plan, false, "plan", 4}, {slot, (size_t)d->batch * 4, false, "slot", 4},
+           {state_in == state ? nullptr : state_in, states, false, "state_in"},
+           {q, z.qk, false, "q"}, {k, z.qk, false, "k"}, {v, z.v, false, "v"},
+           {decay, z.gate, false, "decay", z.gate_align}, {beta, z.beta, false, "beta", 4},
+           {state, states, true, "state"}, {y, z.y, true, "y"},
+           {workspace, w.bytes, true, "workspace"}});
+  if (st != SSM_OK) return st;
+  ssm::ScanArgs a{};
+  a.plan = ssm::ScanPlan{plan, d->batch, total_tokens, ssm::scan_capacity(total_tokens, d->batch)};
+  a.heads = d->heads;
+  a.d_v = d->d_v;
+  a.num_slots = num_slots;
+  a.slot = slot;
+  a.state_in = state_in;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.decay = decay;
+  a.beta = beta;
+  a.state = state;
+  a.y = y;
+  a.w = w;
+  (void)hipGetLastError();
+  return launched(launch_scan(*d, a, false, stream), fn);
+}
+
+ssm_status ssm_scan_backward(const ssm_dims* d, int32_t total_tokens, const int32_t* plan,
+                             const float* state_in, const void* q, const void* k, const void* v,
+                             const float* decay, const float* beta, const float* dy,
+                             const float* dstate, void* dq, void* dk, void* dv,
+                             float* dlog_decay, float* dbeta, float* dstate_in, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+  static const char* fn = "ssm_scan_backward";
+  ssm_status st = check_scan(d, total_tokens, fn);
+  if (st != SSM_OK) return st;
+  if (d->batch == 0) return ok();
+  if ((st = check_packed(*d, total_tokens, plan, q, k, v, decay, beta, fn)) != SSM_OK) return st;
+  if (total_tokens > 0) {
+    if (dy == nullptr) return fail(SSM_E_NULL, "%s: dy is NULL", fn);
+    if (dq == nullptr) return fail(SSM_E_NULL, "%s: dq is NULL", fn);
+    if (dk == nullptr) return fail(SSM_E_NULL, "%s: dk is NULL", fn);
+    if (dv == nullptr) return fail(SSM_E_NULL, "%s: dv is NULL", fn);
+    if (dlog_decay == nullptr) return fail(SSM_E_NULL, "%s: dlog_decay is NULL", fn);
+    if ((st = check_beta(*d, dbeta, "dbeta", fn)) != SSM_OK) return st;
+  }
+  const ssm::ScanWork w = ssm::scan_work(*d, total_tokens, true, workspace);
+  if ((st = check_workspace(workspace, workspace_bytes, w.bytes, fn)) != SSM_OK) return st;
+  const PackedSizes z = packed_sizes(*d, total_tokens);
+  const size_t states = sizes_of(*d).state;
+  st = check_arrays(
+      fn, {{plan, z.plan, false, "plan", 4}, {state_in, states, false, "state_in"},
+           {q, z.qk, false, "q"}, {k, z.qk, false, "k"}, {v, z.v, false, "v"},
+           {decay, z.gate, false, "decay", z.gate_align}, {beta, z.beta, false, "beta", 4},
+           {dy, z.y, false, "dy"},
+           {dstate, states, false, "dstate"}, {dq, z.qk, true, "dq"}, {dk, z.qk, true, "dk"},
+           {dv, z.v, true, "dv"}, {dlog_decay, z.gate, true, "dlog_decay", z.gate_align},
+           {dbeta, z.beta, true, "dbeta", 4}, {dstate_in, states, true, "dstate_in"},
+           {workspace, w.bytes, true, "workspace"}});
+  if (st != SSM_OK) return st;
+  ssm::ScanArgs a{};
+  a.plan = ssm::ScanPlan{plan, d->batch, total_tokens, ssm::scan_capacity(total_tokens, d->batch)};
+  a.heads = d->heads;
+  a.d_v = d->d_v;
+  a.num_slots = d->batch;
+  a.state_in = state_in;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.decay = decay;
+  a.beta = beta;
+  a.dy = dy;
+  a.dstate = dstate;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dlog = dlog_decay;
+  a.dbeta = dbeta;
+  a.dstate_in = dstate_in;
+  a.w = w;
+  (void)hipGetLastError();
+  return launched(launch_scan(*d, a, true, stream), fn);
 }
 
 }  // extern "C"

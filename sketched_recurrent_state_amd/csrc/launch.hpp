@@ -165,6 +165,20 @@ hipError_t launch_recurrent_step(const ssm_dims& d, float* state, const void* q,
 hipError_t launch_fit_basis(const ssm_dims& d, const void* samples, int n_samples, float* basis,
                             hipStream_t stream);
 
+// Whole sequences (scan.hpp): the forward pass, or the backward pass with its own recomputation
+// of the states.
+struct ScanArgs;
+template <int RULE>
+hipError_t launch_scan_rule(const ssm_dims& d, const ScanArgs& a, bool backward,
+                            hipStream_t stream);
+
+// Index arrays from request lengths (plan.hip).
+hipError_t launch_scan_plan(const int32_t* lengths, int n_seqs, int total_tokens, int32_t* plan,
+                            hipStream_t stream);
+hipError_t launch_window_plan(const int32_t* lengths, int batch, int window, int32_t* tau,
+                              int32_t* parity, int32_t* update_rows, int32_t* n_update,
+                              hipStream_t stream);
+
 hipError_t launch_stream_probe(float* buf, long long n_tiles, int shape, hipStream_t stream);
 
 }  // namespace ssm

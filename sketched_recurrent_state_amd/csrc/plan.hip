@@ -1,0 +1,194 @@
+// plan.hip -- index arrays built on the device from request lengths: the chunk table of
+// a packed batch of sequences (for the scan kernels) and the window positions of a
+// serving step (for ssm_decode_step_varlen).
+//
+// Both are a few hundred kilobytes at most, so a launch costs more than the bytes. Each
+// is one launch: instead of passing prefix sums from workgroup to workgroup (which
+// would need a second launch or a wait), every workgroup sums what lies before its part
+// again.
+#include "common.hpp"
+#include "launch.hpp"
+#include "scan.hpp"
+
+namespace ssm {
+
+namespace {
+
+constexpr int PT = 1024;  // threads of a workgroup, and entries of the chunk table it fills
+constexpr int PW = PT / 64;
+
+// Exclusive sum over the workgroup's threads; `total` is the sum of all. sw: PW values.
+template <typename I>
+__device__ __forceinline__ I block_exclusive(I x, I* sw, I& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  I s = x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const I y = __shfl_up(s, o);
+    if (lane >= o) s += y;
+  }
+  __syncthreads();  // the last call's reads of sw are done
+  if (lane == 63) sw[wave] = s;
+  __syncthreads();
+  I before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < PW; ++w) {
+    const I y = sw[w];
+    if (w < wave) before += y;
+    total += y;
+  }
+  return before + s - x;
+}
+
+constexpr int PS = 4;            // sequences of a thread
+constexpr int TILE = PT * PS;    // sequences of a tile
+
+// Workgroup b fills the chunk table's entries [b * PT, (b + 1) * PT) and the starts of the
+// tiles b, b + gridDim.x, .. of the sequences. A thread holds PS consecutive sequences.
+__global__ void __launch_bounds__(PT)
+scan_plan_kernel(const int32_t* __restrict__ lengths, int n, int total, int cap,
+                 int32_t* __restrict__ plan) {
+  __shared__ int64_t sw64[PW];
+  __shared__ int32_t sw32[PW], owner[PT];
+  const int tid = threadIdx.x, e0 = blockIdx.x * PT;
+  int32_t* seq_start = plan;
+  int32_t* chunk_start = plan + n + 1;
+  int32_t* chunk_seq = plan + 2 * (n + 1);
+  owner[tid] = -1;
+  int64_t tokens = 0;  // of the tiles before
+  int chunks = 0;
+  for (int t0 = 0, tile = 0; t0 < n; t0 += TILE, ++tile) {
+    int64_t len[PS], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PS; ++i) {
+      const int s = t0 + tid * PS + i;
+      const int l = s < n ? lengths[s] : 0;
+      len[i] = l > 0 ? l : 0;
+      sum += len[i];
+    }
+    int64_t all;
+    int64_t at = tokens + block_exclusive(sum, sw64, all);
+    tokens += all;
+    // lengths past the arrays' end are cut
+    int start[PS], nc[PS], mine = 0;
+#pragma unroll
+    for (int i = 0; i < PS; ++i) {
+      const int64_t end = at + len[i];
+      start[i] = (int)(at < total ? at : total);
+      nc[i] = ((int)(end < total ? end : total) - start[i] + CT - 1) / CT;
+      mine += nc[i];
+      at = end;
+    }
+    int all_chunks;
+    int c = chunks + block_exclusive(mine, sw32, all_chunks);
+    chunks += all_chunks;
+    const bool writes = tile % (int)gridDim.x == (int)blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < PS; ++i) {
+      const int s = t0 + tid * PS + i;
+      if (s >= n) break;
+      if (writes) {
+        seq_start[s] = start[i];
+        chunk_start[s] = c;
+        if (s == n - 1) {
+          seq_start[n] = (int)(at < total ? at : total);
+          chunk_start[n] = c + nc[i];
+        }
+      }
+      // the sequence's first entry of this workgroup's part
+      const int first = c > e0 ? c : e0;
+      if (nc[i] > 0 && c + nc[i] > e0 && first < e0 + PT) owner[first - e0] = s;
+      c += nc[i];
+    }
+  }
+  __syncthreads();
+  // an entry belongs to the last sequence that starts at or before it
+  const int lane = tid & 63, wave = tid >> 6;
+  int s = owner[tid];
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(s, o);
+    if (lane >= o) s = max(s, y);
+  }
+  if (lane == 63) sw32[wave] = s;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) s = max(s, sw32[w]);
+  const int entry = e0 + tid;
+  if (entry < cap) chunk_seq[entry] = entry < chunks ? s : -1;
+}
+
+// L / W for L < 2^31 and W <= 16: magic = ceil(2^(31 + s) / W) with 2^s >= W exceeds the
+// quotient's multiple by less than W / 2^(31 + s) per unit of L, too little to reach the
+// next integer.
+struct WindowDiv {
+  uint32_t magic;
+  int shift, window;
+  __device__ __forceinline__ int div(int x) const {
+    return window == 1 ? x : (int)(__umulhi((uint32_t)x, magic) >> shift);
+  }
+};
+
+// Workgroup b plans rows [b * PT * PS, ..): the listed rows before them are counted from
+// the lengths again.
+__global__ void __launch_bounds__(PT)
+window_plan_kernel(const int32_t* __restrict__ lengths, int n, WindowDiv w,
+                   int32_t* __restrict__ tau, int32_t* __restrict__ parity,
+                   int32_t* __restrict__ rows, int32_t* __restrict__ count) {
+  __shared__ int sw[PW];
+  const int tid = threadIdx.x, r0 = blockIdx.x * TILE;
+  auto full = [&](int l) { return l >= 0 && l - w.div(l) * w.window == w.window - 1; };
+  int before = 0, total;
+#pragma unroll 8
+  for (int r = tid; r < r0; r += PT) before += full(lengths[r]);
+  block_exclusive(before, sw, total);
+  const int listed = total;
+  int l[PS], mine = 0;
+#pragma unroll
+  for (int i = 0; i < PS; ++i) {
+    const int r = r0 + tid * PS + i;
+    l[i] = r < n ? lengths[r] : -1;
+    mine += full(l[i]);
+  }
+  int at = listed + block_exclusive(mine, sw, total);
+  // the rows not listed fill the list's tail with -1: this part's have the places that
+  // follow when the list's places are counted from its end
+  int tail = n - 1 - (r0 + tid * PS - at);
+#pragma unroll
+  for (int i = 0; i < PS; ++i) {
+    const int r = r0 + tid * PS + i;
+    if (r >= n) break;
+    const int q = l[i] >= 0 ? w.div(l[i]) : 0;
+    tau[r] = l[i] >= 0 ? l[i] - q * w.window + 1 : 0;
+    parity[r] = q & 1;
+    if (full(l[i])) rows[at++] = r;
+    else rows[tail--] = -1;
+    if (r == n - 1) *count = at;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_scan_plan(const int32_t* lengths, int n, int total, int32_t* plan,
+                            hipStream_t stream) {
+  const int cap = scan_capacity(total, n);
+  hipLaunchKernelGGL(scan_plan_kernel, dim3((cap + PT - 1) / PT), dim3(PT), 0, stream, lengths, n,
+                     total, cap, plan);
+  return hipGetLastError();
+}
+
+hipError_t launch_window_plan(const int32_t* lengths, int n, int window, int32_t* tau,
+                              int32_t* parity, int32_t* rows, int32_t* count, hipStream_t stream) {
+  WindowDiv w{0, 0, window};
+  int s = 0;
+  while ((1 << s) < window) ++s;
+  if (window > 1) {
+    w.magic = (uint32_t)(((1ull << (31 + s)) + window - 1) / window);
+    w.shift = s - 1;
+  }
+  hipLaunchKernelGGL(window_plan_kernel, dim3((n + TILE - 1) / TILE), dim3(PT), 0, stream, lengths,
+                     n, w, tau, parity, rows, count);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

@@ -1,0 +1,199 @@
+// scan.hpp -- the layer's recurrence over whole sequences (prompt processing and
+// training): shared definitions of the scan kernels.
+//
+// Per (sequence, head), with D_t = a_t I (Mamba-2, GDN) or Diag(a_t) (KDA):
+//   S_t = D_t S_{t-1} + k_t w_t^T,   y_t = S_t^T q_t,
+//   w_t = v_t (Mamba-2)  or  b_t r_t,  r_t = v_t - (D_t S_{t-1})^T k_t (delta rules),
+// which is the update S <- M S + b k v^T of the decode entry points with the rank-one
+// part of M moved into the write.
+//
+// Sixteen tokens ("a block") at a time. With S the state before the block and, inside
+// it, I_i = a_1 .. a_i (decay into the block), O_j = a_{j+1} .. a_16 (decay out of it)
+// and G_ij = a_{j+1} .. a_i, all products of gates taken directly (no logarithms and no
+// quotients, so a gate of zero is exact):
+//   K_ij = k_i^T G_ij k_j  (j < i),     P_ij = q_i^T G_ij k_j  (j <= i)
+//   r = (I + K diag(b))^-1 (v - (I k) S),  w = b r
+//   y = (I q) S + P w,       S' = a_1..a_16 S + (O k)^T w
+// and backwards, with G = dL/dS after the block and e = dL/dw:
+//   e = (I + diag(b) K)^-T (P^T dy + (O k) G),  dr = b e = dv,  db_i = e_i . r_i
+//   G' = a_1..a_16 G + (I q)^T dy - (I k)^T dr
+//   dP = dy w^T, dK = -dr w^T (same triangles);
+//   dq_i = I_i S dy_i + sum_j dP_ij G_ij k_j
+//   dk_i = -I_i S dr_i + sum_j dK_ij G_ij k_j                       (its part as a reader)
+//        + O_i G w_i + sum_j G_ji (dP_ji q_j + dK_ji k_j)           (its part as a writer)
+//   d ln a_t = rowsum(S_end * G_end) + sum_{i >= t} (q_i dq_i + k_i dk_i^reader - k_i dk_i^writer),
+// the last summed over the channels when the gate is a scalar.
+//
+// Products run on the fp32 matrix cores (v_mfma_f32_16x16x4_f32): with C-layout tiles
+// (row 4g + i, column lane % 16, g = lane / 16) the i-th register of a tile is the
+// B operand of the i-th product of a 16-deep contraction whose slot g stands for row
+// 4g + i, so states and right-hand sides stay in registers from one product to the next.
+#pragma once
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace ssm {
+
+constexpr int SB = 16;          // tokens of a block
+constexpr int CT = 64;          // tokens of a chunk (an entry of the chunk table)
+constexpr int NB = CT / SB;     // blocks of a chunk
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+
+// fp32 -> the input type (bf16: to nearest, ties to even)
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(uint16_t* p, float x) { *p = (uint16_t)pack_bf16x2(x, x); }
+
+// Four consecutive elements, raw until unpacked.
+template <typename T>
+struct Quad;
+template <>
+struct Quad<float> {
+  float4 x;
+  __device__ __forceinline__ void load(const float* p) { x = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void zero() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float operator[](int i) const {
+    return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+  }
+};
+template <>
+struct Quad<uint16_t> {
+  uint2 x;
+  __device__ __forceinline__ void load(const uint16_t* p) { x = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void zero() { x = make_uint2(0u, 0u); }
+  __device__ __forceinline__ float operator[](int i) const {
+    const uint32_t w = i < 2 ? x.x : x.y;
+    return (i & 1) ? bf16_hi(w) : bf16_lo(w);
+  }
+};
+
+// The plan of ssm_scan_plan: [seq_start (n + 1) | chunk_start (n + 1) | chunk_seq (cap)].
+struct ScanPlan {
+  const int32_t* p;
+  int seqs, total, cap;
+  __device__ __forceinline__ int start(int s) const { return p[s]; }
+  __device__ __forceinline__ int chunk(int s) const { return p[seqs + 1 + s]; }
+  // Chunk c's first token and token count; false where c holds none. Whatever the
+  // table holds, the tokens named are inside [0, total).
+  __device__ __forceinline__ bool cell(int c, int& tok, int& count) const {
+    const int s = p[2 * (seqs + 1) + c];
+    if (s < 0 || s >= seqs) return false;
+    const long long k = (long long)c - chunk(s);
+    const long long b = start(s) + CT * k, e = start(s + 1);
+    if (k < 0 || b < 0 || b >= e || e > total || start(s) < 0) return false;
+    tok = (int)b;
+    count = (int)(e - b < CT ? e - b : CT);
+    return true;
+  }
+  // Sequence s's first token, length and first chunk; false where the table is not a plan's.
+  __device__ __forceinline__ bool sequence(int s, int& tok, int& len, int& first) const {
+    const int b = start(s), e = start(s + 1);
+    first = chunk(s);
+    if (b < 0 || e < b || e > total || first < 0) return false;
+    tok = b;
+    len = e - b;
+    return (long long)first + (len + CT - 1) / CT <= cap;
+  }
+};
+
+inline int scan_capacity(int total, int seqs) { return total / CT + seqs; }
+
+// Workspace: fp32 arrays with one part per cell (chunk, head), cell = chunk * heads + head.
+struct ScanWork {
+  float* P;      // [cells][NB][16][16]
+  float* A;      // [cells][NB][16][16]  (I + K diag(b))^-1           (delta rules)
+  float* A2;     // [cells][NB][16][16]  (I + diag(b) K)^-1           (backward, delta rules)
+  float* row;    // [cells][3][CT]       decay in, decay out (scalar gates), b
+  float* qh;     // [cells][CT][d_k]     I q                          (KDA)
+  float* kh;     // [cells][CT][d_k]     I k
+  float* kt;     // [cells][CT][d_k]     O k
+  float* all;    // [cells][NB][d_k]     a_1 .. a_16
+  float* r;      // [cells][CT][d_v]     r                            (backward, delta rules)
+  float* e;      // [cells][CT][d_v]     e
+  float* S;      // [cells][d_k][d_v]    state at the chunk's start   (backward)
+  float* G;      // [cells][d_k][d_v]    dL/dS at the chunk's end
+  size_t bytes;
+};
+
+inline ScanWork scan_work(const ssm_dims& d, int total, bool backward, void* base) {
+  const size_t cells = (size_t)scan_capacity(total, d.batch) * d.heads;
+  const bool delta = d.rule != SSM_MAMBA2, kda = d.rule == SSM_KDA;
+  ScanWork w{};
+  size_t at = 0;
+  auto take = [&](bool used, size_t per_cell) -> float* {
+    if (!used) return nullptr;
+    float* p = reinterpret_cast<float*>(static_cast<char*>(base) + at);
+    at += cells * per_cell * sizeof(float);  // every part is a multiple of 16 bytes
+    return p;
+  };
+  w.P = take(true, NB * SB * SB);
+  w.A = take(delta, NB * SB * SB);
+  w.A2 = take(delta && backward, NB * SB * SB);
+  w.row = take(true, 3 * CT);
+  w.qh = take(kda, (size_t)CT * d.d_k);
+  w.kh = take(kda, (size_t)CT * d.d_k);
+  w.kt = take(kda, (size_t)CT * d.d_k);
+  w.all = take(kda, (size_t)NB * d.d_k);
+  w.r = take(delta && backward, (size_t)CT * d.d_v);
+  w.e = take(delta && backward, (size_t)CT * d.d_v);
+  w.S = take(backward, (size_t)d.d_k * d.d_v);
+  w.G = take(backward, (size_t)d.d_k * d.d_v);
+  w.bytes = at;
+  return w;
+}
+
+struct ScanArgs {
+  ScanPlan plan;
+  int heads, d_v, num_slots;
+  const int32_t* slot;
+  const float* state_in;
+  const void *q, *k, *v;
+  const float *decay, *beta;
+  float* state;  // forward: final states
+  float* y;
+  const float *dy, *dstate;
+  void *dq, *dk, *dv;
+  float *dlog, *dbeta, *dstate_in;
+  ScanWork w;
+};
+
+// Products of the block's scalar gates for lane (m = lane % 16, g = lane / 16), whose own
+// gate is a: in = a_0..a_m, out = a_{m+1}..a_15, and ratio[i] = a_{m+1}..a_{4g+i} (row
+// 4g + i, column m; 1 on and above the diagonal).
+__device__ __forceinline__ void gate_products(float a, int m, int g, float& in, float& out,
+                                              float (&ratio)[4]) {
+  in = out = 1.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ratio[i] = 1.f;
+#pragma unroll
+  for (int l = 0; l < SB; ++l) {
+    const float al = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(a), l));
+    if (l <= m) in *= al;
+    if (l > m) {
+      out *= al;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (l <= 4 * g + i) ratio[i] *= al;
+    }
+  }
+}
+
+// Units to workgroups: the `parts` workgroups of a unit on one XCD (block b runs on XCD
+// b % 8), so that its keys and queries are fetched into one L2.
+__device__ __forceinline__ void unit_of(int b, int parts, int& unit, int& part) {
+  unit = (b & 7) + 8 * (b / (8 * parts));
+  part = (b >> 3) % parts;
+}
+inline unsigned unit_grid(long long units, int parts) {
+  return (unsigned)((units + 7) / 8 * 8 * parts);
+}
+
+}  // namespace ssm

@@ -1,0 +1,161 @@
+// scan_prep.hpp -- what a block of 16 tokens needs before the state is known: the
+// decayed products K and P, the inverse of the unit lower triangular I + K diag(b),
+// and the gate products (notation in scan.hpp). One wave per block, all blocks at once.
+#pragma once
+
+#include "scan.hpp"
+
+namespace ssm {
+
+template <int RULE, int DK, typename TIN, bool BWD>
+__global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
+  constexpr bool DELTA = RULE != MAMBA2, CH = RULE == KDA;
+  constexpr int T = DK / 16, LD = DK + 4, LK = 20;
+  __shared__ __align__(16) float sq[CH ? SB * LD : 1], sk[CH ? SB * LD : 1], sa[CH ? SB * LD : 1];
+  __shared__ __align__(16) float sl[DELTA ? 2 * SB * LK : 1];
+  const int cell = blockIdx.x / NB, blk = blockIdx.x % NB;
+  const int h = cell % a.heads, c = cell / a.heads;
+  int tok, count;
+  if (!a.plan.cell(c, tok, count) || SB * blk >= count) return;
+  tok += SB * blk;
+  count -= SB * blk;  // valid rows: min(count, 16)
+  const int lane = threadIdx.x, m = lane & 15, g = lane >> 4;
+  const bool valid = m < count;
+  const size_t at = (size_t)(tok + (valid ? m : 0)) * a.heads + h;  // lane's token row
+  const TIN* q = static_cast<const TIN*>(a.q);
+  const TIN* k = static_cast<const TIN*>(a.k);
+
+  float b = 0.f;
+  if constexpr (DELTA) b = valid ? a.beta[at] : 0.f;
+  f32x4 P = {0.f, 0.f, 0.f, 0.f}, K = P;
+  if constexpr (!CH) {
+    const float gate = valid ? a.decay[at] : 1.f;
+    float in, out, ratio[4];
+    gate_products(gate, m, g, in, out, ratio);
+    float* row = a.w.row + (size_t)cell * 3 * CT + SB * blk;
+    if (g == 0) {
+      row[m] = in;
+      row[CT + m] = out;
+      row[2 * CT + m] = b;
+    }
+    // q k^T and k k^T: slot g of product (t, i) is channel 16 t + 4 g + i
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      Quad<TIN> qa, ka;
+      qa.load(q + at * DK + 16 * t + 4 * g);
+      ka.load(k + at * DK + 16 * t + 4 * g);
+      if (!valid) {
+        qa.zero();
+        ka.zero();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        P = mfma4(qa[i], ka[i], P);
+        if constexpr (DELTA) K = mfma4(ka[i], ka[i], K);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      P[i] = m <= 4 * g + i ? P[i] * ratio[i] : 0.f;
+      K[i] = m < 4 * g + i ? K[i] * ratio[i] : 0.f;
+    }
+  } else {
+    // stage the block; lane (m, g) takes token m, channels 16 t + 4 g + i
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      Quad<TIN> qa, ka;
+      Quad<float> aa;
+      const size_t o = at * DK + 16 * t + 4 * g;
+      qa.load(q + o);
+      ka.load(k + o);
+      aa.load(a.decay + o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int s = m * LD + 16 * t + 4 * g + i;
+        sq[s] = valid ? qa[i] : 0.f;
+        sk[s] = valid ? ka[i] : 0.f;
+        sa[s] = valid ? aa[i] : 1.f;
+      }
+    }
+    if (g == 0) a.w.row[(size_t)cell * 3 * CT + 2 * CT + SB * blk + m] = b;
+    __syncthreads();
+    // I q, I k, O k and the whole block's decay, one channel at a time
+    const size_t o = ((size_t)cell * CT + SB * blk) * DK;
+    for (int ch = lane; ch < DK; ch += 64) {
+      float p = 1.f;
+#pragma unroll
+      for (int l = 0; l < SB; ++l) {
+        p *= sa[l * LD + ch];
+        a.w.qh[o + l * DK + ch] = p * sq[l * LD + ch];
+        a.w.kh[o + l * DK + ch] = p * sk[l * LD + ch];
+      }
+      a.w.all[((size_t)cell * NB + blk) * DK + ch] = p;
+      p = 1.f;
+#pragma unroll
+      for (int l = SB - 1; l >= 0; --l) {
+        a.w.kt[o + l * DK + ch] = p * sk[l * LD + ch];
+        p *= sa[l * LD + ch];
+      }
+    }
+    // column m of K and P, channels 16 t + 4 g + i of them: the key decays from row to row
+    float p[4 * T];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[4 * t + i] = sk[m * LD + 16 * t + 4 * g + i];
+#pragma unroll
+    for (int r = 0; r < SB; ++r) {
+      float sp = 0.f, sK = 0.f;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const float4 qr = *reinterpret_cast<const float4*>(sq + r * LD + 16 * t + 4 * g);
+        const float4 kr = *reinterpret_cast<const float4*>(sk + r * LD + 16 * t + 4 * g);
+        const float4 ar = *reinterpret_cast<const float4*>(sa + r * LD + 16 * t + 4 * g);
+        const float qq[4] = {qr.x, qr.y, qr.z, qr.w}, kk[4] = {kr.x, kr.y, kr.z, kr.w},
+                    aa[4] = {ar.x, ar.y, ar.z, ar.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float& x = p[4 * t + i];
+          x *= r > m ? aa[i] : 1.f;
+          sp += qq[i] * x;
+          sK += kk[i] * x;
+        }
+      }
+      sp = xsum32(xsum16(sp));
+      sK = xsum32(xsum16(sK));
+      if (r >> 2 == g) {  // lane (m, g) keeps rows 4 g + i
+        P[r & 3] = m <= r ? sp : 0.f;
+        K[r & 3] = m < r ? sK : 0.f;
+      }
+    }
+  }
+  const size_t o = ((size_t)cell * NB + blk) * (SB * SB);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a.w.P[o + (4 * g + i) * SB + m] = P[i];
+  if constexpr (DELTA) {
+    // (I + L)^-1 by forward substitution, column m: lanes of g = 0 take L = K diag(b), of
+    // g = 1 L = diag(b) K. In fp32 throughout: later rows inherit the earlier rows' errors.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sl[(4 * g + i) * LK + m] = K[i] * b;
+      sl[SB * LK + (4 * g + i) * LK + m] = K[i] * __shfl(b, 4 * g + i);
+    }
+    __syncthreads();
+    const float* L = sl + (g & 1) * SB * LK;
+    float x[SB];
+#pragma unroll
+    for (int r = 0; r < SB; ++r) {
+      float s = r == m ? 1.f : 0.f;
+#pragma unroll
+      for (int l = 0; l < r; ++l) s -= L[r * LK + l] * x[l];
+      x[r] = s;
+    }
+    if (g < (BWD ? 2 : 1)) {
+      float* X = (g == 0 ? a.w.A : a.w.A2) + o;
+#pragma unroll
+      for (int r = 0; r < SB; ++r) X[r * SB + m] = x[r];
+    }
+  }
+}
+
+}  // namespace ssm

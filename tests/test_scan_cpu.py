@@ -1,0 +1,173 @@
+"""Whole-sequence scan and serving plans without a GPU: argument checks, sizes, and the
+64-bit reference against differences."""
+import numpy as np
+import pytest
+
+import sketched_recurrent_state_amd as ssm
+from tests import scan_reference as ref
+
+A = 1 << 32  # a 16-byte aligned fake device address (never dereferenced)
+
+
+def dims(rule="gdn", in_dtype="bf16", batch=2, heads=3, d_k=32, d_v=64):
+    return ssm.Dims.make(rule, in_dtype, batch, heads, d_k, d_v, 4, 4)
+
+
+def addrs(n, gap=1 << 28):
+    return [A + i * gap for i in range(n)]
+
+
+def raw(name, *args):
+    import ctypes
+    lib = ssm.library()
+    args = [ctypes.byref(a) if isinstance(a, ssm.Dims) else a for a in args]
+    st = getattr(lib, name)(*args)
+    return st, lib.ssm_last_error().decode()
+
+
+def forward(d, total=100, **kw):
+    p = addrs(12)
+    a = dict(plan=p[0], num_slots=d.batch, slot=None, state_in=p[1], q=p[2], k=p[3], v=p[4],
+             decay=p[5], beta=p[6], state=p[7], y=p[8], workspace=p[9], nbytes=1 << 40)
+    a.update(kw)
+    return raw("ssm_scan_forward", d, total, a["plan"], a["num_slots"], a["slot"], a["state_in"],
+               a["q"], a["k"], a["v"], a["decay"], a["beta"], a["state"], a["y"], a["workspace"],
+               a["nbytes"], None)
+
+
+def backward(d, total=100, **kw):
+    p = addrs(18)
+    names = ["plan", "state_in", "q", "k", "v", "decay", "beta", "dy", "dstate", "dq", "dk", "dv",
+             "dlog_decay", "dbeta", "dstate_in", "workspace"]
+    a = dict(zip(names, p), nbytes=1 << 40)
+    a.update(kw)
+    return raw("ssm_scan_backward", d, total, *[a[n] for n in names], a["nbytes"], None)
+
+
+def test_forward_refusals():
+    d = dims()
+    for name in ("plan", "q", "k", "v", "decay", "beta", "state", "y", "workspace"):
+        st, msg = forward(d, **{name: None})
+        assert st == 1 and name in msg, (name, st, msg)
+    assert forward(dims(rule="mamba2"))[0] == 4  # Mamba-2 takes no beta
+    for name in ("q", "state", "y", "workspace", "state_in"):
+        st, msg = forward(d, **{name: A + (13 << 28) + 8})
+        assert st == 3 and name in msg
+    st, msg = forward(d, plan=A + 2)
+    assert st == 3 and "plan" in msg
+    st, msg = forward(d, y=A + (2 << 28))
+    assert st == 5
+    st, msg = forward(d, state=A + (1 << 28) + 64)  # partly over state_in
+    assert st == 5 and "state" in msg
+    need = ssm.scan_sizes(d, 100)[1]
+    st, msg = forward(d, nbytes=need - 1)
+    assert st == 4 and "workspace" in msg
+    st, msg = forward(d, nbytes=-1)
+    assert st == 4
+    st, msg = forward(d, total=-1)
+    assert st == 2 and "total_tokens" in msg
+    st, msg = forward(d, num_slots=0)
+    assert st == 2 and "num_slots" in msg
+    st, msg = forward(d, num_slots=1)
+    assert st == 2 and "slot map" in msg
+    st, msg = forward(dims(heads=1 << 12), total=1 << 17)
+    assert st == 2 and "heads" in msg
+    assert forward(dims(batch=0))[0] == 0
+    bad = dims()
+    bad.d_k = 48
+    assert forward(bad)[0] == 2
+
+
+def test_backward_refusals():
+    d = dims()
+    for name in ("plan", "q", "k", "v", "decay", "beta", "dy", "dq", "dk", "dv", "dlog_decay",
+                 "dbeta", "workspace"):
+        st, msg = backward(d, **{name: None})
+        assert st == 1 and name in msg, (name, st, msg)
+    m = dims(rule="mamba2")
+    assert backward(m)[0] == 4
+    st, msg = backward(m, beta=None)
+    assert st == 4 and "dbeta" in msg
+    st, msg = backward(d, dq=A + (3 << 28))  # over k
+    assert st == 5
+    st, msg = backward(d, dstate_in=A + (1 << 28))  # over state_in
+    assert st == 5 and "dstate_in" in msg
+    st, msg = backward(d, dlog_decay=A + (20 << 28) + 2)
+    assert st == 3 and "dlog_decay" in msg
+    st, msg = backward(dims(rule="kda"), dlog_decay=A + (20 << 28) + 4)
+    assert st == 3 and "dlog_decay" in msg
+    st, msg = backward(d, nbytes=ssm.scan_sizes(d, 100)[2] - 1)
+    assert st == 4 and "workspace" in msg
+    assert backward(dims(batch=0))[0] == 0
+
+
+def test_plan_refusals():
+    assert raw("ssm_scan_plan", A, -1, 10, A + 4096, None)[0] == 2
+    assert raw("ssm_scan_plan", A, 1 << 24, 10, A + 4096, None)[0] == 2
+    assert raw("ssm_scan_plan", A, 4, -1, A + 4096, None)[0] == 2
+    assert raw("ssm_scan_plan", None, 4, 10, A, None)[0] == 1
+    assert raw("ssm_scan_plan", A, 4, 10, None, None)[0] == 1
+    assert raw("ssm_scan_plan", A, 4, 10, A + 8, None)[0] == 5
+    assert raw("ssm_scan_plan", A + 2, 4, 10, A + 4096, None)[0] == 3
+    assert raw("ssm_scan_plan", None, 0, 10, None, None)[0] == 0
+    d = dims(batch=8)
+    p = addrs(5)
+    for i, name in enumerate(("lengths", "tau", "parity", "update_rows", "n_update")):
+        q = list(p)
+        q[i] = None
+        st, msg = raw("ssm_window_plan", d, *q, None)
+        assert st == 1 and name in msg
+    st, msg = raw("ssm_window_plan", d, p[0], p[1], p[1] + 16, p[3], p[4], None)
+    assert st == 5
+    st, msg = raw("ssm_window_plan", d, p[0] + 1, *p[1:], None)
+    assert st == 3
+    assert raw("ssm_window_plan", dims(batch=0), None, None, None, None, None, None)[0] == 0
+
+
+def test_sizes():
+    for rule in ("mamba2", "gdn", "kda"):
+        d = dims(rule=rule, batch=5)
+        ints, fwd, bwd = ssm.scan_sizes(d, 1000)
+        assert ints == 2 * 6 + 1000 // 64 + 5
+        assert 0 < fwd < bwd
+        assert ssm.scan_sizes(d, 0)[0] == 2 * 6 + 5
+    with pytest.raises(ssm.SSMError):
+        ssm.scan_sizes(dims(), -1)
+
+
+def test_binding_checks():
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ValueError, match="device tensor"):
+        ssm.scan_plan(torch.zeros(3, dtype=torch.int32), 10, torch.zeros(20, dtype=torch.int32))
+    with pytest.raises(ValueError, match="device tensor"):
+        ssm.window_plan(dims(), *[torch.zeros(2, dtype=torch.int32)] * 5)
+    with pytest.raises(ValueError):
+        p = addrs(10)
+        ssm.scan_forward(dims(), 100, *p[:6], p[6], p[7])  # raw addresses, no workspace
+
+
+@pytest.mark.parametrize("rule", ["mamba2", "gdn", "kda"])
+def test_reference_gradients_match_differences(rule):
+    rng = np.random.default_rng(3)
+    T, H, dk, dv = 7, 2, 4, 3
+    q, k, v = rng.standard_normal((T, H, dk)), rng.standard_normal((T, H, dk)) / 2, rng.standard_normal((T, H, dv))
+    gate = rng.uniform(0.3, 0.99, (T, H, dk) if rule == "kda" else (T, H))
+    beta = None if rule == "mamba2" else rng.uniform(0, 1, (T, H))
+    S0, dy, dS = rng.standard_normal((H, dk, dv)), rng.standard_normal((T, H, dv)), rng.standard_normal((H, dk, dv))
+    got, _ = ref.backward(q, k, v, gate, beta, S0, dy, dS)
+
+    def loss(q, k, v, lg, b, S):
+        y, last = ref.forward(q, k, v, np.exp(lg), b, S)
+        return (y * dy).sum() + (last * dS).sum()
+
+    args = [q, k, v, np.log(gate), beta, S0]
+    for i, name in enumerate(("dq", "dk", "dv", "dlog", "dbeta", "dS0")):
+        if args[i] is None:
+            continue
+        # central differences: error of order eps^2 of the third derivative, and 2^-53 / eps
+        d = rng.standard_normal(args[i].shape)
+        eps = 1e-5
+        hi = loss(*[a if j != i else a + eps * d for j, a in enumerate(args)])
+        lo = loss(*[a if j != i else a - eps * d for j, a in enumerate(args)])
+        want = (got[name] * d).sum()
+        assert abs((hi - lo) / (2 * eps) - want) <= 1e-7 * (np.abs(got[name] * d).sum() + 1)
