@@ -52,6 +52,14 @@ __device__ __forceinline__ float to_f32(uint16_t x) { return __uint_as_float((ui
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(uint16_t* p, float x) { *p = (uint16_t)pack_bf16x2(x, x); }
 
+// x where the row holds a token, else 0. A mask on the bits, not a select: a select lets the
+// compiler put every load of a partial block behind a branch of its own.
+__device__ __forceinline__ uint32_t row_mask(bool ok) { return ok ? 0xFFFFFFFFu : 0u; }
+__device__ __forceinline__ float masked(float x, uint32_t mask) {
+  return __uint_as_float(__float_as_uint(x) & mask);
+}
+__device__ __forceinline__ uint16_t masked(uint16_t x, uint32_t mask) { return (uint16_t)(x & mask); }
+
 // Four consecutive elements, raw until unpacked.
 template <typename T>
 struct Quad;
@@ -59,7 +67,9 @@ template <>
 struct Quad<float> {
   float4 x;
   __device__ __forceinline__ void load(const float* p) { x = *reinterpret_cast<const float4*>(p); }
-  __device__ __forceinline__ void zero() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void mask(uint32_t m) {
+    x = make_float4(masked(x.x, m), masked(x.y, m), masked(x.z, m), masked(x.w, m));
+  }
   __device__ __forceinline__ float operator[](int i) const {
     return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
   }
@@ -68,7 +78,7 @@ template <>
 struct Quad<uint16_t> {
   uint2 x;
   __device__ __forceinline__ void load(const uint16_t* p) { x = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ void zero() { x = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void mask(uint32_t m) { x = make_uint2(x.x & m, x.y & m); }
   __device__ __forceinline__ float operator[](int i) const {
     const uint32_t w = i < 2 ? x.x : x.y;
     return (i & 1) ? bf16_hi(w) : bf16_lo(w);

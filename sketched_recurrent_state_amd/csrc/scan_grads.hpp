@@ -57,13 +57,13 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
       Quad<float> y, r, e;
       Quad<TIN> x;
       y.load(a.dy + at * DV + 16 * t + 4 * g);
-      if (!valid) y.zero();
+      y.mask(row_mask(valid));
       if constexpr (DELTA) {
         r.load(a.w.r + wr + 16 * t);
         e.load(a.w.e + wr + 16 * t);
       } else {
         x.load(v + at * DV + 16 * t + 4 * g);
-        if (!valid) x.zero();
+        x.mask(row_mask(valid));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
 #pragma unroll
       for (int u = 0; u < TD; ++u) {
         if constexpr (!CH) {
-          z.q[u][i] = ok ? to_f32(q[at + 16 * u]) : 0.f;
-          z.k[u][i] = ok ? to_f32(k[at + 16 * u]) : 0.f;
+          z.q[u][i] = to_f32(masked(q[at + 16 * u], row_mask(ok)));
+          z.k[u][i] = to_f32(masked(k[at + 16 * u], row_mask(ok)));
           z.in[u][i] = row[SB * blk + 4 * g + i];
           z.out[u][i] = row[CT + SB * blk + 4 * g + i];
           z.all[u] = row[SB * blk + SB - 1];
@@ -136,9 +136,10 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
         for (int l = 0; l < SB; ++l) {
           const bool ok = l < left;
           const size_t at = (base + (size_t)(SB * blk + (ok ? l : 0)) * H) * DK + d0 + 16 * u;
-          z.qc[u][l] = ok ? to_f32(q[at]) : 0.f;
-          z.kc[u][l] = ok ? to_f32(k[at]) : 0.f;
-          z.ac[u][l] = ok ? a.decay[at] : 1.f;
+          z.qc[u][l] = to_f32(masked(q[at], row_mask(ok)));
+          z.kc[u][l] = to_f32(masked(k[at], row_mask(ok)));
+          const float gate = a.decay[at];
+          z.ac[u][l] = ok ? gate : 1.f;
         }
         float p = 1.f;
 #pragma unroll
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
     for (int t = 0; t < TV; ++t) {
       Quad<float> y, e;
       y.load(a.dy + at + 16 * t);
-      if (!valid) y.zero();
+      y.mask(row_mask(valid));
       if constexpr (DELTA) e.load(a.w.e + wr + 16 * t);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -239,8 +240,8 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
           wv[i] = a.w.r[((size_t)cell * CT + SB * blk + 4 * g + i) * DV + 16 * t + m];
         } else {
           const bool ok = 4 * g + i < left;
-          wv[i] = ok ? to_f32(v[(base + (size_t)(SB * blk + (ok ? 4 * g + i : 0)) * H) * DV + 16 * t + m])
-                     : 0.f;
+          wv[i] = to_f32(masked(v[(base + (size_t)(SB * blk + (ok ? 4 * g + i : 0)) * H) * DV + 16 * t + m],
+                                row_mask(ok)));
         }
       }
 #pragma unroll
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
         r.load(a.w.r + wr + 16 * t);
       } else {
         w.load(v + at + 16 * t);
-        if (!valid) w.zero();
+        w.mask(row_mask(valid));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -373,7 +374,8 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool ok = 4 * g + i < left;
-        yv[i] = ok ? a.dy[(base + (size_t)(SB * blk + (ok ? 4 * g + i : 0)) * H) * DV + 16 * t + m] : 0.f;
+        yv[i] = masked(a.dy[(base + (size_t)(SB * blk + (ok ? 4 * g + i : 0)) * H) * DV + 16 * t + m],
+                       row_mask(ok));
         if constexpr (DELTA) ev[i] = a.w.e[((size_t)cell * CT + SB * blk + 4 * g + i) * DV + 16 * t + m];
       }
 #pragma unroll

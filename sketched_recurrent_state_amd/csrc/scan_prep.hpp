@@ -21,6 +21,7 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
   count -= SB * blk;  // valid rows: min(count, 16)
   const int lane = threadIdx.x, m = lane & 15, g = lane >> 4;
   const bool valid = m < count;
+  const uint32_t rm = row_mask(valid);
   const size_t at = (size_t)(tok + (valid ? m : 0)) * a.heads + h;  // lane's token row
   const TIN* q = static_cast<const TIN*>(a.q);
   const TIN* k = static_cast<const TIN*>(a.k);
@@ -44,10 +45,8 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
       Quad<TIN> qa, ka;
       qa.load(q + at * DK + 16 * t + 4 * g);
       ka.load(k + at * DK + 16 * t + 4 * g);
-      if (!valid) {
-        qa.zero();
-        ka.zero();
-      }
+      qa.mask(rm);
+      ka.mask(rm);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         P = mfma4(qa[i], ka[i], P);
@@ -72,8 +71,8 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int s = m * LD + 16 * t + 4 * g + i;
-        sq[s] = valid ? qa[i] : 0.f;
-        sk[s] = valid ? ka[i] : 0.f;
+        sq[s] = masked(qa[i], rm);
+        sk[s] = masked(ka[i], rm);
         sa[s] = valid ? aa[i] : 1.f;
       }
     }

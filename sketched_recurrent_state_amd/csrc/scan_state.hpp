@@ -23,7 +23,8 @@ struct StateStep {
   using KT = KeyT<RULE, TIN>;
   Quad<KT> k[T], q[T];
   KT kt[T][4];
-  float v[4], A[4], P[4], in[4], out[4], b[4], all[RULE == KDA ? 4 * T : 1];
+  TIN v[4];
+  float A[4], P[4], in[4], out[4], b[4], all[RULE == KDA ? 4 * T : 1];
 
   __device__ __forceinline__ void load(const ScanArgs& a, size_t cell, int blk, int tok, int count,
                                        int h, int col, int m, int g) {
@@ -47,21 +48,15 @@ struct StateStep {
       const size_t at = ((size_t)(tok + (valid ? m : 0)) * H + h) * DK + 4 * g;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        if constexpr (DELTA) {
-          k[t].load(pk + at + 16 * t);
-          if (!valid) k[t].zero();
-        }
-        if constexpr (!BWD) {
-          q[t].load(pq + at + 16 * t);
-          if (!valid) q[t].zero();
-        }
+        if constexpr (DELTA) k[t].load(pk + at + 16 * t);
+        if constexpr (!BWD) q[t].load(pq + at + 16 * t);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool ok = 4 * g + i < count;
         const size_t r = ((size_t)(tok + (ok ? 4 * g + i : 0)) * H + h) * DK + m;
 #pragma unroll
-        for (int t = 0; t < T; ++t) kt[t][i] = ok ? pk[r + 16 * t] : KT(0);
+        for (int t = 0; t < T; ++t) kt[t][i] = pk[r + 16 * t];
       }
       const float* row = a.w.row + cell * 3 * CT + SB * blk + 4 * g;
       *reinterpret_cast<float4*>(in) = *reinterpret_cast<const float4*>(row);
@@ -72,7 +67,7 @@ struct StateStep {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool ok = 4 * g + i < count;
-      v[i] = ok ? to_f32(pv[((size_t)(tok + (ok ? 4 * g + i : 0)) * H + h) * a.d_v + col]) : 0.f;
+      v[i] = pv[((size_t)(tok + (ok ? 4 * g + i : 0)) * H + h) * a.d_v + col];
     }
     const size_t o = (cell * NB + blk) * (SB * SB) + m * SB + 4 * g;
     if constexpr (!BWD) *reinterpret_cast<float4*>(P) = *reinterpret_cast<const float4*>(a.w.P + o);
@@ -80,6 +75,27 @@ struct StateStep {
       *reinterpret_cast<float4*>(A) = *reinterpret_cast<const float4*>(a.w.A + o);
       *reinterpret_cast<float4*>(b) =
           *reinterpret_cast<const float4*>(a.w.row + cell * 3 * CT + 2 * CT + SB * blk + 4 * g);
+    }
+  }
+
+  // Zero for the rows behind the sequence's end. Applied when the block is used, not when it
+  // is loaded: a loaded value that is touched has been waited for.
+  __device__ __forceinline__ void clip(int count, int m, int g) {
+    if constexpr (RULE != KDA) {
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        if constexpr (RULE != MAMBA2) k[t].mask(row_mask(m < count));
+        if constexpr (!BWD) q[t].mask(row_mask(m < count));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t ok = row_mask(4 * g + i < count);
+      v[i] = masked(v[i], ok);
+      if constexpr (RULE != KDA) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) kt[t][i] = masked(kt[t][i], ok);
+      }
     }
   }
 };
@@ -113,8 +129,9 @@ __global__ void __launch_bounds__(64) scan_state_kernel(const ScanArgs a) {
   auto fetch = [&](Step& s, int j) {
     s.load(a, (size_t)(first + j / NB) * a.heads + h, j % NB, tok + SB * j, len - SB * j, h, col, m, g);
   };
-  auto run = [&](const Step& s, int j) {
+  auto run = [&](Step& s, int j) {
     const size_t cell = (size_t)(first + j / NB) * a.heads + h;
+    if (len - SB * j < SB) s.clip(len - SB * j, m, g);
     if constexpr (BWD) {
       if (j % NB == 0) {
         float* p = a.w.S + (cell * DK + 4 * g) * a.d_v + col;
@@ -135,7 +152,7 @@ __global__ void __launch_bounds__(64) scan_state_kernel(const ScanArgs a) {
     if constexpr (DELTA) {
       f32x4 r = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r = mfma4(s.A[i], s.v[i] - (CH ? ks[i] : s.in[i] * ks[i]), r);
+      for (int i = 0; i < 4; ++i) r = mfma4(s.A[i], to_f32(s.v[i]) - (CH ? ks[i] : s.in[i] * ks[i]), r);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (BWD) a.w.r[(cell * CT + SB * (j % NB) + 4 * g + i) * a.d_v + col] = r[i];
@@ -143,7 +160,7 @@ __global__ void __launch_bounds__(64) scan_state_kernel(const ScanArgs a) {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = s.v[i];
+      for (int i = 0; i < 4; ++i) w[i] = to_f32(s.v[i]);
     }
     if constexpr (!BWD) {
       if constexpr (!CH) {
@@ -217,18 +234,15 @@ struct GradientStep {
       const bool valid = m < count;
       const size_t at = ((size_t)(tok + (valid ? m : 0)) * H + h) * DK + 4 * g;
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        k[t].load(pk + at + 16 * t);
-        if (!valid) k[t].zero();
-      }
+      for (int t = 0; t < T; ++t) k[t].load(pk + at + 16 * t);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool ok = 4 * g + i < count;
         const size_t r = ((size_t)(tok + (ok ? 4 * g + i : 0)) * H + h) * DK + m;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-          qt[t][i] = ok ? pq[r + 16 * t] : KT(0);
-          if constexpr (DELTA) kt[t][i] = ok ? pk[r + 16 * t] : KT(0);
+          qt[t][i] = pq[r + 16 * t];
+          if constexpr (DELTA) kt[t][i] = pk[r + 16 * t];
         }
       }
       const float* row = a.w.row + cell * 3 * CT + SB * blk + 4 * g;
@@ -240,13 +254,32 @@ struct GradientStep {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool ok = 4 * g + i < count;
-      dy[i] = ok ? a.dy[((size_t)(tok + (ok ? 4 * g + i : 0)) * H + h) * a.d_v + col] : 0.f;
+      dy[i] = a.dy[((size_t)(tok + (ok ? 4 * g + i : 0)) * H + h) * a.d_v + col];
       P[i] = a.w.P[o + i * SB];  // column m: the transposed operand
       if constexpr (DELTA) A[i] = a.w.A2[o + i * SB];
     }
     if constexpr (DELTA)
       *reinterpret_cast<float4*>(b) =
           *reinterpret_cast<const float4*>(a.w.row + cell * 3 * CT + 2 * CT + SB * blk + 4 * g);
+  }
+
+  __device__ __forceinline__ void clip(int count, int m, int g) {
+    if constexpr (RULE != KDA) {
+#pragma unroll
+      for (int t = 0; t < T; ++t) k[t].mask(row_mask(m < count));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t ok = row_mask(4 * g + i < count);
+      dy[i] = masked(dy[i], ok);
+      if constexpr (RULE != KDA) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          qt[t][i] = masked(qt[t][i], ok);
+          if constexpr (RULE != MAMBA2) kt[t][i] = masked(kt[t][i], ok);
+        }
+      }
+    }
   }
 };
 
@@ -277,8 +310,9 @@ __global__ void __launch_bounds__(64) scan_gradient_kernel(const ScanArgs a) {
   auto fetch = [&](Step& s, int j) {
     s.load(a, (size_t)(first + j / NB) * a.heads + h, j % NB, tok + SB * j, len - SB * j, h, col, m, g);
   };
-  auto run = [&](const Step& s, int j) {
+  auto run = [&](Step& s, int j) {
     const size_t cell = (size_t)(first + j / NB) * a.heads + h;
+    if (len - SB * j < SB) s.clip(len - SB * j, m, g);
     if (j % NB == NB - 1 || j == blocks - 1) {
       float* p = a.w.G + (cell * DK + 4 * g) * a.d_v + col;
 #pragma unroll
