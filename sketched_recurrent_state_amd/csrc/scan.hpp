@@ -24,10 +24,12 @@
 //   d ln a_t = rowsum(S_end * G_end) + sum_{i >= t} (q_i dq_i + k_i dk_i^reader - k_i dk_i^writer),
 // the last summed over the channels when the gate is a scalar.
 //
-// Products run on the fp32 matrix cores (v_mfma_f32_16x16x4_f32): with C-layout tiles
-// (row 4g + i, column lane % 16, g = lane / 16) the i-th register of a tile is the
-// B operand of the i-th product of a 16-deep contraction whose slot g stands for row
-// 4g + i, so states and right-hand sides stay in registers from one product to the next.
+// Matrix-core layouts. A result tile holds row 4g + i (g = lane / 16) and column lane % 16
+// in its i-th register. In fp32 (v_mfma_f32_16x16x4_f32) that register is the B operand of
+// the i-th product of a 16-deep contraction whose slot g stands for row 4g + i; split in
+// bf16 (below) two tiles' registers, or one tile's in two parts, are the B operand of one
+// 32-deep product. So states and right-hand sides stay in registers from
+// one product to the next.
 #pragma once
 
 #include "common.hpp"
@@ -59,6 +61,9 @@ __device__ __forceinline__ float masked(float x, uint32_t mask) {
   return __uint_as_float(__float_as_uint(x) & mask);
 }
 __device__ __forceinline__ uint16_t masked(uint16_t x, uint32_t mask) { return (uint16_t)(x & mask); }
+__device__ __forceinline__ uint4 masked(uint4 x, uint32_t mask) {
+  return make_uint4(x.x & mask, x.y & mask, x.z & mask, x.w & mask);
+}
 
 // Four consecutive elements, raw until unpacked.
 template <typename T>
@@ -84,6 +89,76 @@ struct Quad<uint16_t> {
     return (i & 1) ? bf16_hi(w) : bf16_lo(w);
   }
 };
+
+// ---------------------------------------------------------------------------
+// fp32 products on the bf16 matrix cores
+// ---------------------------------------------------------------------------
+// x = h + m + l: three bf16 values of 8 bits each. A product with
+// an exact bf16 operand takes three matrix products, one with another split operand six
+// (hh, hm, mh, hl, lh, mm; the dropped ones are below 2^-24), with fp32 sums. bf16 products
+// run 16 times faster than fp32 ones, so three cost a fifth and six three eighths.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+struct Split4 {
+  uint2 h, m, l;  // four values each
+};
+
+// Each part is the leading 16 bits of what the parts before it leave (cut, not rounded), so
+// the three hold all 24 bits. (Rounded parts with the differences from v_dot2_f32_bf16 take 7
+// instructions a pair instead of 11, but ran slower: 1057 us against 1015 us for a GDN prompt
+// of 8192 tokens x 32 heads.)
+__device__ __forceinline__ float without_head(float x) {
+  return x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t heads(float a, float b) {  // their leading 16 bits, a's low
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ void split2(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) {
+  h = heads(a, b);
+  a = without_head(a);
+  b = without_head(b);
+  m = heads(a, b);
+  l = heads(without_head(a), without_head(b));
+}
+__device__ __forceinline__ Split4 split4(f32x4 x) {
+  Split4 s;
+  split2(x[0], x[1], s.h.x, s.m.x, s.l.x);
+  split2(x[2], x[3], s.h.y, s.m.y, s.l.y);
+  return s;
+}
+
+__device__ __forceinline__ f32x4 mfma32(uint4 a, uint4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+// Two 16-deep contractions in one 32-deep product: of its slots 8g + j, j < 4 take the
+// first pair's rows 4g + j and j >= 4 the second pair's.
+__device__ __forceinline__ f32x4 mfma_two(uint2 a0, uint2 b0, uint2 a1, uint2 b1, f32x4 c) {
+  return mfma32(make_uint4(a0.x, a0.y, a1.x, a1.y), make_uint4(b0.x, b0.y, b1.x, b1.y), c);
+}
+// c + a b, both split (16-deep)
+__device__ __forceinline__ f32x4 mfma_split(const Split4& a, const Split4& b, f32x4 c) {
+  c = mfma_two(a.l, b.h, a.h, b.l, c);
+  c = mfma_two(a.m, b.h, a.m, b.m, c);
+  return mfma_two(a.h, b.h, a.h, b.m, c);
+}
+// c + a b, a exact. The last part takes a 32-deep product with an empty half: a 16-deep one
+// (v_mfma_f32_16x16x16_bf16) right before a 32-deep one that adds to its result left rows 2 and
+// 3 of some tiles without it, from run to run, so chains of products keep to one instruction.
+__device__ __forceinline__ f32x4 mfma_exact(uint2 a, const Split4& b, f32x4 c) {
+  const uint2 none = make_uint2(0u, 0u);
+  c = mfma_two(a, b.l, none, none, c);
+  return mfma_two(a, b.h, a, b.m, c);
+}
+
+// Whether a scan runs on the bf16 matrix cores: keys and queries are exact bf16 operands
+// (KDA's, decayed channel by channel, and fp32 ones are not) and fill the 32-deep product.
+template <int RULE, int DK, typename TIN>
+constexpr bool kSplit = RULE != KDA && DK >= 32 && sizeof(TIN) == 2;
+inline bool uses_split(const ssm_dims& d) {
+  return d.rule != SSM_KDA && d.d_k >= 32 && d.in_dtype == SSM_IN_BF16;
+}
 
 // The plan of ssm_scan_plan: [seq_start (n + 1) | chunk_start (n + 1) | chunk_seq (cap)].
 struct ScanPlan {
@@ -118,9 +193,10 @@ inline int scan_capacity(int total, int seqs) { return total / CT + seqs; }
 
 // Workspace: fp32 arrays with one part per cell (chunk, head), cell = chunk * heads + head.
 struct ScanWork {
-  float* P;      // [cells][NB][16][16]
-  float* A;      // [cells][NB][16][16]  (I + K diag(b))^-1           (delta rules)
-  float* A2;     // [cells][NB][16][16]  (I + diag(b) K)^-1           (backward, delta rules)
+  // [cells][NB][16][16], or split: [cells][NB][3][64 lanes][4] bf16, the operand's layout
+  float* P;      // P                    (split backward: its transpose)
+  float* A;      // (I + K diag(b))^-1   (delta rules)
+  float* A2;     // (I + diag(b) K)^-1   (backward, delta rules; split: its transpose)
   float* row;    // [cells][3][CT]       decay in, decay out (scalar gates), b
   float* qh;     // [cells][CT][d_k]     I q                          (KDA)
   float* kh;     // [cells][CT][d_k]     I k
@@ -136,6 +212,7 @@ struct ScanWork {
 inline ScanWork scan_work(const ssm_dims& d, int total, bool backward, void* base) {
   const size_t cells = (size_t)scan_capacity(total, d.batch) * d.heads;
   const bool delta = d.rule != SSM_MAMBA2, kda = d.rule == SSM_KDA;
+  const size_t block = uses_split(d) ? 3 * 64 * 4 / 2 : SB * SB;
   ScanWork w{};
   size_t at = 0;
   auto take = [&](bool used, size_t per_cell) -> float* {
@@ -144,9 +221,9 @@ inline ScanWork scan_work(const ssm_dims& d, int total, bool backward, void* bas
     at += cells * per_cell * sizeof(float);  // every part is a multiple of 16 bytes
     return p;
   };
-  w.P = take(true, NB * SB * SB);
-  w.A = take(delta, NB * SB * SB);
-  w.A2 = take(delta && backward, NB * SB * SB);
+  w.P = take(true, NB * block);
+  w.A = take(delta, NB * block);
+  w.A2 = take(delta && backward, NB * block);
   w.row = take(true, 3 * CT);
   w.qh = take(kda, (size_t)CT * d.d_k);
   w.kh = take(kda, (size_t)CT * d.d_k);
@@ -158,6 +235,20 @@ inline ScanWork scan_work(const ssm_dims& d, int total, bool backward, void* bas
   w.G = take(backward, (size_t)d.d_k * d.d_v);
   w.bytes = at;
   return w;
+}
+
+// A split 16 x 16 operand in the workspace: three 512-byte runs of 8 bytes per lane.
+__device__ __forceinline__ void store_split(float* base, size_t block, int lane, const Split4& s) {
+  uint2* p = reinterpret_cast<uint2*>(base) + block * 192 + lane;
+  p[0] = s.h;
+  p[64] = s.m;
+  p[128] = s.l;
+}
+__device__ __forceinline__ void load_split(const float* base, size_t block, int lane, Split4& s) {
+  const uint2* p = reinterpret_cast<const uint2*>(base) + block * 192 + lane;
+  s.h = p[0];
+  s.m = p[64];
+  s.l = p[128];
 }
 
 struct ScanArgs {

@@ -3,6 +3,7 @@
 
 #include "scan_grads.hpp"
 #include "scan_prep.hpp"
+#include "scan_split.hpp"
 #include "scan_state.hpp"
 
 namespace ssm {
@@ -17,15 +18,27 @@ hipError_t launch_scan_rule(const ssm_dims& d, const ScanArgs& a, bool backward,
     if (!backward) {
       hipLaunchKernelGGL((scan_prep_kernel<RULE, kDK, TIN, false>), dim3(cells * NB), dim3(64), 0,
                          stream, a);
-      hipLaunchKernelGGL((scan_state_kernel<RULE, kDK, TIN, false>), dim3(units), dim3(64), 0,
-                         stream, a);
+      if constexpr (kSplit<RULE, kDK, TIN>)
+        hipLaunchKernelGGL((scan_split_state_kernel<RULE, kDK, false>), dim3(units), dim3(64), 0,
+                           stream, a);
+      else
+        hipLaunchKernelGGL((scan_state_kernel<RULE, kDK, TIN, false>), dim3(units), dim3(64), 0,
+                           stream, a);
       return hipGetLastError();
     }
     hipLaunchKernelGGL((scan_prep_kernel<RULE, kDK, TIN, true>), dim3(cells * NB), dim3(64), 0,
                        stream, a);
-    hipLaunchKernelGGL((scan_state_kernel<RULE, kDK, TIN, true>), dim3(units), dim3(64), 0, stream,
-                       a);
-    hipLaunchKernelGGL((scan_gradient_kernel<RULE, kDK, TIN>), dim3(units), dim3(64), 0, stream, a);
+    if constexpr (kSplit<RULE, kDK, TIN>) {
+      hipLaunchKernelGGL((scan_split_state_kernel<RULE, kDK, true>), dim3(units), dim3(64), 0,
+                         stream, a);
+      hipLaunchKernelGGL((scan_split_gradient_kernel<RULE, kDK>), dim3(units), dim3(64), 0, stream,
+                         a);
+    } else {
+      hipLaunchKernelGGL((scan_state_kernel<RULE, kDK, TIN, true>), dim3(units), dim3(64), 0,
+                         stream, a);
+      hipLaunchKernelGGL((scan_gradient_kernel<RULE, kDK, TIN>), dim3(units), dim3(64), 0, stream,
+                         a);
+    }
     hipLaunchKernelGGL((scan_grads_kernel<RULE, kDK, kDV, TIN>), dim3(cells),
                        dim3(kDK >= 32 ? 2 * kDK : 64), 0, stream, a);
     return hipGetLastError();
