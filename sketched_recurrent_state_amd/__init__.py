@@ -543,13 +543,20 @@ def sketch_decode_step_ls(d: Dims, sketch_q, read_map, q, k_buf, v_buf, decay_bu
 def _on_device(args, stream, call) -> None:
     """call(stream address) on the device that the tensors among args share: their device
     becomes the current one for the call, and its current stream is the default."""
-    devs = {a.device for a in args if a is not None and not isinstance(a, int)}
-    if len(devs) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-    if not devs or not next(iter(devs)).type == "cuda":
-        return call(_stream(stream))  # raw addresses (a CPU tensor was refused before)
+    dev = None
+    for a in args:
+        if a is None or isinstance(a, int):
+            continue
+        if dev is None:
+            dev = a.device
+        elif a.device != dev:
+            raise ValueError(f"tensors on different devices: {dev}, {a.device}")
+    if dev is None:
+        return call(_stream(stream))  # raw addresses
     import torch
-    with torch.cuda.device(devs.pop()):
+    if dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
         call(_stream(stream))
 
 

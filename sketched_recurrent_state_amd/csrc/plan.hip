@@ -118,14 +118,21 @@ scan_plan_kernel(const int32_t* __restrict__ lengths, int n, int total, int cap,
   if (entry < cap) chunk_seq[entry] = entry < chunks ? s : -1;
 }
 
-// L / W for L < 2^31 and W <= 16: magic = ceil(2^(31 + s) / W) with 2^s >= W exceeds the
-// quotient's multiple by less than W / 2^(31 + s) per unit of L, too little to reach the
-// next integer.
+// L / W and "L is the last of its window" for any int32 L and W <= 16.
+// Quotient of L >= 0: magic = ceil(2^(31 + s) / W) with 2^s >= W exceeds the quotient's multiple
+// by less than W / 2^(31 + s) per unit of L, too little to reach the next integer.
+// Last (W divides x = L + 1): with W = 2^k odd, x times the inverse of the odd part modulo 2^32,
+// rotated right by k, is x / W for the multiples of W and at least 2^32 / W for the others. The
+// window's last L >= 0 are those with 1 <= x / W <= 2^31 / W. Half the instructions of a quotient.
 struct WindowDiv {
-  uint32_t magic;
-  int shift, window;
+  uint32_t magic, inverse, limit;
+  int shift, rotate, window;
   __device__ __forceinline__ int div(int x) const {
     return window == 1 ? x : (int)(__umulhi((uint32_t)x, magic) >> shift);
+  }
+  __device__ __forceinline__ bool last(int l) const {
+    const uint32_t x = ((uint32_t)l + 1u) * inverse;
+    return __builtin_amdgcn_alignbit(x, x, rotate) - 1u < limit;
   }
 };
 
@@ -137,10 +144,9 @@ window_plan_kernel(const int32_t* __restrict__ lengths, int n, WindowDiv w,
                    int32_t* __restrict__ rows, int32_t* __restrict__ count) {
   __shared__ int sw[PW];
   const int tid = threadIdx.x, r0 = blockIdx.x * TILE;
-  auto full = [&](int l) { return l >= 0 && l - w.div(l) * w.window == w.window - 1; };
   int before = 0, total;
 #pragma unroll 8
-  for (int r = tid; r < r0; r += PT) before += full(lengths[r]);
+  for (int r = tid; r < r0; r += PT) before += w.last(lengths[r]);
   block_exclusive(before, sw, total);
   const int listed = total;
   int l[PS], mine = 0;
@@ -148,7 +154,7 @@ window_plan_kernel(const int32_t* __restrict__ lengths, int n, WindowDiv w,
   for (int i = 0; i < PS; ++i) {
     const int r = r0 + tid * PS + i;
     l[i] = r < n ? lengths[r] : -1;
-    mine += full(l[i]);
+    mine += w.last(l[i]);
   }
   int at = listed + block_exclusive(mine, sw, total);
   // the rows not listed fill the list's tail with -1: this part's have the places that
@@ -161,7 +167,7 @@ window_plan_kernel(const int32_t* __restrict__ lengths, int n, WindowDiv w,
     const int q = l[i] >= 0 ? w.div(l[i]) : 0;
     tau[r] = l[i] >= 0 ? l[i] - q * w.window + 1 : 0;
     parity[r] = q & 1;
-    if (full(l[i])) rows[at++] = r;
+    if (w.last(l[i])) rows[at++] = r;
     else rows[tail--] = -1;
     if (r == n - 1) *count = at;
   }
@@ -179,7 +185,13 @@ hipError_t launch_scan_plan(const int32_t* lengths, int n, int total, int32_t* p
 
 hipError_t launch_window_plan(const int32_t* lengths, int n, int window, int32_t* tau,
                               int32_t* parity, int32_t* rows, int32_t* count, hipStream_t stream) {
-  WindowDiv w{0, 0, window};
+  WindowDiv w{};
+  w.window = window;
+  uint32_t odd = (uint32_t)window;
+  for (; !(odd & 1); odd >>= 1) ++w.rotate;
+  w.inverse = 1;
+  for (int i = 0; i < 5; ++i) w.inverse *= 2 - odd * w.inverse;  // Newton: correct bits double
+  w.limit = (1u << 31) / (uint32_t)window;
   int s = 0;
   while ((1 << s) < window) ++s;
   if (window > 1) {

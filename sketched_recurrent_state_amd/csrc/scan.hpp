@@ -152,13 +152,10 @@ __device__ __forceinline__ f32x4 mfma_exact(uint2 a, const Split4& b, f32x4 c) {
   return mfma_two(a, b.h, a, b.m, c);
 }
 
-// Whether a scan runs on the bf16 matrix cores: keys and queries are exact bf16 operands
-// (KDA's, decayed channel by channel, and fp32 ones are not) and fill the 32-deep product.
-template <int RULE, int DK, typename TIN>
-constexpr bool kSplit = RULE != KDA && DK >= 32 && sizeof(TIN) == 2;
-inline bool uses_split(const ssm_dims& d) {
-  return d.rule != SSM_KDA && d.d_k >= 32 && d.in_dtype == SSM_IN_BF16;
-}
+// Whether the keys and queries are exact bf16 operands: KDA's, decayed channel by channel, and
+// fp32 ones are split.
+template <int RULE, typename TIN>
+constexpr bool kExact = RULE != KDA && sizeof(TIN) == 2;
 
 // The plan of ssm_scan_plan: [seq_start (n + 1) | chunk_start (n + 1) | chunk_seq (cap)].
 struct ScanPlan {
@@ -193,10 +190,10 @@ inline int scan_capacity(int total, int seqs) { return total / CT + seqs; }
 
 // Workspace: fp32 arrays with one part per cell (chunk, head), cell = chunk * heads + head.
 struct ScanWork {
-  // [cells][NB][16][16], or split: [cells][NB][3][64 lanes][4] bf16, the operand's layout
-  float* P;      // P                    (split backward: its transpose)
-  float* A;      // (I + K diag(b))^-1   (delta rules)
-  float* A2;     // (I + diag(b) K)^-1   (backward, delta rules; split: its transpose)
+  // A operands in three bf16 parts, [cells][NB][3][64 lanes][4]:
+  float* P;      // P                              (backward: its transpose)
+  float* A;      // (I + K diag(b))^-1             (delta rules)
+  float* A2;     // the transpose of (I + diag(b) K)^-1  (backward, delta rules)
   float* row;    // [cells][3][CT]       decay in, decay out (scalar gates), b
   float* qh;     // [cells][CT][d_k]     I q                          (KDA)
   float* kh;     // [cells][CT][d_k]     I k
@@ -212,7 +209,7 @@ struct ScanWork {
 inline ScanWork scan_work(const ssm_dims& d, int total, bool backward, void* base) {
   const size_t cells = (size_t)scan_capacity(total, d.batch) * d.heads;
   const bool delta = d.rule != SSM_MAMBA2, kda = d.rule == SSM_KDA;
-  const size_t block = uses_split(d) ? 3 * 64 * 4 / 2 : SB * SB;
+  const size_t block = 3 * 64 * 4 / 2;
   ScanWork w{};
   size_t at = 0;
   auto take = [&](bool used, size_t per_cell) -> float* {
@@ -244,13 +241,6 @@ __device__ __forceinline__ void store_split(float* base, size_t block, int lane,
   p[64] = s.m;
   p[128] = s.l;
 }
-__device__ __forceinline__ void load_split(const float* base, size_t block, int lane, Split4& s) {
-  const uint2* p = reinterpret_cast<const uint2*>(base) + block * 192 + lane;
-  s.h = p[0];
-  s.m = p[64];
-  s.l = p[128];
-}
-
 struct ScanArgs {
   ScanPlan plan;
   int heads, d_v, num_slots;

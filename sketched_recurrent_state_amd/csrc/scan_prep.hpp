@@ -10,10 +10,10 @@ namespace ssm {
 template <int RULE, int DK, typename TIN, bool BWD>
 __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
   constexpr bool DELTA = RULE != MAMBA2, CH = RULE == KDA;
-  constexpr bool SPLIT = kSplit<RULE, DK, TIN>;
+  constexpr bool EXACT = kExact<RULE, TIN> && DK >= 32;
   constexpr int T = DK / 16, LD = DK + 4, LK = 20;
   __shared__ __align__(16) float sq[CH ? SB * LD : 1], sk[CH ? SB * LD : 1], sa[CH ? SB * LD : 1];
-  __shared__ __align__(16) float sl[DELTA || SPLIT ? 2 * SB * LK : 1];
+  __shared__ __align__(16) float sl[2 * SB * LK];
   const int cell = blockIdx.x / NB, blk = blockIdx.x % NB;
   const int h = cell % a.heads, c = cell / a.heads;
   int tok, count;
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
       row[CT + m] = out;
       row[2 * CT + m] = b;
     }
-    if constexpr (SPLIT) {  // exact operands
+    if constexpr (EXACT) {
 #pragma unroll
       for (int t = 0; t < T / 2; ++t) {
         uint4 qa = *reinterpret_cast<const uint4*>(q + at * DK + 32 * t + 8 * g);
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
     }
     // q k^T and k k^T: slot g of product (t, i) is channel 16 t + 4 g + i
 #pragma unroll
-    for (int t = 0; t < (SPLIT ? 0 : T); ++t) {
+    for (int t = 0; t < (EXACT ? 0 : T); ++t) {
       Quad<TIN> qa, ka;
       qa.load(q + at * DK + 16 * t + 4 * g);
       ka.load(k + at * DK + 16 * t + 4 * g);
@@ -140,11 +140,8 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
       }
     }
   }
-  const size_t block = (size_t)cell * NB + blk, o = block * (SB * SB);
-  if constexpr (!SPLIT) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a.w.P[o + (4 * g + i) * SB + m] = P[i];
-  } else if constexpr (BWD) {  // lane (m, g) holds the transpose's row m, columns 4g + i
+  const size_t block = (size_t)cell * NB + blk;
+  if constexpr (BWD) {  // lane (m, g) holds the transpose's row m, columns 4g + i
     store_split(a.w.P, block, lane, split4(P));
   } else {
 #pragma unroll
@@ -171,26 +168,18 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
       for (int l = 0; l < r; ++l) s -= L[r * LK + l] * x[l];
       x[r] = s;
     }
-    if constexpr (!SPLIT) {
-      if (g < (BWD ? 2 : 1)) {
-        float* X = (g == 0 ? a.w.A : a.w.A2) + o;
+    __syncthreads();  // L has been read
+    if (g < 2) {
 #pragma unroll
-        for (int r = 0; r < SB; ++r) X[r * SB + m] = x[r];
-      }
-    } else {
-      __syncthreads();  // L has been read
-      if (g < 2) {
+      for (int r = 0; r < SB; ++r) sl[g * SB * LK + r * LK + m] = x[r];
+    }
+    __syncthreads();
+    store_split(a.w.A, block, lane, split4(*reinterpret_cast<const f32x4*>(sl + m * LK + 4 * g)));
+    if constexpr (BWD) {
+      f32x4 t;
 #pragma unroll
-        for (int r = 0; r < SB; ++r) sl[g * SB * LK + r * LK + m] = x[r];
-      }
-      __syncthreads();
-      store_split(a.w.A, block, lane, split4(*reinterpret_cast<const f32x4*>(sl + m * LK + 4 * g)));
-      if constexpr (BWD) {
-        f32x4 t;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = sl[SB * LK + (4 * g + i) * LK + m];
-        store_split(a.w.A2, block, lane, split4(t));
-      }
+      for (int i = 0; i < 4; ++i) t[i] = sl[SB * LK + (4 * g + i) * LK + m];
+      store_split(a.w.A2, block, lane, split4(t));
     }
   }
 }

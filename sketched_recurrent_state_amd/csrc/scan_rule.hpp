@@ -3,24 +3,20 @@
 
 #include "scan_grads.hpp"
 #include "scan_prep.hpp"
-#include "scan_split.hpp"
 #include "scan_state.hpp"
 
 namespace ssm {
 
-// Waves of a workgroup and waves per column block (NW, DS) of the split passes. One wave per
-// column block does least work; where that leaves most of the 1,024 SIMDs without a wave, the
-// block's rows are divided.
-template <int RULE, int DK, typename F>
+// Calls f(waves of a workgroup, narrow): wide workgroups do least work; where they leave most
+// of the 1,024 SIMDs without a wave, the rows of a column block are divided over d_k / 32 waves.
+template <int DK, int DV, typename F>
 void split_shape(const ssm_dims& d, F&& f) {
   using std::integral_constant;
-  const long long waves = (long long)d.batch * d.heads * (d.d_v / 16);
-  if constexpr (DK >= 128) {
-    if (waves <= 512) return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
-  }
-  if (d.d_v >= 64) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
-  if (d.d_v == 32) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
-  return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  const long long waves = (long long)d.batch * d.heads * (DV / 16);
+  if (waves <= 512)
+    f(integral_constant<int, kPadded<DK> / 32>{}, std::true_type{});
+  else
+    f(integral_constant<int, (DV >= 64 ? 4 : DV / 16)>{}, std::false_type{});
 }
 
 template <int RULE>
@@ -35,16 +31,13 @@ hipError_t launch_scan_rule(const ssm_dims& d, const ScanArgs& a, bool backward,
                          dim3(64), 0, stream, a);
     };
     auto state = [&](auto B) {
-      if constexpr (kSplit<RULE, kDK, TIN>) {
-        split_shape<RULE, kDK>(d, [&](auto NW, auto DS) {
-          constexpr int nw = decltype(NW)::value, ds = decltype(DS)::value;
-          hipLaunchKernelGGL((scan_split_state_kernel<RULE, kDK, nw, ds, decltype(B)::value>),
-                             dim3(unit_grid(units, kDV * ds / (16 * nw))), dim3(64 * nw), 0, stream, a);
-        });
-      } else {
-        hipLaunchKernelGGL((scan_state_kernel<RULE, kDK, TIN, decltype(B)::value>),
-                           dim3(unit_grid(units, kDV / 16)), dim3(64), 0, stream, a);
-      }
+      split_shape<kDK, kDV>(d, [&](auto NW, auto NARROW) {
+        constexpr int nw = decltype(NW)::value;
+        constexpr bool narrow = decltype(NARROW)::value, bwd = decltype(B)::value;
+        hipLaunchKernelGGL((scan_state_kernel<RULE, kDK, TIN, nw, narrow, bwd>),
+                           dim3(unit_grid(units, kDV / 16 / (narrow ? 1 : nw))),
+                           dim3(64 * (nw + (narrow && !bwd))), 0, stream, a);
+      });
     };
     if (!backward) {
       prep(std::false_type{});
@@ -53,16 +46,13 @@ hipError_t launch_scan_rule(const ssm_dims& d, const ScanArgs& a, bool backward,
     }
     prep(std::true_type{});
     state(std::true_type{});
-    if constexpr (kSplit<RULE, kDK, TIN>) {
-      split_shape<RULE, kDK>(d, [&](auto NW, auto DS) {
-        constexpr int nw = decltype(NW)::value, ds = decltype(DS)::value;
-        hipLaunchKernelGGL((scan_split_gradient_kernel<RULE, kDK, nw, ds>),
-                           dim3(unit_grid(units, kDV * ds / (16 * nw))), dim3(64 * nw), 0, stream, a);
-      });
-    } else {
-      hipLaunchKernelGGL((scan_gradient_kernel<RULE, kDK, TIN>), dim3(unit_grid(units, kDV / 16)),
-                         dim3(64), 0, stream, a);
-    }
+    split_shape<kDK, kDV>(d, [&](auto NW, auto NARROW) {
+      constexpr int nw = decltype(NW)::value;
+      constexpr bool narrow = decltype(NARROW)::value;
+      hipLaunchKernelGGL((scan_gradient_kernel<RULE, kDK, TIN, nw, narrow>),
+                         dim3(unit_grid(units, kDV / 16 / (narrow ? 1 : nw))), dim3(64 * nw), 0,
+                         stream, a);
+    });
     hipLaunchKernelGGL((scan_grads_kernel<RULE, kDK, kDV, TIN>), dim3(cells),
                        dim3(kDK >= 32 ? 2 * kDK : 64), 0, stream, a);
     return hipGetLastError();
