@@ -1,20 +1,29 @@
-// scan_grads.hpp -- the gradients of q, k, the gates and beta of one chunk (64 tokens)
-// of one head, all chunks at once, from the state at the chunk's start, its gradient at
-// the chunk's end, and every token's r and e (notation in scan.hpp).
+// scan_grads.hpp -- the gradients of q, k, the gates and beta of one chunk (64 tokens) of
+// one head, all chunks at once, from the state S at the chunk's start, its gradient G at the
+// chunk's end, and every token's r and e (notation in scan.hpp).
 //
-// A wave owns 32 key channels and holds the transposed state (rows v, columns d), so a
-// product against it contracts the whole d_v in the wave's own registers and no sums
-// cross waves. The state is carried forwards over the chunk's four blocks (its writes w
-// are known), then the state's gradient backwards, which costs four blocks' updates
-// instead of four times the states in memory.
+// The blocks of a chunk meet through decays across whole blocks: with F_a the decay of the
+// blocks before block a and B_b that of the blocks after block b,
+//   dq_a        = F_a I_a (dy_a S) + sum_{b <= a} (dP_ab G_ab) k_b
+//   dk_a reader = -F_a I_a (dr_a S) + sum_{b <= a} (dK_ab G_ab) k_b
+//   dk_b writer = B_b O_b (w_b G) + sum_{a >= b} (dP_ab G_ab)^T q_a + (dK_ab G_ab)^T k_a
+// so S and G are read and split once a chunk and never carried from block to block. A scalar
+// gate's G_ab goes into dP and dK; KDA's, one for each channel, is applied to the keys (within
+// a block), to the sums (across blocks) and term by term (on the diagonal). And
+//   rowsum(S_end * G) = F rowsum(S * G) + sum_j k_j (state part of the writer's dk_j)
+// starts the sums of the gates' gradients without the state at the chunk's end.
+//
+// A wave owns 32 key channels (16 with d_k = 16), so the contractions over d_v stay in its
+// registers; dy, e and r pass through LDS 32 values of d_v at a time, split there once for all
+// waves. The 20 tiles of dP and dK are dealt over the waves.
 #pragma once
 
 #include "scan.hpp"
 
 namespace ssm {
 
-// Sum over the four lanes that differ in bits 4 and 5 of the values of lanes above this
-// one, and over all four.
+// The value of x summed over the lanes above this one of the four that differ in bits 4 and 5,
+// and over all four.
 __device__ __forceinline__ void above(float x, int lane, int g, float& after, float& total) {
   after = total = 0.f;
 #pragma unroll
@@ -25,16 +34,48 @@ __device__ __forceinline__ void above(float x, int lane, int g, float& after, fl
   }
 }
 
+struct Split8 {  // eight values, the operand of a 32-deep product
+  uint4 h, m, l;
+};
+__device__ __forceinline__ Split8 split8(f32x4 x, f32x4 y) {
+  const Split4 a = split4(x), b = split4(y);
+  return Split8{make_uint4(a.h.x, a.h.y, b.h.x, b.h.y), make_uint4(a.m.x, a.m.y, b.m.x, b.m.y),
+                make_uint4(a.l.x, a.l.y, b.l.x, b.l.y)};
+}
+// c + a b, of which a has PA parts and b PB (1: exact values)
+template <int PA, int PB>
+__device__ __forceinline__ f32x4 mfma_parts(const Split8& a, const Split8& b, f32x4 c) {
+  if constexpr (PA == 3) c = mfma32(a.l, b.h, c);
+  if constexpr (PB == 3) c = mfma32(a.h, b.l, c);
+  if constexpr (PA == 3 && PB == 3) c = mfma32(a.m, b.m, c);
+  if constexpr (PA == 3) c = mfma32(a.m, b.h, c);
+  if constexpr (PB == 3) c = mfma32(a.h, b.m, c);
+  return mfma32(a.h, b.h, c);
+}
+
 template <int RULE, int DK, int DV, typename TIN>
 __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(const ScanArgs a) {
-  constexpr bool DELTA = RULE != MAMBA2, CH = RULE == KDA;
-  constexpr int TD = DK >= 32 ? 2 : 1, W = DK >= 32 ? DK / 32 : 1, TV = DV / 16, LP = 20;
-  __shared__ __align__(16) float sp[NB][SB * LP], sk[NB][SB * LP], sx[W][CT];
-  __shared__ float send[W];
+  constexpr bool DELTA = RULE != MAMBA2, CH = RULE == KDA, BF = sizeof(TIN) == 2;
+  constexpr bool EXACT = BF && !CH;                  // keys and queries
+  constexpr int RP = !DELTA && BF ? 1 : 3;           // parts of w / r (Mamba-2: the values)
+  constexpr int TD = DK >= 32 ? 2 : 1, W = DK >= 32 ? DK / 32 : 1, NT = 64 * W;
+  constexpr int NS = DV >= 32 ? DV / 32 : 1;         // steps of 32 values of d_v
+  constexpr int PAIRS = NB * (NB + 1) / 2, TILES = DELTA ? 2 * PAIRS : PAIRS;
+  constexpr int TW = (TILES + W - 1) / W;            // dP and dK tiles of a wave
+  constexpr int RS = 80, PART = CT * RS;             // row of 32 bf16 and its padding, a part
+  constexpr int NY = 0, NR = 3 * PART, NE = NR + RP * PART;  // dy, r, e in LDS
+  constexpr int ROWS = NE + (DELTA ? 3 : 0) * PART;
+  // afterwards, in the same memory: the tiles in three parts, row-major 16 x 16 bf16, and for
+  // KDA the diagonal ones in fp32
+  constexpr int MAT = 3 * 512, LP = 20, DIAG = TILES * MAT;
+  static_assert(DIAG + (CH ? 2 * NB * SB * LP * 4 : 0) <= ROWS, "the tiles fit");
+  __shared__ __align__(16) char rows[ROWS];
+  __shared__ float sx[W][CT], send[W];
   const int cell = blockIdx.x, h = cell % a.heads;
   int tok, count;
   if (!a.plan.cell(cell / a.heads, tok, count)) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int d0 = wave * 16 * TD + m;  // channel of tile u: d0 + 16 u
   const int nb = (count + SB - 1) / SB;
   const size_t H = a.heads;
@@ -44,366 +85,455 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
   const float* row = a.w.row + (size_t)cell * 3 * CT;
   const size_t base = (size_t)tok * H + h;  // token i: base + i * H
 
-  // ---- the blocks' dP and dK, one block per wave in turn, with dbeta
-  for (int blk = wave; blk < nb; blk += W) {
-    const int left = count - SB * blk;
-    const bool valid = m < left;
-    const size_t at = base + (size_t)(SB * blk + (valid ? m : 0)) * H;
-    f32x4 dP = {0.f, 0.f, 0.f, 0.f}, dK = dP;
-    float db = 0.f;
-    const size_t wr = ((size_t)cell * CT + SB * blk + m) * DV + 4 * g;
+  // ---- products with S and G, and dP and dK, over d_v
+  constexpr int PIECES = CT * (DV >= 32 ? 8 : 4);    // of four values, a step and an array
+  constexpr int NP = (PIECES + NT - 1) / NT, PR = PIECES / CT;
+  struct Stage {
+    f32x4 y[NP], r[NP], e[DELTA ? NP : 1];
+  };
+  auto fetch = [&](Stage& s, int step) {
 #pragma unroll
-    for (int t = 0; t < TV; ++t) {
-      Quad<float> y, r, e;
-      Quad<TIN> x;
-      y.load(a.dy + at * DV + 16 * t + 4 * g);
-      y.mask(row_mask(valid));
+    for (int n = 0; n < NP; ++n) {
+      const int i = min(tid + n * NT, PIECES - 1), t = i / PR, c = 32 * step + i % PR * 4;
+      const size_t at = (base + (size_t)min(t, count - 1) * H) * DV + c;
+      const size_t wr = ((size_t)cell * CT + min(t, count - 1)) * DV + c;
+      s.y[n] = *reinterpret_cast<const f32x4*>(a.dy + at);
       if constexpr (DELTA) {
-        r.load(a.w.r + wr + 16 * t);
-        e.load(a.w.e + wr + 16 * t);
+        s.r[n] = *reinterpret_cast<const f32x4*>(a.w.r + wr);
+        s.e[n] = *reinterpret_cast<const f32x4*>(a.w.e + wr);
       } else {
-        x.load(v + at * DV + 16 * t + 4 * g);
-        x.mask(row_mask(valid));
-      }
+        Quad<TIN> x;
+        x.load(v + at);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (DELTA) {
-          dP = mfma4(y[i], r[i], dP);
-          dK = mfma4(e[i], r[i], dK);
-          db += e[i] * r[i];
-        } else {
-          dP = mfma4(y[i], x[i], dP);
+        for (int j = 0; j < 4; ++j) s.r[n][j] = x[j];
+      }
+    }
+  };
+  float db[DELTA ? NP : 1] = {};
+  auto put = [&](const Stage& s) {
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      const int i = tid + n * NT, t = i / PR;
+      if (PIECES % NT != 0 && i >= PIECES) break;
+      char* to = rows + t * RS + i % PR * 8;
+      const uint32_t ok = row_mask(t < count);  // tokens behind the end: zero
+      auto one = [&](f32x4 x, int at, int parts) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = masked(x[j], ok);
+        const Split4 p = split4(x);
+        *reinterpret_cast<uint2*>(to + at) = p.h;
+        if (parts == 3) {
+          *reinterpret_cast<uint2*>(to + at + PART) = p.m;
+          *reinterpret_cast<uint2*>(to + at + 2 * PART) = p.l;
         }
+      };
+      one(s.y[n], NY, 3);
+      one(s.r[n], NR, RP);
+      if constexpr (DELTA) {
+        one(s.e[n], NE, 3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) db[n] += s.e[n][j] * s.r[n][j];
       }
     }
-    float ratio[4] = {1.f, 1.f, 1.f, 1.f};
-    if constexpr (!CH) {
-      float in, out;
-      gate_products(valid ? a.decay[at] : 1.f, m, g, in, out, ratio);
+  };
+  auto operand = [&](int at, int parts, int blk) {  // lane (m, g): token 16 blk + m, values 8g ..
+    const char* p = rows + at + (SB * blk + m) * RS + 16 * g;
+    Split8 s;
+    s.h = *reinterpret_cast<const uint4*>(p);
+    if (parts == 3) {
+      s.m = *reinterpret_cast<const uint4*>(p + PART);
+      s.l = *reinterpret_cast<const uint4*>(p + 2 * PART);
     }
-    const float bj = DELTA ? row[2 * CT + SB * blk + m] : 1.f;
+    return s;
+  };
+
+  f32x4 dq[NB][TD] = {}, dkr[DELTA ? NB : 1][TD] = {}, dkw[NB][TD] = {}, tile[TW] = {};
+  float end[TD] = {};  // rowsum(S * G)
+  const float* S0 = a.w.S + (size_t)cell * DK * DV;
+  const float* G0 = a.w.G + (size_t)cell * DK * DV;
+  if constexpr (DV < 32) {  // the upper half of the only step
+    for (int i = tid; i < ROWS / 4; i += NT) reinterpret_cast<uint32_t*>(rows)[i] = 0;
+  }
+  Stage st;
+  fetch(st, 0);
+#pragma unroll 1
+  for (int step = 0; step < NS; ++step) {
+    __syncthreads();  // the step before has been read
+    put(st);
+    fetch(st, min(step + 1, NS - 1));
+    Split8 S[TD], G[TD];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * g + i;
-      sp[blk][r * LP + m] = m <= r ? dP[i] * bj * ratio[i] : 0.f;
-      if constexpr (DELTA)
-        sk[blk][r * LP + m] = m < r ? -dK[i] * bj * row[2 * CT + SB * blk + r] * ratio[i] : 0.f;
+    for (int u = 0; u < TD; ++u) {
+      const size_t at = (size_t)(d0 + 16 * u) * DV + 32 * step + (DV >= 32 ? 8 * g : 8 * (g & 1));
+      f32x4 s0 = *reinterpret_cast<const f32x4*>(S0 + at), s1 = *reinterpret_cast<const f32x4*>(S0 + at + 4);
+      f32x4 g0 = *reinterpret_cast<const f32x4*>(G0 + at), g1 = *reinterpret_cast<const f32x4*>(G0 + at + 4);
+      if constexpr (DV < 32) {
+        if (g >= 2) s0 = s1 = g0 = g1 = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) end[u] += s0[i] * g0[i] + s1[i] * g1[i];
+      S[u] = split8(s0, s1);
+      G[u] = split8(g0, g1);
     }
-    if constexpr (DELTA) {
-      db = xsum32(xsum16(db));
-      if (g == 0 && valid) a.dbeta[at] = db;
+    __syncthreads();
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      if (blk >= nb) break;
+      const Split8 y = operand(NY, 3, blk), r = operand(NR, RP, blk);
+#pragma unroll
+      for (int u = 0; u < TD; ++u) {
+        dq[blk][u] = mfma_parts<3, 3>(y, S[u], dq[blk][u]);
+        dkw[blk][u] = mfma_parts<RP, 3>(r, G[u], dkw[blk][u]);
+      }
+      if constexpr (DELTA) {
+        const Split8 e = operand(NE, 3, blk);
+#pragma unroll
+        for (int u = 0; u < TD; ++u) dkr[blk][u] = mfma_parts<3, 3>(e, S[u], dkr[blk][u]);
+      }
+    }
+    // dP_ab and dK_ab transposed (rows: block b's tokens), so that a lane holds four columns
+    // of a row of the tile itself
+    int pair = 0;
+#pragma unroll
+    for (int x = 0; x < NB; ++x)
+#pragma unroll
+      for (int y = 0; y <= x; ++y, ++pair)
+#pragma unroll
+        for (int kind = 0; kind < (DELTA ? 2 : 1); ++kind) {
+          const int n = pair + kind * PAIRS;
+          if (n % W == wave && x < nb)
+            tile[n / W] = mfma_parts<RP, 3>(operand(NR, RP, y), operand(kind ? NE : NY, 3, x), tile[n / W]);
+        }
+  }
+  if constexpr (DELTA) {
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      const int t = (tid + n * NT) / PR;
+      float s = db[n] + dpp<DPP_QUAD_1032>(db[n]);
+      s += dpp<DPP_QUAD_2301>(s);
+      if constexpr (PR == 8) s += xor4(s);
+      if ((PIECES % NT == 0 || tid + n * NT < PIECES) && tid % PR == 0 && t < count)
+        a.dbeta[base + (size_t)t * H] = s;
     }
   }
 
-  // ---- forwards: the state, dq and the readers' part of dk
-  f32x4 S[TV][TD];
-  const float* S0 = a.w.S + (size_t)cell * DK * DV;
-#pragma unroll
-  for (int t = 0; t < TV; ++t)
-#pragma unroll
-    for (int u = 0; u < TD; ++u)
-      S[t][u] = *reinterpret_cast<const f32x4*>(S0 + (size_t)(d0 + 16 * u) * DV + 16 * t + 4 * g);
+  // ---- dP and dK: the triangles, beta, and a scalar gate's decay
   __syncthreads();
-  f32x4 dkr[NB][TD], x[NB][TD];
-
-  // this lane's rows 4g + i of the block's keys, queries and gate products
-  struct Rows {
-    float q[TD][4], k[TD][4], in[TD][4], out[TD][4], all[TD], b[4];
-    float qc[CH ? TD : 1][CH ? SB : 1], kc[CH ? TD : 1][CH ? SB : 1], ac[CH ? TD : 1][CH ? SB : 1];
-  };
-  auto rows = [&](Rows& z, int blk) {
-    const int left = count - SB * blk;
+  float whole[NB];  // scalar gates: a block's decay
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool ok = 4 * g + i < left;
-      const size_t at = (base + (size_t)(SB * blk + (ok ? 4 * g + i : 0)) * H) * DK + d0;
-      z.b[i] = DELTA ? row[2 * CT + SB * blk + 4 * g + i] : 1.f;
+  for (int c = 0; c < NB; ++c) whole[c] = !CH && c < nb ? row[SB * c + SB - 1] : 1.f;
+  {
+    int pair = 0;
 #pragma unroll
-      for (int u = 0; u < TD; ++u) {
-        if constexpr (!CH) {
-          z.q[u][i] = to_f32(masked(q[at + 16 * u], row_mask(ok)));
-          z.k[u][i] = to_f32(masked(k[at + 16 * u], row_mask(ok)));
-          z.in[u][i] = row[SB * blk + 4 * g + i];
-          z.out[u][i] = row[CT + SB * blk + 4 * g + i];
-          z.all[u] = row[SB * blk + SB - 1];
+    for (int x = 0; x < NB; ++x)
+#pragma unroll
+      for (int y = 0; y <= x; ++y, ++pair) {
+        float between = 1.f;
+#pragma unroll
+        for (int c = y + 1; c < x; ++c) between *= whole[c];
+#pragma unroll
+        for (int kind = 0; kind < (DELTA ? 2 : 1); ++kind) {
+          const int n = pair + kind * PAIRS;
+          if (n % W != wave || x >= nb) continue;
+          // lane (m, g): row (reader) m of block x, columns (writers) 4g + i of block y
+          f32x4 t = tile[n / W];
+          if constexpr (DELTA) {
+            t *= *reinterpret_cast<const f32x4*>(row + 2 * CT + SB * y + 4 * g);
+            if (kind) t *= -row[2 * CT + SB * x + m];
+          }
+          if constexpr (!CH) {
+            if (x != y) {
+              t *= *reinterpret_cast<const f32x4*>(row + CT + SB * y + 4 * g);
+              t *= row[SB * x + m] * between;
+            } else {
+              const float gate = SB * x + m < count ? a.decay[base + (size_t)(SB * x + m) * H] : 1.f;
+              float ratio[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+              for (int l = 1; l < SB; ++l) {
+                const float al = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gate), l));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (l > 4 * g + i && l <= m) ratio[i] *= al;
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) t[i] *= ratio[i];
+            }
+          }
+          if (x == y) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = 4 * g + i + kind <= m ? t[i] : 0.f;
+            if constexpr (CH)
+              *reinterpret_cast<f32x4*>(rows + DIAG + ((kind * NB + x) * SB + m) * LP * 4 + 16 * g) = t;
+          }
+          const Split4 p = split4(t);
+          char* to = rows + n * MAT + m * 32 + g * 8;
+          *reinterpret_cast<uint2*>(to) = p.h;
+          *reinterpret_cast<uint2*>(to + 512) = p.m;
+          *reinterpret_cast<uint2*>(to + 1024) = p.l;
         }
       }
+  }
+  __syncthreads();
+  auto tile_rows = [&](int n) {  // lane (m, g): row m, columns 4g ..
+    const char* p = rows + n * MAT + m * 32 + g * 8;
+    return Split4{*reinterpret_cast<const uint2*>(p), *reinterpret_cast<const uint2*>(p + 512),
+                  *reinterpret_cast<const uint2*>(p + 1024)};
+  };
+  auto tile_cols = [&](int n) {  // lane (m, g): column m, rows 4g ..
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const char* p = rows + n * MAT + (4 * g + (m >> 2)) * 32 + (m & 3) * 8;
+    Split4 s;
+    s.h = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+    s.m = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 512)));
+    s.l = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 1024)));
+    return s;
+  };
+
+  // ---- a block's keys and queries: rows 4g + i of channel d0 + 16 u
+  auto load_rows = [&](const TIN* p, int blk, int u) {
+    f32x4 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = SB * blk + 4 * g + i;
+      x[i] = to_f32(masked(p[(base + (size_t)min(t, count - 1) * H) * DK + d0 + 16 * u],
+                           row_mask(t < count)));
     }
-    if constexpr (CH) {
+    return x;
+  };
+  // c + a x, x the rows of a block (exact or not)
+  auto times = [&](const Split4& t, f32x4 x, f32x4 c) {
+    if constexpr (EXACT) {
+      const uint2 e = make_uint2(heads(x[0], x[1]), heads(x[2], x[3])), none = make_uint2(0u, 0u);
+      c = mfma_two(t.l, e, none, none, c);
+      return mfma_two(t.h, e, t.m, e, c);
+    } else {
+      return mfma_split(t, split4(x), c);
+    }
+  };
+  auto store = [&](void* p, int blk, int u, f32x4 x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (SB * blk + 4 * g + i < count)
+        ssm::put(static_cast<TIN*>(p) + (base + (size_t)(SB * blk + 4 * g + i) * H) * DK + d0 + 16 * u, x[i]);
+  };
+
+  if constexpr (!CH) {
+    f32x4 kx[NB][TD], qx[NB][TD];
+    float all = 1.f, before = 1.f;
+#pragma unroll
+    for (int c = 0; c < NB; ++c) all *= whole[c];
+#pragma unroll
+    for (int u = 0; u < TD; ++u) end[u] *= all;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      if (blk >= nb) break;
+      float after = 1.f;
+#pragma unroll
+      for (int c = blk + 1; c < NB; ++c) after *= whole[c];
+      const f32x4 in = *reinterpret_cast<const f32x4*>(row + SB * blk + 4 * g) * before;
+      f32x4 out = *reinterpret_cast<const f32x4*>(row + CT + SB * blk + 4 * g) * after, beta;
+      if constexpr (DELTA) {
+        beta = *reinterpret_cast<const f32x4*>(row + 2 * CT + SB * blk + 4 * g);
+        out *= beta;
+      }
 #pragma unroll
       for (int u = 0; u < TD; ++u) {
+        kx[blk][u] = load_rows(k, blk, u);
+        qx[blk][u] = load_rows(q, blk, u);
+        dq[blk][u] *= in;
+        if constexpr (DELTA) dkr[blk][u] *= -in * beta;
+        dkw[blk][u] *= out;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) end[u] += kx[blk][u][i] * dkw[blk][u][i];
+      }
+      before *= whole[blk];
+    }
+    int pair = 0;
+#pragma unroll
+    for (int x = 0; x < NB; ++x)
+#pragma unroll
+      for (int y = 0; y <= x; ++y, ++pair) {
+        if (x >= nb) continue;
+        const Split4 P = tile_rows(pair), Pt = tile_cols(pair);
+#pragma unroll
+        for (int u = 0; u < TD; ++u) {
+          dq[x][u] = times(P, kx[y][u], dq[x][u]);
+          dkw[y][u] = times(Pt, qx[x][u], dkw[y][u]);
+        }
+        if constexpr (DELTA) {
+          const Split4 K = tile_rows(PAIRS + pair), Kt = tile_cols(PAIRS + pair);
+#pragma unroll
+          for (int u = 0; u < TD; ++u) {
+            dkr[x][u] = times(K, kx[y][u], dkr[x][u]);
+            dkw[y][u] = times(Kt, kx[x][u], dkw[y][u]);
+          }
+        }
+      }
+    float e = 0.f;
+#pragma unroll
+    for (int u = 0; u < TD; ++u) e += end[u];
+    e = row_allreduce(xsum32(xsum16(e)));
+    if (lane == 0) send[wave] = e;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) {
+      if (blk >= nb) break;
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < TD; ++u) {
+        f32x4 dk = dkw[blk][u];
+        s += qx[blk][u] * dq[blk][u] - kx[blk][u] * dkw[blk][u];
+        if constexpr (DELTA) {
+          s += kx[blk][u] * dkr[blk][u];
+          dk += dkr[blk][u];
+        }
+        store(a.dq, blk, u, dq[blk][u]);
+        store(a.dk, blk, u, dk);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float t = row_allreduce(s[i]);
+        if (m == 0) sx[wave][SB * blk + 4 * g + i] = t;
+      }
+    }
+    __syncthreads();
+    if (wave == 0) {  // suffix sums over the chunk's tokens, lane = token
+      float s = 0.f, last = 0.f;
+      for (int w = 0; w < W; ++w) {
+        s += lane < SB * nb ? sx[w][lane] : 0.f;
+        last += send[w];
+      }
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const float t = __shfl_down(s, o);
+        if (lane + o < 64) s += t;
+      }
+      if (lane < count) a.dlog[base + (size_t)lane * H] = last + s;
+    }
+  } else {
+    const float* diagP = reinterpret_cast<const float*>(rows + DIAG);
+    const float* diagK = diagP + NB * SB * LP;
+    // a block's rows of the workspace's decayed keys and queries, split
+    auto decayed = [&](const float* p, int blk, int u) {
+      f32x4 x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = p[((size_t)cell * CT + SB * blk + 4 * g + i) * DK + d0 + 16 * u];
+      return split4(x);
+    };
+    float carry[TD];
+#pragma unroll
+    for (int u = 0; u < TD; ++u) {
+      float blocks[NB];
+#pragma unroll
+      for (int c = 0; c < NB; ++c)
+        blocks[c] = c < nb ? a.w.all[((size_t)cell * NB + c) * DK + d0 + 16 * u] : 1.f;
+      // across blocks, from the ends of the writers' blocks to the starts of the readers'
+#pragma unroll
+      for (int x = 0; x < NB; ++x) {
+        if (x >= nb) break;
+        f32x4 sq = {0.f, 0.f, 0.f, 0.f}, sk = sq;
+        float before = 1.f;
+#pragma unroll
+        for (int y = 0; y < x; ++y) {
+          const Split4 t = decayed(a.w.kt, y, u);
+          sq = mfma_split(tile_rows(x * (x + 1) / 2 + y), t, sq * blocks[y]);
+          sk = mfma_split(tile_rows(PAIRS + x * (x + 1) / 2 + y), t, sk * blocks[y]);
+          before *= blocks[y];
+        }
+        const f32x4 beta = *reinterpret_cast<const f32x4*>(row + 2 * CT + SB * x + 4 * g);
+        dq[x][u] = dq[x][u] * before + sq;
+        dkr[x][u] = sk - dkr[x][u] * beta * before;
+      }
+      float all = 1.f;
+#pragma unroll
+      for (int c = 0; c < NB; ++c) all *= blocks[c];
+      end[u] *= all;
+#pragma unroll
+      for (int y = NB - 1; y >= 0; --y) {
+        if (y >= nb) continue;
+        const f32x4 beta = *reinterpret_cast<const f32x4*>(row + 2 * CT + SB * y + 4 * g);
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        float after = 1.f;
+#pragma unroll
+        for (int x = NB - 1; x > y; --x) {
+          if (x >= nb) continue;
+          s = mfma_split(tile_cols(x * (x + 1) / 2 + y), decayed(a.w.qh, x, u), s * blocks[x]);
+          s = mfma_split(tile_cols(PAIRS + x * (x + 1) / 2 + y), decayed(a.w.kh, x, u), s);
+          after *= blocks[x];
+        }
+        dkw[y][u] *= beta * after;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // still without O_j: the workspace's O k has it
+          end[u] += dkw[y][u][i] * a.w.kt[((size_t)cell * CT + SB * y + 4 * g + i) * DK + d0 + 16 * u];
+        dkw[y][u] += s;
+      }
+      carry[u] = xsum32(xsum16(end[u]));
+      // within a block, its gates one by one, from the last block to the first
+#pragma unroll
+      for (int blk = NB - 1; blk >= 0; --blk) {
+        if (blk >= nb) continue;
+        float qc[SB], kc[SB], ac[SB];
 #pragma unroll
         for (int l = 0; l < SB; ++l) {
-          const bool ok = l < left;
-          const size_t at = (base + (size_t)(SB * blk + (ok ? l : 0)) * H) * DK + d0 + 16 * u;
-          z.qc[u][l] = to_f32(masked(q[at], row_mask(ok)));
-          z.kc[u][l] = to_f32(masked(k[at], row_mask(ok)));
+          const int t = SB * blk + l;
+          const size_t at = (base + (size_t)min(t, count - 1) * H) * DK + d0 + 16 * u;
           const float gate = a.decay[at];
-          z.ac[u][l] = ok ? gate : 1.f;
+          qc[l] = to_f32(masked(q[at], row_mask(t < count)));
+          kc[l] = to_f32(masked(k[at], row_mask(t < count)));
+          ac[l] = t < count ? gate : 1.f;
         }
+        f32x4 in, out, qr, kr;
         float p = 1.f;
 #pragma unroll
         for (int l = 0; l < SB; ++l) {
-          p *= z.ac[u][l];
+          p *= ac[l];
           if (l >> 2 == g) {
-            z.in[u][l & 3] = p;
-            z.q[u][l & 3] = z.qc[u][l];
-            z.k[u][l & 3] = z.kc[u][l];
+            in[l & 3] = p;
+            qr[l & 3] = qc[l];
+            kr[l & 3] = kc[l];
           }
         }
-        z.all[u] = p;
         p = 1.f;
 #pragma unroll
         for (int l = SB - 1; l >= 0; --l) {
-          if (l >> 2 == g) z.out[u][l & 3] = p;
-          p *= z.ac[u][l];
+          if (l >> 2 == g) out[l & 3] = p;
+          p *= ac[l];
         }
-      }
-    }
-  };
-
-#pragma unroll
-  for (int blk = 0; blk < NB; ++blk) {
-    if (blk >= nb) break;
-    Rows z;
-    rows(z, blk);
-    const int left = count - SB * blk;
-    const bool valid = m < left;
-    const size_t at = (base + (size_t)(SB * blk + (valid ? m : 0)) * H) * DV + 4 * g;
-    const size_t wr = ((size_t)cell * CT + SB * blk + m) * DV + 4 * g;
-    f32x4 dq[TD], dk[TD];
-#pragma unroll
-    for (int u = 0; u < TD; ++u) dq[u] = dk[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < TV; ++t) {
-      Quad<float> y, e;
-      y.load(a.dy + at + 16 * t);
-      y.mask(row_mask(valid));
-      if constexpr (DELTA) e.load(a.w.e + wr + 16 * t);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int u = 0; u < TD; ++u) {
-          dq[u] = mfma4(y[i], S[t][u][i], dq[u]);
-          if constexpr (DELTA) dk[u] = mfma4(e[i], S[t][u][i], dk[u]);
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < TD; ++u) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        dq[u][i] *= z.in[u][i];
-        dk[u][i] *= -z.in[u][i] * z.b[i];
-      }
-      if constexpr (!CH) {
-        const float4 p4 = *reinterpret_cast<const float4*>(&sp[blk][m * LP + 4 * g]);
-        const float p[4] = {p4.x, p4.y, p4.z, p4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dq[u] = mfma4(p[i], z.k[u][i], dq[u]);
-        if constexpr (DELTA) {
-          const float4 k4 = *reinterpret_cast<const float4*>(&sk[blk][m * LP + 4 * g]);
-          const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dk[u] = mfma4(kk[i], z.k[u][i], dk[u]);
-        }
-      } else {
-        // row r: keys j = r, r - 1, .. decayed on the way (column j of G)
+        f32x4 xq = dq[blk][u] * in, xr = dkr[blk][u] * in, xw = dkw[blk][u] * out;
+        const float* dP = diagP + blk * SB * LP;
+        const float* dK = diagK + blk * SB * LP;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 4 * g + i;
-          float p = 1.f;
+          p = 1.f;
 #pragma unroll
-          for (int j = SB - 1; j >= 0; --j) {
-            const float y = j <= r ? p * z.kc[u][j] : 0.f;
-            dq[u][i] += sp[blk][r * LP + j] * y;
-            dk[u][i] += sk[blk][r * LP + j] * y;
-            if (j <= r) p *= z.ac[u][j];
+          for (int j = SB - 1; j >= 0; --j) {  // keys r, r - 1, .. decayed on the way
+            const float t = j <= r ? p * kc[j] : 0.f;
+            xq[i] += dP[r * LP + j] * t;
+            xr[i] += dK[r * LP + j] * t;
+            if (j <= r) p *= ac[j];
+          }
+          p = 1.f;
+#pragma unroll
+          for (int j = 0; j < SB; ++j) {  // readers r, r + 1, ..
+            if (j > r) p *= ac[j];
+            const float t = dP[j * LP + r] * qc[j] + dK[j * LP + r] * kc[j];
+            xw[i] += j >= r ? p * t : 0.f;
           }
         }
-      }
-      dkr[blk][u] = dk[u];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[blk][u][i] = z.q[u][i] * dq[u][i] + (DELTA ? z.k[u][i] * dk[u][i] : 0.f);
-        if (4 * g + i < left)
-          put(static_cast<TIN*>(a.dq) + (base + (size_t)(SB * blk + 4 * g + i) * H) * DK + d0 + 16 * u,
-              dq[u][i]);
-      }
-    }
-    // S <- a_1..a_16 S + (O k)^T w
-#pragma unroll
-    for (int t = 0; t < TV; ++t) {
-      float wv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (DELTA) {
-          wv[i] = a.w.r[((size_t)cell * CT + SB * blk + 4 * g + i) * DV + 16 * t + m];
-        } else {
-          const bool ok = 4 * g + i < left;
-          wv[i] = to_f32(masked(v[(base + (size_t)(SB * blk + (ok ? 4 * g + i : 0)) * H) * DV + 16 * t + m],
-                                row_mask(ok)));
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < TD; ++u) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[t][u][i] *= z.all[u];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          S[t][u] = mfma4(wv[i], z.out[u][i] * z.k[u][i] * z.b[i], S[t][u]);
-      }
-    }
-  }
-
-  // ---- backwards: the state's gradient, the writers' part of dk, the gates
-  const float* G0 = a.w.G + (size_t)cell * DK * DV;
-  float carry[TD];
-#pragma unroll
-  for (int u = 0; u < TD; ++u) carry[u] = 0.f;
-#pragma unroll
-  for (int t = 0; t < TV; ++t)
-#pragma unroll
-    for (int u = 0; u < TD; ++u) {
-      const f32x4 G =
-          *reinterpret_cast<const f32x4*>(G0 + (size_t)(d0 + 16 * u) * DV + 16 * t + 4 * g);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) carry[u] += S[t][u][i] * G[i];
-      S[t][u] = G;
-    }
-#pragma unroll
-  for (int u = 0; u < TD; ++u) carry[u] = xsum32(xsum16(carry[u]));  // rowsum(S_end * G_end)
-  if constexpr (!CH) {
-    float s = 0.f;
-#pragma unroll
-    for (int u = 0; u < TD; ++u) s += carry[u];
-    s = row_allreduce(s);
-    if (lane == 0) send[wave] = s;
-  }
-#pragma unroll
-  for (int blk = NB - 1; blk >= 0; --blk) {
-    if (blk >= nb) continue;
-    Rows z;
-    rows(z, blk);
-    const int left = count - SB * blk;
-    const bool valid = m < left;
-    const size_t at = (base + (size_t)(SB * blk + (valid ? m : 0)) * H) * DV + 4 * g;
-    const size_t wr = ((size_t)cell * CT + SB * blk + m) * DV + 4 * g;
-    f32x4 dk[TD];
-#pragma unroll
-    for (int u = 0; u < TD; ++u) dk[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < TV; ++t) {
-      Quad<float> r;
-      Quad<TIN> w;
-      if constexpr (DELTA) {
-        r.load(a.w.r + wr + 16 * t);
-      } else {
-        w.load(v + at + 16 * t);
-        w.mask(row_mask(valid));
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int u = 0; u < TD; ++u) {
-          if constexpr (DELTA) dk[u] = mfma4(r[i], S[t][u][i], dk[u]);
-          else dk[u] = mfma4(w[i], S[t][u][i], dk[u]);
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < TD; ++u) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dk[u][i] *= z.out[u][i] * z.b[i];
-      if constexpr (!CH) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dk[u] = mfma4(sp[blk][(4 * g + i) * LP + m], z.q[u][i], dk[u]);
-          if constexpr (DELTA) dk[u] = mfma4(sk[blk][(4 * g + i) * LP + m], z.k[u][i], dk[u]);
-        }
-      } else {
-        // row j: readers i = j, j + 1, .. (row i of G)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = 4 * g + i;
-          float p = 1.f;
-#pragma unroll
-          for (int r = 0; r < SB; ++r) {
-            if (r > j) p *= z.ac[u][r];
-            const float y = sp[blk][r * LP + j] * z.qc[u][r] + sk[blk][r * LP + j] * z.kc[u][r];
-            dk[u][i] += r >= j ? p * y : 0.f;
-          }
-        }
-      }
-      f32x4 s;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[i] = x[blk][u][i] - z.k[u][i] * dk[u][i];
-        if (4 * g + i < left)
-          put(static_cast<TIN*>(a.dk) + (base + (size_t)(SB * blk + 4 * g + i) * H) * DK + d0 + 16 * u,
-              dkr[blk][u][i] + dk[u][i]);
-      }
-      if constexpr (CH) {
+        store(a.dq, blk, u, xq);
+        store(a.dk, blk, u, xr + xw);
+        f32x4 s = qr * xq + kr * (xr - xw);
 #pragma unroll
         for (int i = 2; i >= 0; --i) s[i] += s[i + 1];
         float after, total;
         above(s[0], lane, g, after, total);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (4 * g + i < left)
-            a.dlog[(base + (size_t)(SB * blk + 4 * g + i) * H) * DK + d0 + 16 * u] =
-                carry[u] + after + s[i];
+          if (SB * blk + 4 * g + i < count)
+            a.dlog[(base + (size_t)(SB * blk + 4 * g + i) * H) * DK + d0 + 16 * u] = carry[u] + after + s[i];
         carry[u] += total;
-      } else {
-        x[blk][u] = s;
       }
-    }
-    if constexpr (!CH) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float s = 0.f;
-#pragma unroll
-        for (int u = 0; u < TD; ++u) s += x[blk][u][i];
-        s = row_allreduce(s);
-        if (m == 0) sx[wave][SB * blk + 4 * g + i] = s;
-      }
-    }
-    if (blk == 0) break;
-    // G <- a_1..a_16 G + (I q)^T dy - (I k)^T dr
-#pragma unroll
-    for (int t = 0; t < TV; ++t) {
-      float yv[4], ev[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool ok = 4 * g + i < left;
-        yv[i] = masked(a.dy[(base + (size_t)(SB * blk + (ok ? 4 * g + i : 0)) * H) * DV + 16 * t + m],
-                       row_mask(ok));
-        if constexpr (DELTA) ev[i] = a.w.e[((size_t)cell * CT + SB * blk + 4 * g + i) * DV + 16 * t + m];
-      }
-#pragma unroll
-      for (int u = 0; u < TD; ++u) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[t][u][i] *= z.all[u];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          S[t][u] = mfma4(yv[i], z.in[u][i] * z.q[u][i], S[t][u]);
-          if constexpr (DELTA) S[t][u] = mfma4(ev[i], -z.in[u][i] * z.b[i] * z.k[u][i], S[t][u]);
-        }
-      }
-    }
-  }
-  if constexpr (!CH) {
-    __syncthreads();
-    if (wave == 0) {  // suffix sums over the chunk's tokens, lane = token
-      float s = 0.f, end = 0.f;
-      for (int w = 0; w < W; ++w) {
-        s += lane < SB * nb ? sx[w][lane] : 0.f;
-        end += send[w];
-      }
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const float y = __shfl_down(s, o);
-        if (lane + o < 64) s += y;
-      }
-      if (lane < count) a.dlog[base + (size_t)lane * H] = end + s;
     }
   }
 }
