@@ -348,7 +348,7 @@ ssm_status ssm_recurrent_decode_step(const ssm_dims* d,
  * A non-finite value of a token may reach outputs of its own sequence up to 15
  * tokens before it (tokens are taken 16 at a time), never another sequence or head.
  * Sums and states are fp32. d->window and d->rank are checked but not used.
- * (total_tokens/64 + batch)*heads < 2^22. Results do not depend on the batch's
+ * heads <= 65536; (total_tokens/64 + batch)*heads < 2^22. Results do not depend on the batch's
  * other sequences and are the same bits from run to run.
  */
 

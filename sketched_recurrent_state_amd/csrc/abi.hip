@@ -201,11 +201,14 @@ Sizes pool_sizes(const ssm_dims& d, int32_t num_slots) {
 // Whole-sequence calls: the cells (chunk, head) of a packed batch bound every grid of the scan
 // (at most 512 threads a cell), so this keeps them below 2^32 threads.
 constexpr long long kMaxCells = 1LL << 22;
+constexpr int kMaxScanHeads = 1 << 16;
 
 ssm_status check_scan(const ssm_dims* d, int32_t total_tokens, const char* fn) {
   ssm_status st = check_dims(d, fn);
   if (st != SSM_OK) return st;
   if (total_tokens < 0) return fail(SSM_E_SHAPE, "%s: total_tokens %d < 0", fn, total_tokens);
+  if (d->heads > kMaxScanHeads)  // a block's 16 tokens within 32-bit byte offsets
+    return fail(SSM_E_SHAPE, "%s: %d heads > %d", fn, d->heads, kMaxScanHeads);
   const long long cells =
       ((long long)total_tokens / ssm::CT + d->batch) * d->heads;
   if (cells >= kMaxCells)

@@ -188,13 +188,14 @@ struct ScanPlan {
 
 inline int scan_capacity(int total, int seqs) { return total / CT + seqs; }
 
-// Workspace: fp32 arrays with one part per cell (chunk, head), cell = chunk * heads + head.
+// Workspace: fp32 arrays with one part per cell (head, chunk), cell = head * cap + chunk, so that
+// a unit's blocks follow one another.
 struct ScanWork {
   // A operands in three bf16 parts, [cells][NB][3][64 lanes][4]:
   float* P;      // P                              (backward: its transpose)
   float* A;      // (I + K diag(b))^-1             (delta rules)
   float* A2;     // the transpose of (I + diag(b) K)^-1  (backward, delta rules)
-  float* row;    // [cells][3][CT]       decay in, decay out (scalar gates), b
+  float* row;    // [cells][NB][3][SB]   decay in, decay out (scalar gates), b
   float* qh;     // [cells][CT][d_k]     I q                          (KDA)
   float* kh;     // [cells][CT][d_k]     I k
   float* kt;     // [cells][CT][d_k]     O k
@@ -241,6 +242,8 @@ __device__ __forceinline__ void store_split(float* base, size_t block, int lane,
   p[64] = s.m;
   p[128] = s.l;
 }
+constexpr int ROW = 3 * SB;  // a block's part of ScanWork::row
+
 struct ScanArgs {
   ScanPlan plan;
   int heads, d_v, num_slots;
@@ -254,6 +257,9 @@ struct ScanArgs {
   void *dq, *dk, *dv;
   float *dlog, *dbeta, *dstate_in;
   ScanWork w;
+  __device__ __forceinline__ size_t cell(int chunk, int head) const {
+    return (size_t)head * plan.cap + chunk;
+  }
 };
 
 // Products of the block's scalar gates for lane (m = lane % 16, g = lane / 16), whose own

@@ -13,7 +13,7 @@
 //   rowsum(S_end * G) = F rowsum(S * G) + sum_j k_j (state part of the writer's dk_j)
 // starts the sums of the gates' gradients without the state at the chunk's end.
 //
-// A wave owns 32 key channels (16 with d_k = 16), so the contractions over d_v stay in its
+// A wave owns 16 or 32 key channels, so the contractions over d_v stay in its
 // registers; dy, e and r pass through LDS 32 values of d_v at a time, split there once for all
 // waves. The 20 tiles of dP and dK are dealt over the waves.
 #pragma once
@@ -53,12 +53,21 @@ __device__ __forceinline__ f32x4 mfma_parts(const Split8& a, const Split8& b, f3
   return mfma32(a.h, b.h, c);
 }
 
+// Channel tiles of a wave: two with Mamba-2's two products; the delta rules' three leave no
+// registers for a second tile (GDN, 4,096 cells of 128 x 128: TILES2 us, with one ONETILE us).
+template <int RULE, int DK>
+constexpr int kGradTiles = RULE == MAMBA2 && DK >= 32 ? 2 : 1;
+template <int RULE, int DK>
+constexpr int kGradThreads = 64 * (DK / 16 / kGradTiles<RULE, DK>);
+
 template <int RULE, int DK, int DV, typename TIN>
-__global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__((kGradThreads<RULE, DK>),
+                                  (DK == 128 || (RULE == MAMBA2 && DK == 64) ? 2 : 1))
+scan_grads_kernel(const ScanArgs a) {
   constexpr bool DELTA = RULE != MAMBA2, CH = RULE == KDA, BF = sizeof(TIN) == 2;
   constexpr bool EXACT = BF && !CH;                  // keys and queries
   constexpr int RP = !DELTA && BF ? 1 : 3;           // parts of w / r (Mamba-2: the values)
-  constexpr int TD = DK >= 32 ? 2 : 1, W = DK >= 32 ? DK / 32 : 1, NT = 64 * W;
+  constexpr int TD = kGradTiles<RULE, DK>, NT = kGradThreads<RULE, DK>, W = NT / 64;
   constexpr int NS = DV >= 32 ? DV / 32 : 1;         // steps of 32 values of d_v
   constexpr int PAIRS = NB * (NB + 1) / 2, TILES = DELTA ? 2 * PAIRS : PAIRS;
   constexpr int TW = (TILES + W - 1) / W;            // dP and dK tiles of a wave
@@ -71,9 +80,10 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
   static_assert(DIAG + (CH ? 2 * NB * SB * LP * 4 : 0) <= ROWS, "the tiles fit");
   __shared__ __align__(16) char rows[ROWS];
   __shared__ float sx[W][CT], send[W];
-  const int cell = blockIdx.x, h = cell % a.heads;
+  const int h = blockIdx.x % a.heads, chunk = blockIdx.x / a.heads;
+  const size_t cell = a.cell(chunk, h);
   int tok, count;
-  if (!a.plan.cell(cell / a.heads, tok, count)) return;
+  if (!a.plan.cell(chunk, tok, count)) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int d0 = wave * 16 * TD + m;  // channel of tile u: d0 + 16 u
@@ -82,7 +92,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
   const TIN* q = static_cast<const TIN*>(a.q);
   const TIN* k = static_cast<const TIN*>(a.k);
   const TIN* v = static_cast<const TIN*>(a.v);
-  const float* row = a.w.row + (size_t)cell * 3 * CT;
+  const float* row = a.w.row + cell * NB * ROW;  // block x: + ROW * x
   const size_t base = (size_t)tok * H + h;  // token i: base + i * H
 
   // ---- products with S and G, and dP and dK, over d_v
@@ -96,7 +106,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
     for (int n = 0; n < NP; ++n) {
       const int i = min(tid + n * NT, PIECES - 1), t = i / PR, c = 32 * step + i % PR * 4;
       const size_t at = (base + (size_t)min(t, count - 1) * H) * DV + c;
-      const size_t wr = ((size_t)cell * CT + min(t, count - 1)) * DV + c;
+      const size_t wr = (cell * CT + min(t, count - 1)) * DV + c;
       s.y[n] = *reinterpret_cast<const f32x4*>(a.dy + at);
       if constexpr (DELTA) {
         s.r[n] = *reinterpret_cast<const f32x4*>(a.w.r + wr);
@@ -149,8 +159,8 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
 
   f32x4 dq[NB][TD] = {}, dkr[DELTA ? NB : 1][TD] = {}, dkw[NB][TD] = {}, tile[TW] = {};
   float end[TD] = {};  // rowsum(S * G)
-  const float* S0 = a.w.S + (size_t)cell * DK * DV;
-  const float* G0 = a.w.G + (size_t)cell * DK * DV;
+  const float* S0 = a.w.S + cell * DK * DV;
+  const float* G0 = a.w.G + cell * DK * DV;
   if constexpr (DV < 32) {  // the upper half of the only step
     for (int i = tid; i < ROWS / 4; i += NT) reinterpret_cast<uint32_t*>(rows)[i] = 0;
   }
@@ -221,7 +231,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
   __syncthreads();
   float whole[NB];  // scalar gates: a block's decay
 #pragma unroll
-  for (int c = 0; c < NB; ++c) whole[c] = !CH && c < nb ? row[SB * c + SB - 1] : 1.f;
+  for (int c = 0; c < NB; ++c) whole[c] = !CH && c < nb ? row[ROW * c + SB - 1] : 1.f;
   {
     int pair = 0;
 #pragma unroll
@@ -238,13 +248,13 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
           // lane (m, g): row (reader) m of block x, columns (writers) 4g + i of block y
           f32x4 t = tile[n / W];
           if constexpr (DELTA) {
-            t *= *reinterpret_cast<const f32x4*>(row + 2 * CT + SB * y + 4 * g);
-            if (kind) t *= -row[2 * CT + SB * x + m];
+            t *= *reinterpret_cast<const f32x4*>(row + ROW * y + 2 * SB + 4 * g);
+            if (kind) t *= -row[ROW * x + 2 * SB + m];
           }
           if constexpr (!CH) {
             if (x != y) {
-              t *= *reinterpret_cast<const f32x4*>(row + CT + SB * y + 4 * g);
-              t *= row[SB * x + m] * between;
+              t *= *reinterpret_cast<const f32x4*>(row + ROW * y + SB + 4 * g);
+              t *= row[ROW * x + m] * between;
             } else {
               const float gate = SB * x + m < count ? a.decay[base + (size_t)(SB * x + m) * H] : 1.f;
               float ratio[4] = {1.f, 1.f, 1.f, 1.f};
@@ -330,10 +340,10 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
       float after = 1.f;
 #pragma unroll
       for (int c = blk + 1; c < NB; ++c) after *= whole[c];
-      const f32x4 in = *reinterpret_cast<const f32x4*>(row + SB * blk + 4 * g) * before;
-      f32x4 out = *reinterpret_cast<const f32x4*>(row + CT + SB * blk + 4 * g) * after, beta;
+      const f32x4 in = *reinterpret_cast<const f32x4*>(row + ROW * blk + 4 * g) * before;
+      f32x4 out = *reinterpret_cast<const f32x4*>(row + ROW * blk + SB + 4 * g) * after, beta;
       if constexpr (DELTA) {
-        beta = *reinterpret_cast<const f32x4*>(row + 2 * CT + SB * blk + 4 * g);
+        beta = *reinterpret_cast<const f32x4*>(row + ROW * blk + 2 * SB + 4 * g);
         out *= beta;
       }
 #pragma unroll
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
       f32x4 x;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        x[i] = p[((size_t)cell * CT + SB * blk + 4 * g + i) * DK + d0 + 16 * u];
+        x[i] = p[(cell * CT + SB * blk + 4 * g + i) * DK + d0 + 16 * u];
       return split4(x);
     };
     float carry[TD];
@@ -426,11 +436,12 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
       float blocks[NB];
 #pragma unroll
       for (int c = 0; c < NB; ++c)
-        blocks[c] = c < nb ? a.w.all[((size_t)cell * NB + c) * DK + d0 + 16 * u] : 1.f;
+        blocks[c] = c < nb ? a.w.all[(cell * NB + c) * DK + d0 + 16 * u] : 1.f;
       // across blocks, from the ends of the writers' blocks to the starts of the readers'
 #pragma unroll
       for (int x = 0; x < NB; ++x) {
         if (x >= nb) break;
+        __builtin_amdgcn_sched_barrier(0);
         f32x4 sq = {0.f, 0.f, 0.f, 0.f}, sk = sq;
         float before = 1.f;
 #pragma unroll
@@ -440,7 +451,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
           sk = mfma_split(tile_rows(PAIRS + x * (x + 1) / 2 + y), t, sk * blocks[y]);
           before *= blocks[y];
         }
-        const f32x4 beta = *reinterpret_cast<const f32x4*>(row + 2 * CT + SB * x + 4 * g);
+        const f32x4 beta = *reinterpret_cast<const f32x4*>(row + ROW * x + 2 * SB + 4 * g);
         dq[x][u] = dq[x][u] * before + sq;
         dkr[x][u] = sk - dkr[x][u] * beta * before;
       }
@@ -451,7 +462,8 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
 #pragma unroll
       for (int y = NB - 1; y >= 0; --y) {
         if (y >= nb) continue;
-        const f32x4 beta = *reinterpret_cast<const f32x4*>(row + 2 * CT + SB * y + 4 * g);
+        __builtin_amdgcn_sched_barrier(0);
+        const f32x4 beta = *reinterpret_cast<const f32x4*>(row + ROW * y + 2 * SB + 4 * g);
         f32x4 s = {0.f, 0.f, 0.f, 0.f};
         float after = 1.f;
 #pragma unroll
@@ -464,7 +476,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
         dkw[y][u] *= beta * after;
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // still without O_j: the workspace's O k has it
-          end[u] += dkw[y][u][i] * a.w.kt[((size_t)cell * CT + SB * y + 4 * g + i) * DK + d0 + 16 * u];
+          end[u] += dkw[y][u][i] * a.w.kt[(cell * CT + SB * y + 4 * g + i) * DK + d0 + 16 * u];
         dkw[y][u] += s;
       }
       carry[u] = xsum32(xsum16(end[u]));
@@ -472,6 +484,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
 #pragma unroll
       for (int blk = NB - 1; blk >= 0; --blk) {
         if (blk >= nb) continue;
+        __builtin_amdgcn_sched_barrier(0);  // one block's 48 values at a time
         float qc[SB], kc[SB], ac[SB];
 #pragma unroll
         for (int l = 0; l < SB; ++l) {
@@ -505,6 +518,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 4 * g + i;
+          __builtin_amdgcn_sched_barrier(0);
           p = 1.f;
 #pragma unroll
           for (int j = SB - 1; j >= 0; --j) {  // keys r, r - 1, .. decayed on the way
@@ -513,6 +527,7 @@ __global__ void __launch_bounds__(DK >= 32 ? 2 * DK : 64) scan_grads_kernel(cons
             xr[i] += dK[r * LP + j] * t;
             if (j <= r) p *= ac[j];
           }
+          __builtin_amdgcn_sched_barrier(0);
           p = 1.f;
 #pragma unroll
           for (int j = 0; j < SB; ++j) {  // readers r, r + 1, ..

@@ -14,8 +14,8 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
   constexpr int T = DK / 16, LD = DK + 4, LK = 20;
   __shared__ __align__(16) float sq[CH ? SB * LD : 1], sk[CH ? SB * LD : 1], sa[CH ? SB * LD : 1];
   __shared__ __align__(16) float sl[2 * SB * LK];
-  const int cell = blockIdx.x / NB, blk = blockIdx.x % NB;
-  const int h = cell % a.heads, c = cell / a.heads;
+  const int blk = blockIdx.x % NB, h = blockIdx.x / NB % a.heads, c = blockIdx.x / NB / a.heads;
+  const size_t cell = a.cell(c, h), block = cell * NB + blk;
   int tok, count;
   if (!a.plan.cell(c, tok, count) || SB * blk >= count) return;
   tok += SB * blk;
@@ -34,11 +34,11 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
     const float gate = valid ? a.decay[at] : 1.f;
     float in, out, ratio[4];
     gate_products(gate, m, g, in, out, ratio);
-    float* row = a.w.row + (size_t)cell * 3 * CT + SB * blk;
+    float* row = a.w.row + block * ROW;
     if (g == 0) {
       row[m] = in;
-      row[CT + m] = out;
-      row[2 * CT + m] = b;
+      row[SB + m] = out;
+      row[2 * SB + m] = b;
     }
     if constexpr (EXACT) {
 #pragma unroll
@@ -88,10 +88,10 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
         sa[s] = valid ? aa[i] : 1.f;
       }
     }
-    if (g == 0) a.w.row[(size_t)cell * 3 * CT + 2 * CT + SB * blk + m] = b;
+    if (g == 0) a.w.row[block * ROW + 2 * SB + m] = b;
     __syncthreads();
     // I q, I k, O k and the whole block's decay, one channel at a time
-    const size_t o = ((size_t)cell * CT + SB * blk) * DK;
+    const size_t o = block * SB * DK;
     for (int ch = lane; ch < DK; ch += 64) {
       float p = 1.f;
 #pragma unroll
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
         a.w.qh[o + l * DK + ch] = p * sq[l * LD + ch];
         a.w.kh[o + l * DK + ch] = p * sk[l * LD + ch];
       }
-      a.w.all[((size_t)cell * NB + blk) * DK + ch] = p;
+      a.w.all[block * DK + ch] = p;
       p = 1.f;
 #pragma unroll
       for (int l = SB - 1; l >= 0; --l) {
@@ -140,7 +140,6 @@ __global__ void __launch_bounds__(64) scan_prep_kernel(const ScanArgs a) {
       }
     }
   }
-  const size_t block = (size_t)cell * NB + blk;
   if constexpr (BWD) {  // lane (m, g) holds the transpose's row m, columns 4g + i
     store_split(a.w.P, block, lane, split4(P));
   } else {

@@ -7,14 +7,18 @@
 
 namespace ssm {
 
-// Calls f(waves of a workgroup, narrow): wide workgroups do least work; where they leave most
-// of the 1,024 SIMDs without a wave, the rows of a column block are divided over d_k / 32 waves.
-template <int DK, int DV, typename F>
+// Calls f(waves of a workgroup, narrow). Wide workgroups do least work; where they leave SIMDs
+// (there are 1,024) without a wave, the rows of a column block are divided over as many waves
+// as fill them: 32 rows a wave at least.
+template <int RULE, int DK, int DV, typename F>
 void split_shape(const ssm_dims& d, F&& f) {
   using std::integral_constant;
-  const long long waves = (long long)d.batch * d.heads * (DV / 16);
-  if (waves <= 512)
-    f(integral_constant<int, kPadded<DK> / 32>{}, std::true_type{});
+  const long long blocks = (long long)d.batch * d.heads * (DV / 16);
+  if constexpr (DK == 128) {
+    if (blocks <= 256) return f(integral_constant<int, 4>{}, std::true_type{});
+  }
+  if (blocks <= (RULE == KDA ? 256 : 512))
+    f(integral_constant<int, (DK >= 64 ? 2 : 1)>{}, std::true_type{});
   else
     f(integral_constant<int, (DV >= 64 ? 4 : DV / 16)>{}, std::false_type{});
 }
@@ -31,7 +35,7 @@ hipError_t launch_scan_rule(const ssm_dims& d, const ScanArgs& a, bool backward,
                          dim3(64), 0, stream, a);
     };
     auto state = [&](auto B) {
-      split_shape<kDK, kDV>(d, [&](auto NW, auto NARROW) {
+      split_shape<RULE, kDK, kDV>(d, [&](auto NW, auto NARROW) {
         constexpr int nw = decltype(NW)::value;
         constexpr bool narrow = decltype(NARROW)::value, bwd = decltype(B)::value;
         hipLaunchKernelGGL((scan_state_kernel<RULE, kDK, TIN, nw, narrow, bwd>),
@@ -46,7 +50,7 @@ hipError_t launch_scan_rule(const ssm_dims& d, const ScanArgs& a, bool backward,
     }
     prep(std::true_type{});
     state(std::true_type{});
-    split_shape<kDK, kDV>(d, [&](auto NW, auto NARROW) {
+    split_shape<RULE, kDK, kDV>(d, [&](auto NW, auto NARROW) {
       constexpr int nw = decltype(NW)::value;
       constexpr bool narrow = decltype(NARROW)::value;
       hipLaunchKernelGGL((scan_gradient_kernel<RULE, kDK, TIN, nw, narrow>),
@@ -54,7 +58,7 @@ hipError_t launch_scan_rule(const ssm_dims& d, const ScanArgs& a, bool backward,
                          stream, a);
     });
     hipLaunchKernelGGL((scan_grads_kernel<RULE, kDK, kDV, TIN>), dim3(cells),
-                       dim3(kDK >= 32 ? 2 * kDK : 64), 0, stream, a);
+                       dim3(kGradThreads<RULE, kDK>), 0, stream, a);
     return hipGetLastError();
   });
 }

@@ -6,9 +6,9 @@
 // queries, which are exact (bf16 inputs with scalar gates) or split too.
 //
 // Two shapes. Wide: each of a workgroup's waves holds a column block of its own. Narrow, for
-// few units (scan_rule.hpp says when): the rows of one column block are divided over
-// DS = d_k / 32 waves, which add up their parts of k S through LDS, and one more wave works
-// out y a block behind, off the recurrence's path.
+// few units (scan_rule.hpp says when): the rows of one column block are divided over DS
+// waves, which add up their parts of k S through LDS, and one more wave works out y a block
+// behind, off the recurrence's path.
 //
 // The waves of a workgroup share the block's operands: they are loaded into registers two
 // blocks ahead, put into LDS when the block before is under way, and read from there.
@@ -130,38 +130,60 @@ struct SplitShare {
   uint2 p[P ? NP : 1], a[DELTA ? NP : 1];
   float row, all[RULE == KDA ? (DK + NT - 1) / NT : 1];
 
-  // rows, cols: KDA's decayed keys in the workspace; A: the pass's inverse.
-  __device__ __forceinline__ void load(const ScanArgs& s, const float* rows, const float* cols,
-                                       const float* A, size_t cell, int blk, int tok, int count,
-                                       int h, int tid) {
+  // Where a thread's pieces are: byte offsets from the block's first token, in two parts, of
+  // which the first (the token's) is cut at the sequence's last token.
+  struct Place {
+    uint32_t token[NK], column[NK];
+    __device__ __forceinline__ Place(const ScanArgs& s, int tid) {
 #pragma unroll
-    for (int n = 0; n < NK; ++n) {
-      const int piece = min(tid + n * NT, KP - 1);  // the surplus threads load the last one again
-      if constexpr (RULE == KDA) {
-        const size_t at = (cell * CT + SB * blk) * DK + piece * 4;
-        k[n] = *reinterpret_cast<const uint4*>(rows + at);
-        c[n] = *reinterpret_cast<const uint4*>(cols + at);
-        if constexpr (Q) q[n] = *reinterpret_cast<const uint4*>(s.w.qh + at);
-      } else {
-        const int r = min(piece / (DK / E), count - 1);
-        const size_t at = ((size_t)(tok + r) * s.heads + h) * DK + piece % (DK / E) * E;
-        k[n] = *reinterpret_cast<const uint4*>(static_cast<const TIN*>(s.k) + at);
-        if constexpr (Q) q[n] = *reinterpret_cast<const uint4*>(static_cast<const TIN*>(s.q) + at);
+      for (int n = 0; n < NK; ++n) {
+        const int piece = min(tid + n * NT, KP - 1);  // the surplus threads load the last one again
+        token[n] = piece / (DK / E) * token_bytes(s);
+        column[n] = piece % (DK / E) * 16;
       }
     }
-    const size_t block = (cell * NB + blk) * 192;
+    static __device__ __forceinline__ uint32_t token_bytes(const ScanArgs& s) {
+      return (uint32_t)(s.heads * DK * sizeof(TIN));
+    }
+  };
+  // Block j of a unit whose first token is row `at` of the inputs and whose first block is
+  // `block0` of the workspace; `count` tokens from the block's first to the sequence's end.
+  // rows, cols: KDA's decayed keys in the workspace; A: the pass's inverse.
+  __device__ __forceinline__ void load(const ScanArgs& s, const Place& place, const float* rows,
+                                       const float* cols, const float* A, size_t at, size_t block0,
+                                       int j, int count, int tid) {
+    const size_t block = block0 + j;
+    if constexpr (RULE == KDA) {
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        const uint32_t piece = min(tid + n * NT, KP - 1);
+        k[n] = reinterpret_cast<const uint4*>(rows + block * SB * DK)[piece];
+        c[n] = reinterpret_cast<const uint4*>(cols + block * SB * DK)[piece];
+        if constexpr (Q) q[n] = reinterpret_cast<const uint4*>(s.w.qh + block * SB * DK)[piece];
+      }
+    } else {
+      const size_t first = (at + (size_t)(SB * j) * s.heads) * DK * sizeof(TIN);
+      const char* pk = static_cast<const char*>(s.k) + first;
+      const char* pq = static_cast<const char*>(s.q) + first;
+      const uint32_t last = (uint32_t)(min(count, SB) - 1) * Place::token_bytes(s);
+#pragma unroll
+      for (int n = 0; n < NK; ++n) {
+        const uint32_t o = min(place.token[n], last) + place.column[n];
+        k[n] = *reinterpret_cast<const uint4*>(pk + o);
+        if constexpr (Q) q[n] = *reinterpret_cast<const uint4*>(pq + o);
+      }
+    }
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-      const int i = min(tid + n * NT, 191);
-      if constexpr (P) p[n] = reinterpret_cast<const uint2*>(s.w.P)[block + i];
-      if constexpr (DELTA) a[n] = reinterpret_cast<const uint2*>(A)[block + i];
+      const uint32_t i = min(tid + n * NT, 191);
+      if constexpr (P) p[n] = (reinterpret_cast<const uint2*>(s.w.P) + block * 192)[i];
+      if constexpr (DELTA) a[n] = (reinterpret_cast<const uint2*>(A) + block * 192)[i];
     }
-    const int i = min(tid, 3 * SB - 1);
-    row = s.w.row[cell * 3 * CT + (i / SB) * CT + SB * blk + i % SB];
+    row = (s.w.row + block * ROW)[(uint32_t)min(tid, ROW - 1)];
     if constexpr (RULE == KDA) {
 #pragma unroll
       for (int n = 0; n < (DK + NT - 1) / NT; ++n)
-        all[n] = s.w.all[(cell * NB + blk) * DK + min(tid + n * NT, DK - 1)];
+        all[n] = (s.w.all + block * DK)[(uint32_t)min(tid + n * NT, DK - 1)];
     }
   }
   static __device__ __forceinline__ void put_piece(Block& b, int array, int piece, uint4 x) {
@@ -199,6 +221,22 @@ struct SplitShare {
       for (int n = 0; n < (DK + NT - 1) / NT; ++n)
         if (tid + n * NT < DK) b.all[tid + n * NT] = all[n];
     }
+  }
+};
+
+// A lane's four values of a block's tokens 4g + i (one column), cut at the sequence's last token.
+template <typename T>
+struct ColumnPlace {
+  uint32_t token[4], bytes;
+  __device__ __forceinline__ ColumnPlace(size_t stride, int g) : bytes((uint32_t)(stride * sizeof(T))) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) token[i] = (4 * g + i) * bytes;
+  }
+  __device__ __forceinline__ void load(const T* p, int j, int len, T (&x)[4]) const {
+    const char* first = reinterpret_cast<const char*>(p) + (size_t)(SB * j) * bytes;
+    const uint32_t last = (uint32_t)(min(len - SB * j, SB) - 1) * bytes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const T*>(first + min(token[i], last));
   }
 };
 
@@ -261,7 +299,6 @@ struct SplitShape {
   static constexpr int DS = NARROW ? NW : 1;            // waves of a column block
   static constexpr int TL = kPadded<DK> / 16 / DS;      // tiles of a wave
   static constexpr int CB = NW / DS;                    // column blocks of the workgroup
-  static_assert(!NARROW || NW == kPadded<DK> / 32, "32 channels a wave");
 };
 
 template <int RULE, int DK, typename TIN, bool NARROW>
@@ -348,14 +385,15 @@ __global__ void __launch_bounds__(64 * (NW + (NARROW && !BWD)), 2) scan_state_ke
     Share s;
     TIN v[4];
   };
+  const size_t cell0 = a.cell(first, h);
+  const typename Share::Place place(a, tid);
+  const ColumnPlace<TIN> vplace(stride, g);
   auto fetch = [&](Ahead& x, int j) {
-    x.s.load(a, a.w.kh, a.w.kt, a.w.A, (size_t)(first + j / NB) * a.heads + h, j % NB, tok + SB * j,
-             len - SB * j, h, tid);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x.v[i] = v[(size_t)min(SB * j + 4 * g + i, len - 1) * stride];
+    x.s.load(a, place, a.w.kh, a.w.kt, a.w.A, (size_t)tok * a.heads + h, cell0 * NB, j, len - SB * j, tid);
+    vplace.load(v, j, len, x.v);
   };
   auto run = [&](const Block& b, const TIN (&vr)[4], int j) {
-    const size_t cell = (size_t)(first + j / NB) * a.heads + h;
+    const size_t cell = cell0 + j / NB;
     if constexpr (BWD) {
       if (j % NB == 0) {
         float* p = a.w.S + cell * DK * a.d_v + col;
@@ -365,10 +403,12 @@ __global__ void __launch_bounds__(64 * (NW + (NARROW && !BWD)), 2) scan_state_ke
     // what follows the sum over waves is read before it
     f32x4 ks, o, w;
     const f32x4 in = b.rows(0, g), out = b.rows(1, g), beta = b.rows(2, g);
-    Split4 A, kt[TL];
+    Split4 A, kt[NARROW ? TL : 1];
     if constexpr (DELTA) A = b.split(b.A, lane);
+    if constexpr (NARROW) {
 #pragma unroll
-    for (int t = 0; t < TL; ++t) kt[t] = b.columns(Block::COLS, m, g, 2 * s0 + t);
+      for (int t = 0; t < TL; ++t) kt[t] = b.columns(Block::COLS, m, g, 2 * s0 + t);
+    }
     if constexpr (DELTA || !BWD) {
       const StateParts<TL> x(S);
       if constexpr (DELTA) ks = x.times(b, 0, s0, m, g);
@@ -403,7 +443,8 @@ __global__ void __launch_bounds__(64 * (NW + (NARROW && !BWD)), 2) scan_state_ke
     const Split4 ow = split4(SCALAR ? out * w : w);
 #pragma unroll
     for (int t = 0; t < TL; ++t)
-      S[t] = Block::update(kt[t], ow, S[t] * b.whole(2 * s0 + t, g));
+      S[t] = Block::update(NARROW ? kt[NARROW ? t : 0] : b.columns(Block::COLS, m, g, t), ow,
+                           S[t] * b.whole(2 * s0 + t, g));
     if constexpr (YWAVE) xq[j & 1][tid] = o;
     if constexpr (!BWD && !YWAVE) {
       if constexpr (SCALAR) o *= in;
@@ -475,14 +516,16 @@ __global__ void __launch_bounds__(64 * NW, 2) scan_gradient_kernel(const ScanArg
     Share s;
     float dy[4];
   };
+  const size_t cell0 = a.cell(first, h);
+  const typename Share::Place place(a, tid);
+  const ColumnPlace<float> yplace(stride, g);
   auto fetch = [&](Ahead& x, int j) {
-    x.s.load(a, a.w.kt, a.w.kh, a.w.A2, (size_t)(first + j / NB) * a.heads + h, j % NB, tok + SB * j,
-             len - SB * j, h, tid);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x.dy[i] = dy[(size_t)min(SB * j + 4 * g + i, len - 1) * stride];
+    x.s.load(a, place, a.w.kt, a.w.kh, a.w.A2, (size_t)tok * a.heads + h, cell0 * NB, j, len - SB * j,
+             tid);
+    yplace.load(dy, j, len, x.dy);
   };
   auto run = [&](const Block& b, const float (&yr)[4], int j) {
-    const size_t cell = (size_t)(first + j / NB) * a.heads + h;
+    const size_t cell = cell0 + j / NB;
     if (j % NB == NB - 1 || j == blocks - 1) {
       float* p = a.w.G + cell * DK * a.d_v + col;
       each_row<DK, TL>(s0, g, [&](int t, int i, size_t c) { p[c * a.d_v] = G[t][i]; });
@@ -492,26 +535,33 @@ __global__ void __launch_bounds__(64 * NW, 2) scan_gradient_kernel(const ScanArg
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = SB * j + 4 * g + i < len ? yr[i] : 0.f;
     iy = SCALAR ? in * y : y;
-    Split4 A, P = b.split(b.P, lane), q[TL], k[TL];
-    if constexpr (DELTA) A = b.split(b.A, lane);
+    Split4 A, P, q[NARROW ? TL : 1], k[NARROW ? TL : 1];
+    if constexpr (NARROW) {  // what follows the sum over waves is read before it
+      P = b.split(b.P, lane);
+      if constexpr (DELTA) A = b.split(b.A, lane);
 #pragma unroll
-    for (int t = 0; t < TL; ++t) {
-      q[t] = b.columns(1, m, g, 2 * s0 + t);
-      if constexpr (DELTA) k[t] = b.columns(Block::COLS, m, g, 2 * s0 + t);
+      for (int t = 0; t < TL; ++t) {
+        q[t] = b.columns(1, m, g, 2 * s0 + t);
+        if constexpr (DELTA) k[t] = b.columns(Block::COLS, m, g, 2 * s0 + t);
+      }
     }
-    const Split4 ys = split4(y), iys = split4(iy);
     f32x4 w = StateParts<TL>(G).times(b, 0, s0, m, g);
+    if constexpr (DS > 1) xk[tid] = w;
+    if constexpr (!NARROW) P = b.split(b.P, lane);
+    const f32x4 pdy = mfma_split(P, split4(y), f32x4{0.f, 0.f, 0.f, 0.f});
+    const Split4 iys = split4(iy);
+#pragma unroll
+    for (int t = 0; t < TL; ++t)
+      G[t] = Block::update(NARROW ? q[NARROW ? t : 0] : b.columns(1, m, g, t), iys,
+                           G[t] * b.whole(2 * s0 + t, g));
     if constexpr (DS > 1) {
-      xk[tid] = w;
       __syncthreads();
       w = wave_sum<DS>(xk, lane);
     }
-    if constexpr (SCALAR) w *= out;
-    w = mfma_split(P, ys, w);
-#pragma unroll
-    for (int t = 0; t < TL; ++t) G[t] = Block::update(q[t], iys, G[t] * b.whole(2 * s0 + t, g));
+    w = (SCALAR ? out * w : w) + pdy;
     f32x4 dr = w;
     if constexpr (DELTA) {
+      if constexpr (!NARROW) A = b.split(b.A, lane);
       const f32x4 e = mfma_split(A, split4(w), f32x4{0.f, 0.f, 0.f, 0.f});
       if (dpart == 0) {
         float* p = a.w.e + (cell * CT + SB * (j % NB) + 4 * g) * a.d_v + col;
@@ -521,7 +571,8 @@ __global__ void __launch_bounds__(64 * NW, 2) scan_gradient_kernel(const ScanArg
       dr = beta * e;
       const Split4 ir = split4(SCALAR ? -(in * dr) : -dr);
 #pragma unroll
-      for (int t = 0; t < TL; ++t) G[t] = Block::update(k[t], ir, G[t]);
+      for (int t = 0; t < TL; ++t)
+        G[t] = Block::update(NARROW ? k[NARROW ? t : 0] : b.columns(Block::COLS, m, g, t), ir, G[t]);
     }
     if (dpart == 0) {
       TIN* dv = static_cast<TIN*>(a.dv) + ro + (size_t)(SB * j + 4 * g) * stride;

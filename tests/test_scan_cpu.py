@@ -72,6 +72,8 @@ def test_forward_refusals():
     assert st == 2 and "slot map" in msg
     st, msg = forward(dims(heads=1 << 12), total=1 << 17)
     assert st == 2 and "heads" in msg
+    st, msg = forward(dims(heads=65537, batch=1), total=1)
+    assert st == 2 and "heads" in msg
     assert forward(dims(batch=0))[0] == 0
     bad = dims()
     bad.d_k = 48
