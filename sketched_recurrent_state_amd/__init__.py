@@ -540,6 +540,14 @@ def sketch_decode_step_ls(d: Dims, sketch_q, read_map, q, k_buf, v_buf, decay_bu
 # ----------------------------------------------------------------------------
 # whole sequences and serving plans
 # ----------------------------------------------------------------------------
+# These calls take a few microseconds on the device at small sizes, so their marshalling keeps
+# to one look at each tensor, one at the device and one at its stream.
+import torch as _torch  # noqa: E402  (loaded above, before the library)
+
+_F32_T, _I32_T = (_torch.float32,), (_torch.int32,)
+_IN_T = {IN_BF16: (_torch.bfloat16,), IN_F32: (_torch.float32,)}
+
+
 def _on_device(args, stream, call) -> None:
     """call(stream address) on the device that the tensors among args share: their device
     becomes the current one for the call, and its current stream is the default."""
@@ -553,11 +561,14 @@ def _on_device(args, stream, call) -> None:
             raise ValueError(f"tensors on different devices: {dev}, {a.device}")
     if dev is None:
         return call(_stream(stream))  # raw addresses
-    import torch
-    if dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(dev):
-        call(_stream(stream))
+    if stream is None:
+        stream = _torch.cuda.current_stream(dev)
+    if not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev.index == _torch.cuda.current_device():
+        return call(stream)
+    with _torch.cuda.device(dev):
+        call(stream)
 
 
 def scan_sizes(d: Dims, total_tokens: int) -> tuple:
@@ -572,43 +583,41 @@ def scan_plan(lengths, total_tokens: int, plan, *, n_seqs: Optional[int] = None,
     """ssm_scan_plan: the plan of a packed batch from its sequences' lengths (int32 [n]).
     plan: int32, 2 (n + 1) + total_tokens // 64 + n elements. n_seqs is needed with raw addresses."""
     n = int(lengths.numel() if n_seqs is None else n_seqs)
-    raw = isinstance(lengths, int) or isinstance(plan, int)
-    i32 = None if raw else _i32()
-    args = (_addr(lengths, "lengths", i32, n),
-            _addr(plan, "plan", i32, 2 * (n + 1) + int(total_tokens) // 64 + n))
-    _on_device((lengths, plan), stream, lambda s: _check(
-        _lib.ssm_scan_plan(args[0], n, int(total_tokens), args[1], s)))
+    total = int(total_tokens)
+    a = _addr(lengths, "lengths", _I32_T, n)
+    b = _addr(plan, "plan", _I32_T, 2 * (n + 1) + total // 64 + n)
+    _on_device((lengths, plan), stream,
+               lambda s: _check(_lib.ssm_scan_plan(a, n, total, b, s)))
 
 
-def _packed(d: Dims, total_tokens: int, plan, q, k, v, decay, beta):
+def _packed(d: Dims, total: int, plan, q, k, v, decay, beta):
     """Addresses of a packed batch's arrays."""
-    rows = int(total_tokens) * d.heads
-    gate = rows * (d.d_k if d.rule == KDA else 1)
-    tin, f32 = _types(d, (plan, q, k, v, decay, beta))
-    i32 = None if tin is None else _i32()
-    return (_addr(plan, "plan", i32, scan_sizes(d, total_tokens)[0]),
+    rows, n, tin = total * d.heads, d.batch, _IN_T.get(d.in_dtype)
+    return (_addr(plan, "plan", _I32_T, 2 * (n + 1) + total // 64 + n),
             _addr(q, "q", tin, rows * d.d_k), _addr(k, "k", tin, rows * d.d_k),
-            _addr(v, "v", tin, rows * d.d_v), _addr(decay, "decay", f32, gate),
-            _addr(beta, "beta", f32, rows))
+            _addr(v, "v", tin, rows * d.d_v),
+            _addr(decay, "decay", _F32_T, rows * d.d_k if d.rule == KDA else rows),
+            _addr(beta, "beta", _F32_T, rows))
 
 
-def _scan_workspace(workspace, nbytes: int, args, stream):
-    """A workspace of nbytes: the caller's, or one of its own from PyTorch."""
-    import torch
+def _scan_workspace(workspace, d: Dims, total: int, which: int, args, stream):
+    """A workspace and its bytes: the caller's, or one of the size needed from PyTorch."""
     if isinstance(workspace, int):
         raise ValueError("workspace: expected a device tensor or None")
     if workspace is not None:
         _addr(workspace, "workspace")
-        have = workspace.numel() * workspace.element_size()
-        return workspace, have
+        return workspace, workspace.numel() * workspace.element_size()
     dev = next((a.device for a in args if a is not None and not isinstance(a, int)), None)
     if dev is None:
         raise ValueError("workspace: raw addresses need a workspace tensor")
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if stream is not None and nbytes:  # used there, allocated on the current stream
-        ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=dev)
+    need = ctypes.c_int64()
+    out = (None, ctypes.byref(need), None) if which == 1 else (None, None, ctypes.byref(need))
+    _check(_lib.ssm_scan_sizes(ctypes.byref(d), total, *out))
+    ws = _torch.empty(need.value, dtype=_torch.uint8, device=dev)
+    if stream is not None and need.value:  # used there, allocated on the current stream
+        ws.record_stream(_torch.cuda.ExternalStream(stream, device=dev)
                          if isinstance(stream, int) else stream)
-    return ws, nbytes
+    return ws, need.value
 
 
 def scan_forward(d: Dims, total_tokens: int, plan, q, k, v, decay, beta, state, y, *,
@@ -618,18 +627,15 @@ def scan_forward(d: Dims, total_tokens: int, plan, q, k, v, decay, beta, state, 
     [total_tokens][H][d_v] and the final states [num_slots][H][d_k][d_v] (num_slots defaults to
     d.batch), from state_in (None: zero; may be `state` itself). workspace: a device tensor of
     scan_sizes(...)[1] bytes, or None to take one from PyTorch for the call."""
-    ns = d.batch if num_slots is None else int(num_slots)
-    args = (plan, q, k, v, decay, beta, state, y, state_in, slot)
-    packed = _packed(d, total_tokens, plan, q, k, v, decay, beta)
-    f32 = None if all(a is None or isinstance(a, int) for a in args) else _f32()
+    total, ns = int(total_tokens), d.batch if num_slots is None else int(num_slots)
+    p = _packed(d, total, plan, q, k, v, decay, beta)
     states = ns * d.heads * d.d_k * d.d_v
-    at = (_addr(slot, "slot", None if f32 is None else _i32(), d.batch),
-          _addr(state_in, "state_in", f32, states), *packed[1:],
-          _addr(state, "state", f32, states),
-          _addr(y, "y", f32, int(total_tokens) * d.heads * d.d_v))
-    ws, have = _scan_workspace(workspace, scan_sizes(d, total_tokens)[1], args, stream)
+    a = (_addr(slot, "slot", _I32_T, d.batch), _addr(state_in, "state_in", _F32_T, states))
+    b = (_addr(state, "state", _F32_T, states), _addr(y, "y", _F32_T, total * d.heads * d.d_v))
+    args = (plan, q, k, v, decay, beta, state, y, state_in, slot)
+    ws, have = _scan_workspace(workspace, d, total, 1, args, stream)
     _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_scan_forward(
-        ctypes.byref(d), int(total_tokens), packed[0], ns, *at, ws.data_ptr(), have, s)))
+        ctypes.byref(d), total, p[0], ns, *a, *p[1:], *b, ws.data_ptr(), have, s)))
 
 
 def scan_backward(d: Dims, total_tokens: int, plan, q, k, v, decay, beta, dy, dq, dk, dv,
@@ -637,28 +643,29 @@ def scan_backward(d: Dims, total_tokens: int, plan, q, k, v, decay, beta, dy, dq
                   workspace=None, stream=None) -> None:
     """ssm_scan_backward: the gradients of scan_forward (dlog_decay is decay * dL/d(decay)).
     workspace: a device tensor of scan_sizes(...)[2] bytes, or None."""
+    total = int(total_tokens)
+    p = _packed(d, total, plan, q, k, v, decay, beta)
+    rows, tin = total * d.heads, _IN_T.get(d.in_dtype)
+    states = d.batch * d.heads * d.d_k * d.d_v
+    s0 = _addr(state_in, "state_in", _F32_T, states)
+    b = (_addr(dy, "dy", _F32_T, rows * d.d_v), _addr(dstate, "dstate", _F32_T, states),
+         _addr(dq, "dq", tin, rows * d.d_k), _addr(dk, "dk", tin, rows * d.d_k),
+         _addr(dv, "dv", tin, rows * d.d_v),
+         _addr(dlog_decay, "dlog_decay", _F32_T, rows * d.d_k if d.rule == KDA else rows),
+         _addr(dbeta, "dbeta", _F32_T, rows), _addr(dstate_in, "dstate_in", _F32_T, states))
     args = (plan, q, k, v, decay, beta, dy, dq, dk, dv, dlog_decay, dbeta, state_in, dstate,
             dstate_in)
-    packed = _packed(d, total_tokens, plan, q, k, v, decay, beta)
-    tin, f32 = _types(d, args)
-    rows = int(total_tokens) * d.heads
-    states = d.batch * d.heads * d.d_k * d.d_v
-    at = (_addr(dy, "dy", f32, rows * d.d_v), _addr(dstate, "dstate", f32, states),
-          _addr(dq, "dq", tin, rows * d.d_k), _addr(dk, "dk", tin, rows * d.d_k),
-          _addr(dv, "dv", tin, rows * d.d_v),
-          _addr(dlog_decay, "dlog_decay", f32, rows * (d.d_k if d.rule == KDA else 1)),
-          _addr(dbeta, "dbeta", f32, rows), _addr(dstate_in, "dstate_in", f32, states))
-    ws, have = _scan_workspace(workspace, scan_sizes(d, total_tokens)[2], args, stream)
+    ws, have = _scan_workspace(workspace, d, total, 2, args, stream)
     _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_scan_backward(
-        ctypes.byref(d), int(total_tokens), packed[0],
-        _addr(state_in, "state_in", f32, states), *packed[1:], *at, ws.data_ptr(), have, s)))
+        ctypes.byref(d), total, p[0], s0, *p[1:], *b, ws.data_ptr(), have, s)))
 
 
 def window_plan(d: Dims, lengths, tau, parity, update_rows, n_update, stream=None) -> None:
     """ssm_window_plan: tau, parity, update_rows (int32 [d.batch] each) and n_update (one int32)
     of a serving step from the tokens each row has decoded (int32 [d.batch], negative: padding)."""
-    args = (lengths, tau, parity, update_rows, n_update)
-    i32 = None if all(isinstance(a, int) or a is None for a in args) else _i32()
-    names = ("lengths", "tau", "parity", "update_rows", "n_update")
-    at = [_addr(a, x, i32, 1 if x == "n_update" else d.batch) for a, x in zip(args, names)]
-    _on_device(args, stream, lambda s: _check(_lib.ssm_window_plan(ctypes.byref(d), *at, s)))
+    n = d.batch
+    a = (_addr(lengths, "lengths", _I32_T, n), _addr(tau, "tau", _I32_T, n),
+         _addr(parity, "parity", _I32_T, n), _addr(update_rows, "update_rows", _I32_T, n),
+         _addr(n_update, "n_update", _I32_T, 1))
+    _on_device((lengths, tau, parity, update_rows, n_update), stream,
+               lambda s: _check(_lib.ssm_window_plan(ctypes.byref(d), *a, s)))

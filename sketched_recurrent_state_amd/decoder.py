@@ -21,9 +21,22 @@ from typing import Optional
 import torch
 
 from . import (Dims, IN_BF16, KDA, MAMBA2, SKETCH_BF16, buffer_append, full_read_decode_step,
-               rank_offsets, recurrent_decode_step, sketch_decode_step, sketch_decode_step_ls,
-               sketch_decode_step_ranked, window_update_refresh, window_update_refresh_ls,
+               rank_offsets, recurrent_decode_step, scan_forward, scan_plan, scan_sizes,
+               sketch_decode_step, sketch_decode_step_ls, sketch_decode_step_ranked,
+               window_update_refresh, window_update_refresh_ls,
                window_update_refresh_ranked)
+
+
+def _prefill(d: Dims, state: torch.Tensor, lengths, q, k, v, decay, beta) -> torch.Tensor:
+    """A packed batch of d.batch prompts (lengths [N]; token arrays [sum][H][..]) through the
+    recurrence, from `state` and into it; returns y [sum][H][d_v]."""
+    total = q.shape[0]
+    lengths = torch.as_tensor(lengths, dtype=torch.int32, device=state.device)
+    plan = torch.empty(scan_sizes(d, total)[0], dtype=torch.int32, device=state.device)
+    scan_plan(lengths, total, plan)
+    y = torch.empty((total, d.heads, d.d_v), device=state.device, dtype=torch.float32)
+    scan_forward(d, total, plan, q, k, v, decay, beta, state, y, state_in=state)
+    return y
 
 
 class WindowedDecoder:
@@ -114,6 +127,17 @@ class WindowedDecoder:
         self._update(self.tau)
         self.tau = 0
 
+    # -- prompts -----------------------------------------------------------------
+    def prefill(self, lengths, q, k, v, decay, beta=None) -> torch.Tensor:
+        """Take a packed batch of prompts (lengths [N], zero for a sequence with no new tokens;
+        token arrays [sum of lengths][H][..]) into the state and refresh the sketch; returns the
+        outputs [sum of lengths][H][d_v]. Tokens still in the window are written first."""
+        if self.tau:
+            self.flush()
+        y = _prefill(self.d, self.state, lengths, q, k, v, decay, beta)
+        self.refresh()
+        return y
+
     # -- one decode step -----------------------------------------------------------
     def step(self, q, k, v, decay, beta=None, *, y=None, y_full=None):
         """Read the output for the current token; returns y (or (y, y_full) for read="both")."""
@@ -158,3 +182,7 @@ class RecurrentDecoder:
             y = torch.empty((d.batch, d.heads, d.d_v), device=q.device, dtype=torch.float32)
         recurrent_decode_step(d, self.state, q, k, v, decay, beta, y)
         return y
+
+    def prefill(self, lengths, q, k, v, decay, beta=None) -> torch.Tensor:
+        """Take a packed batch of prompts into the state; returns their outputs."""
+        return _prefill(self.d, self.state, lengths, q, k, v, decay, beta)

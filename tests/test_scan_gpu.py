@@ -435,3 +435,69 @@ def test_prefill_then_serving_steps(rule):
         if prompts[i]:
             near(y0.double().cpu().numpy()[s], want[:prompts[i]], (dk + 48) * U, f"prompt {i}")
         near(np.stack([y[i] for y in ys]), want[prompts[i]:], 4 * (dk + 48) * U, f"decode of row {i}")
+
+
+@pytest.mark.parametrize("rule", RULES)
+def test_decoders_prefill(rule):
+    """WindowedDecoder and RecurrentDecoder from a prompt on: prefill (twice, the second time with
+    tokens in the window), then steps, against the recurrence over the whole streams. The window
+    sums its tokens apart from the state: 4 (d_k + 48) u as for the serving steps."""
+    from sketched_recurrent_state_amd.decoder import RecurrentDecoder, WindowedDecoder
+    n, H, dk, dv, W = 2, 3, 16, 32, 4
+    first = Batch(rule, "f32", [21, 40], H, dk, dv)
+    second = Batch(rule, "f32", [0, 17], H, dk, dv, seed=5)
+    toks = [Batch(rule, "f32", [1] * n, H, dk, dv, seed=10 + t) for t in range(9)]
+    d = ssm.Dims.make(rule, "f32", n, H, dk, dv, W, dk)
+    rng = np.random.default_rng(2)
+    basis = dev_f32(np.stack([np.linalg.qr(rng.standard_normal((dk, dk)))[0].T for _ in range(H)]))
+    names = ("q", "k", "v", "decay", "beta")
+    for dec in (WindowedDecoder(d, first.t["state_in"].clone(), basis),
+                WindowedDecoder(d, first.t["state_in"].clone(), read="full"),
+                RecurrentDecoder(d, first.t["state_in"].clone())):
+        one = lambda t: dec.step(*[t.t[x] for x in names]).double().cpu().numpy()
+        ya = dec.prefill(first.lens, *[first.t[x] for x in names]).double().cpu().numpy()
+        got = [one(t) for t in toks[:3]]
+        yb = dec.prefill(torch.tensor(second.lens), *[second.t[x] for x in names]).double().cpu().numpy()
+        got += [one(t) for t in toks[3:]]
+        at = [s for _, s in first.parts()], [s for _, s in second.parts()]
+        for i in range(n):
+            *a, S = first.seq(i, at[0][i])
+            b = second.seq(i, at[1][i])
+            x = [None if u is None else np.concatenate(
+                [u] + [t.host(m)[i:i + 1] for t in toks[:3]] + [w] + [t.host(m)[i:i + 1] for t in toks[3:]])
+                for u, w, m in zip(a, b, names)]
+            want, _ = ref.forward(*x, S)
+            p = first.lens[i]
+            e = p + 3 + second.lens[i]
+            near(ya[at[0][i]], want[:p], (dk + 48) * U, "first prompt")
+            if second.lens[i]:
+                near(yb[at[1][i]], want[p + 3:e], 4 * (dk + 48) * U, "second prompt")
+            near(np.stack([g[i] for g in got]), np.concatenate([want[p:p + 3], want[e:]]),
+                 4 * (dk + 48) * U, "steps")
+
+
+SIZES = [(1, 2, 128, 128), (1, 40, 128, 128), (1, 80, 128, 64), (3, 150, 64, 128), (2, 400, 32, 16)]
+
+
+@pytest.mark.parametrize("n,H,dk,dv", SIZES, ids=str)
+@pytest.mark.parametrize("rule", RULES)
+def test_every_shape_of_the_passes(rule, n, H, dk, dv):
+    """Few units (rows divided over 4 or 2 waves) and many (a wave a column block), on a sample of
+    heads, with the same bits from run to run."""
+    for dtype in ("bf16", "f32"):
+        b = Batch(rule, dtype, [70 + 13 * i for i in range(n)], H, dk, dv, spare=2)
+        y, state = b.forward()
+        o = b.backward()
+        for _ in range(3):
+            torch.empty(1 << 28, dtype=torch.uint8, device="cuda").fill_(255)  # NaN in new workspaces
+            y2, state2 = b.forward()
+            o2 = b.backward()
+            assert torch.equal(y, y2) and torch.equal(state, state2)
+            assert all(o[x] is None or torch.equal(o[x], o2[x]) for x in o)
+        heads = [0, H // 2, H - 1]
+        few = Batch.__new__(Batch)
+        few.__dict__.update(b.__dict__, H=len(heads))
+        pick = lambda x, dim: None if x is None else x.index_select(dim, torch.tensor(heads, device="cuda"))
+        few.t = {x: pick(t, 1) for x, t in b.t.items()}
+        check_forward(few, pick(y, 1), pick(state, 1))
+        check_backward(few, {x: pick(t, 1) for x, t in o.items()})
