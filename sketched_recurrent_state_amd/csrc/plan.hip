@@ -19,26 +19,44 @@ constexpr int PW = PT / 64;
 
 // Exclusive sum over the workgroup's threads; `total` is the sum of all. sw: PW values.
 template <typename I>
-__device__ __forceinline__ I block_exclusive(I x, I* sw, I& total) {
+__device__ __forceinline__ I wave_inclusive(I x, int lanes) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < lanes; o <<= 1) {
+    const I y = __shfl_up(x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+template <typename I>
+__device__ __forceinline__ I before_wave(const I* sw, I& total) {  // the waves' sums, by every wave
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  I s = x;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const I y = __shfl_up(s, o);
-    if (lane >= o) s += y;
-  }
+  const I w = wave_inclusive(lane < PW ? sw[lane] : I(0), PW);
+  total = __shfl(w, PW - 1);
+  const I before = __shfl(w, wave > 0 ? wave - 1 : 0);
+  return wave > 0 ? before : I(0);
+}
+template <typename I>
+__device__ __forceinline__ I block_exclusive(I x, I* sw, I& total) {
+  const I s = wave_inclusive(x, 64);
   __syncthreads();  // the last call's reads of sw are done
-  if (lane == 63) sw[wave] = s;
+  if ((threadIdx.x & 63) == 63) sw[threadIdx.x >> 6] = s;
   __syncthreads();
-  I before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < PW; ++w) {
-    const I y = sw[w];
-    if (w < wave) before += y;
-    total += y;
+  return before_wave(sw, total) + s - x;
+}
+// The same for two values at once.
+__device__ __forceinline__ void block_exclusive(int64_t& t, int& c, int64_t* sw64, int* sw32,
+                                                int64_t& all_t, int& all_c) {
+  const int64_t st = wave_inclusive(t, 64);
+  const int sc = wave_inclusive(c, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) {
+    sw64[threadIdx.x >> 6] = st;
+    sw32[threadIdx.x >> 6] = sc;
   }
-  return before + s - x;
+  __syncthreads();
+  t = before_wave(sw64, all_t) + st - t;
+  c = before_wave(sw32, all_c) + sc - c;
 }
 
 constexpr int PS = 4;            // sequences of a thread
@@ -58,35 +76,44 @@ scan_plan_kernel(const int32_t* __restrict__ lengths, int n, int total, int cap,
   owner[tid] = -1;
   int64_t tokens = 0;  // of the tiles before
   int chunks = 0;
-  for (int t0 = 0, tile = 0; t0 < n; t0 += TILE, ++tile) {
-    int64_t len[PS], sum = 0;
+  const int grid = gridDim.x, tiles = (n + TILE - 1) / TILE;
+  for (int tile = 0; tile < tiles; ++tile) {
+    // done: the table's part is full, and no tile's starts are left to write
+    const int left = tiles - 1 - (int)blockIdx.x;
+    if (chunks >= e0 + PT && (left < 0 || tile > (int)blockIdx.x + left / grid * grid)) break;
+    const int s0 = tile * TILE + tid * PS;
+    int len[PS];
+    int64_t sum = 0;
+    int mine = 0;
 #pragma unroll
     for (int i = 0; i < PS; ++i) {
-      const int s = t0 + tid * PS + i;
-      const int l = s < n ? lengths[s] : 0;
+      const int l = s0 + i < n ? lengths[s0 + i] : 0;
       len[i] = l > 0 ? l : 0;
       sum += len[i];
+      mine += (int)(((int64_t)len[i] + CT - 1) / CT);
     }
-    int64_t all;
-    int64_t at = tokens + block_exclusive(sum, sw64, all);
+    int64_t at = sum, all;
+    int c = mine, all_chunks;
+    block_exclusive(at, c, sw64, sw32, all, all_chunks);
+    at += tokens;
     tokens += all;
     // lengths past the arrays' end are cut
-    int start[PS], nc[PS], mine = 0;
+    int start[PS], nc[PS], kept = 0;
 #pragma unroll
     for (int i = 0; i < PS; ++i) {
       const int64_t end = at + len[i];
       start[i] = (int)(at < total ? at : total);
       nc[i] = ((int)(end < total ? end : total) - start[i] + CT - 1) / CT;
-      mine += nc[i];
+      kept += nc[i];
       at = end;
     }
-    int all_chunks;
-    int c = chunks + block_exclusive(mine, sw32, all_chunks);
+    if (tokens > total) c = block_exclusive(kept, sw32, all_chunks);
+    c += chunks;
     chunks += all_chunks;
-    const bool writes = tile % (int)gridDim.x == (int)blockIdx.x;
+    const bool writes = tile % grid == (int)blockIdx.x;
 #pragma unroll
     for (int i = 0; i < PS; ++i) {
-      const int s = t0 + tid * PS + i;
+      const int s = s0 + i;
       if (s >= n) break;
       if (writes) {
         seq_start[s] = start[i];
