@@ -156,6 +156,19 @@ def test_scan_plan(n, total):
     assert buf[0] == -9 and (buf[-5:] == -9).all()
 
 
+def test_scan_plan_of_the_longest_arrays():
+    total = 2 ** 31 - 1
+    lens = torch.tensor([total - 100, total], dtype=torch.int32, device="cuda")
+    plan = torch.empty(6 + total // 64 + 2, dtype=torch.int32, device="cuda")
+    ssm.scan_plan(lens, total, plan)
+    first = (total - 100 + 63) // 64
+    assert plan[:6].tolist() == [0, total - 100, total, 0, first, first + 2]
+    assert (plan[6:6 + first] == 0).all() and plan[6 + first:].tolist() == [1, 1] + [-1] * (total // 64 - first)
+    one = plan[:4 + total // 64 + 1]
+    ssm.scan_plan(lens[1:], total, one)
+    assert one[:4].tolist() == [0, total, 0, total // 64 + 1] and (one[4:] == 0).all()
+
+
 @pytest.mark.parametrize("n", [1, 7, 1024, 4096, 4099, 50001])
 @pytest.mark.parametrize("W", [1, 2, 7, 8, 15, 16])
 def test_window_plan(n, W):
