@@ -346,10 +346,12 @@ ssm_status ssm_recurrent_decode_step(const ssm_dims* d,
  * has skips its chunk or sequence). Gates are meant to be in [0, 1]; 0 and 1 are exact.
  * Scalar decays, beta, their gradients and the plan need 4-byte alignment only.
  * A non-finite value of a token may reach outputs of its own sequence up to 15
- * tokens before it (tokens are taken 16 at a time), never another sequence or head.
+ * tokens before it (tokens are taken 16 at a time), in the backward pass any gradient of
+ * its own sequence; never another sequence or head. An infinity may come out as NaN.
  * Sums and states are fp32. d->window and d->rank are checked but not used.
- * heads <= 65536; (total_tokens/64 + batch)*heads < 2^22. Results do not depend on the batch's
- * other sequences and are the same bits from run to run.
+ * heads <= 65536; (total_tokens/64 + batch)*heads < 2^22. Results are the same bits from run
+ * to run. A sequence's depend on the rest of the batch only by rounding: batch*heads chooses
+ * how a sum over d_k is divided.
  */
 
 /* Sizes for a packed batch: int32 elements of the plan, and the bytes of the

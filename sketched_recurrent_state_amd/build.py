@@ -34,6 +34,9 @@ FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
     # packed fp32 (v_pk_*_f32) stays off in every kernel
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    # the scan asks for registers of two waves a SIMD also where LDS holds fewer (fp32, KDA):
+    # with all registers the fp32 passes were 2 to 5 % slower
+    "-Wno-pass-failed",
     "-I", INCLUDE, "-I", CSRC,
 ]
 

@@ -1,6 +1,11 @@
 // scan_prep.hpp -- what a block of 16 tokens needs before the state is known: the
 // decayed products K and P, the inverse of the unit lower triangular I + K diag(b),
 // and the gate products (notation in scan.hpp). One wave per block, all blocks at once.
+//
+// KDA also writes three decayed copies of its keys and queries in fp32 (the passes would
+// otherwise decay them once for each column block): 107 us for 262,144 token rows of 128, which
+// is 6.7 TB/s. With scalar gates the 16 dependent steps of the substitution take most of the
+// time: 40 us for as many rows (GDN, bf16).
 #pragma once
 
 #include "scan.hpp"
