@@ -8,8 +8,11 @@
 //   dk_a reader = -F_a I_a (dr_a S) + sum_{b <= a} (dK_ab G_ab) k_b
 //   dk_b writer = B_b O_b (w_b G) + sum_{a >= b} (dP_ab G_ab)^T q_a + (dK_ab G_ab)^T k_a
 // so S and G are read and split once a chunk and never carried from block to block. A scalar
-// gate's G_ab goes into dP and dK; KDA's, one for each channel, is applied to the keys (within
-// a block), to the sums (across blocks) and term by term (on the diagonal). And
+// gate's G_ab goes into dP and dK. KDA's, one for each channel, goes into the keys and queries:
+// a product over the gates between two tokens is taken in two factors that meet at the boundary
+// between their blocks, halves of a block or runs of four tokens, and term by term within a run,
+// so that all but the last are matrix products (2 x 4096 tokens x 32 heads of 128 x 128, bf16:
+// 2,412 -> 564 us against the whole 16-token diagonal term by term). And
 //   rowsum(S_end * G) = F rowsum(S * G) + sum_j k_j (state part of the writer's dk_j)
 // starts the sums of the gates' gradients without the state at the chunk's end.
 //
@@ -18,8 +21,7 @@
 // waves. The 20 tiles of dP and dK are dealt over the waves.
 //
 // Bound by HBM, nearly: a GDN cell of 128 x 128 reads 128 KB of S and G, 96 KB of dy, r and e and
-// writes 33 KB, 1.2 GB for 4,096 cells (2 x 4096 tokens x 32 heads), in 268 us. Carrying S and G
-// from block to block instead, a wave a column block, took 475 us.
+// writes 33 KB, 1.2 GB for 4,096 cells (2 x 4096 tokens x 32 heads), in 268 us.
 #pragma once
 
 #include "scan.hpp"
@@ -424,135 +426,141 @@ scan_grads_kernel(const ScanArgs a) {
       if (lane < count) a.dlog[base + (size_t)lane * H] = last + s;
     }
   } else {
+    static_assert(!CH || TD == 1, "a channel tile a wave");
     const float* diagP = reinterpret_cast<const float*>(rows + DIAG);
     const float* diagK = diagP + NB * SB * LP;
-    // a block's rows of the workspace's decayed keys and queries, split
-    auto decayed = [&](const float* p, int blk, int u) {
-      f32x4 x;
+    // Rows 4g + i of every block, and their gates in runs of four tokens: the run's decay into
+    // token i (in4) and out of it (out4), of runs 1 and 2 (w1, w2), and of the runs before and
+    // after this lane's.
+    f32x4 kx[NB], qx[NB], ax[NB], in4[NB], out4[NB];
+    float w1[NB], w2[NB], pre[NB], post[NB], blocks[NB];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[i] = p[(cell * CT + SB * blk + 4 * g + i) * DK + d0 + 16 * u];
-      return split4(x);
-    };
-    float carry[TD];
+    for (int x = 0; x < NB; ++x) {
+      kx[x] = load_rows(k, x, 0);
+      qx[x] = load_rows(q, x, 0);
 #pragma unroll
-    for (int u = 0; u < TD; ++u) {
-      float blocks[NB];
+      for (int i = 0; i < 4; ++i) {
+        const int t = SB * x + 4 * g + i;
+        const float gate = a.decay[(base + (size_t)min(t, count - 1) * H) * DK + d0];
+        ax[x][i] = t < count ? gate : 1.f;
+      }
+    }
 #pragma unroll
-      for (int c = 0; c < NB; ++c)
-        blocks[c] = c < nb ? a.w.all[(cell * NB + c) * DK + d0 + 16 * u] : 1.f;
-      // across blocks, from the ends of the writers' blocks to the starts of the readers'
+    for (int x = 0; x < NB; ++x) {
+      in4[x][0] = ax[x][0];
+      out4[x][3] = 1.f;
 #pragma unroll
-      for (int x = 0; x < NB; ++x) {
-        if (x >= nb) break;
-        __builtin_amdgcn_sched_barrier(0);
-        f32x4 sq = {0.f, 0.f, 0.f, 0.f}, sk = sq;
-        float before = 1.f;
+      for (int i = 1; i < 4; ++i) {
+        in4[x][i] = in4[x][i - 1] * ax[x][i];
+        out4[x][3 - i] = out4[x][4 - i] * ax[x][4 - i];
+      }
+      const float w = in4[x][3], w0 = __shfl(w, m), w3 = __shfl(w, m + 48);
+      w1[x] = __shfl(w, m + 16);
+      w2[x] = __shfl(w, m + 32);
+      pre[x] = (g > 0 ? w0 : 1.f) * (g > 1 ? w1[x] : 1.f) * (g > 2 ? w2[x] : 1.f);
+      post[x] = (g < 3 ? w3 : 1.f) * (g < 2 ? w2[x] : 1.f) * (g < 1 ? w1[x] : 1.f);
+      blocks[x] = w0 * w1[x] * w2[x] * w3;
+    }
+    float after = 1.f;
 #pragma unroll
-        for (int y = 0; y < x; ++y) {
-          const Split4 t = decayed(a.w.kt, y, u);
-          sq = mfma_split(tile_rows(x * (x + 1) / 2 + y), t, sq * blocks[y]);
-          sk = mfma_split(tile_rows(PAIRS + x * (x + 1) / 2 + y), t, sk * blocks[y]);
-          before *= blocks[y];
-        }
+    for (int x = 0; x < NB; ++x) end[0] *= blocks[x];
+#pragma unroll
+    for (int x = NB - 1; x >= 0; --x) {  // end: rowsum(S_end * G), the last token's sum
+      if (x < nb) {
         const f32x4 beta = *reinterpret_cast<const f32x4*>(row + ROW * x + 2 * SB + 4 * g);
-        dq[x][u] = dq[x][u] * before + sq;
-        dkr[x][u] = sk - dkr[x][u] * beta * before;
+        dkr[x][0] *= -beta;
+        dkw[x][0] *= beta;
+        const f32x4 out = out4[x] * (post[x] * after);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) end[0] += dkw[x][0][i] * out[i] * kx[x][i];
       }
-      float all = 1.f;
+      after *= blocks[x];
+    }
+    // across blocks, from the ends of the writers' blocks to the starts of the readers'
 #pragma unroll
-      for (int c = 0; c < NB; ++c) all *= blocks[c];
-      end[u] *= all;
+    for (int y = 0; y < NB - 1; ++y) {
+      const Split4 t = split4(kx[y] * (out4[y] * post[y]));
 #pragma unroll
-      for (int y = NB - 1; y >= 0; --y) {
-        if (y >= nb) continue;
-        __builtin_amdgcn_sched_barrier(0);
-        const f32x4 beta = *reinterpret_cast<const f32x4*>(row + ROW * y + 2 * SB + 4 * g);
-        f32x4 s = {0.f, 0.f, 0.f, 0.f};
-        float after = 1.f;
-#pragma unroll
-        for (int x = NB - 1; x > y; --x) {
-          if (x >= nb) continue;
-          s = mfma_split(tile_cols(x * (x + 1) / 2 + y), decayed(a.w.qh, x, u), s * blocks[x]);
-          s = mfma_split(tile_cols(PAIRS + x * (x + 1) / 2 + y), decayed(a.w.kh, x, u), s);
-          after *= blocks[x];
-        }
-        dkw[y][u] *= beta * after;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)  // still without O_j: the workspace's O k has it
-          end[u] += dkw[y][u][i] * a.w.kt[(cell * CT + SB * y + 4 * g + i) * DK + d0 + 16 * u];
-        dkw[y][u] += s;
+      for (int x = y + 1; x < NB; ++x) {
+        if (x >= nb) continue;
+        dq[x][0] = mfma_split(tile_rows(x * (x + 1) / 2 + y), t, dq[x][0] * blocks[y]);
+        dkr[x][0] = mfma_split(tile_rows(PAIRS + x * (x + 1) / 2 + y), t, dkr[x][0] * blocks[y]);
       }
-      carry[u] = xsum32(xsum16(end[u]));
-      // within a block, its gates one by one, from the last block to the first
+    }
 #pragma unroll
-      for (int blk = NB - 1; blk >= 0; --blk) {
-        if (blk >= nb) continue;
-        __builtin_amdgcn_sched_barrier(0);  // one block's 48 values at a time
-        float qc[SB], kc[SB], ac[SB];
+    for (int x = NB - 1; x > 0; --x) {
+      if (x >= nb) continue;
+      const f32x4 in = in4[x] * pre[x];
+      const Split4 tq = split4(qx[x] * in), tk = split4(kx[x] * in);
 #pragma unroll
-        for (int l = 0; l < SB; ++l) {
-          const int t = SB * blk + l;
-          const size_t at = (base + (size_t)min(t, count - 1) * H) * DK + d0 + 16 * u;
-          const float gate = a.decay[at];
-          qc[l] = to_f32(masked(q[at], row_mask(t < count)));
-          kc[l] = to_f32(masked(k[at], row_mask(t < count)));
-          ac[l] = t < count ? gate : 1.f;
-        }
-        f32x4 in, out, qr, kr;
+      for (int y = 0; y < x; ++y) {
+        dkw[y][0] = mfma_split(tile_cols(x * (x + 1) / 2 + y), tq, dkw[y][0] * blocks[x]);
+        dkw[y][0] = mfma_split(tile_cols(PAIRS + x * (x + 1) / 2 + y), tk, dkw[y][0]);
+      }
+    }
+    // within a block, from the last block to the first: between its halves, between the runs of
+    // a half (tiles with all else masked), and within the lane's run term by term
+    const int run = m >> 2;
+    const uint32_t half = row_mask(run >= 2 && g < 2), runs = row_mask((run & 1) && g == run - 1);
+    const uint32_t halfT = row_mask(run < 2 && g >= 2), runsT = row_mask(!(run & 1) && g == run + 1);
+    auto only = [](const Split4& t, uint32_t mask) {
+      return Split4{make_uint2(t.h.x & mask, t.h.y & mask), make_uint2(t.m.x & mask, t.m.y & mask),
+                    make_uint2(t.l.x & mask, t.l.y & mask)};
+    };
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    float carry = xsum32(xsum16(end[0]));
+#pragma unroll
+    for (int x = NB - 1; x >= 0; --x) {
+      if (x >= nb) continue;
+      const int n = x * (x + 1) / 2 + x;
+      const float far1 = g == 0 ? w1[x] : 1.f, far2 = g == 3 ? w2[x] : 1.f;
+      const f32x4 kw = kx[x] * out4[x], qr = qx[x] * in4[x], kr = kx[x] * in4[x];
+      const Split4 kw4 = split4(kw), kw8 = split4(kw * far1);
+      const Split4 qr4 = split4(qr), qr8 = split4(qr * far2);
+      const Split4 kr4 = split4(kr), kr8 = split4(kr * far2);
+      const Split4 P = tile_rows(n), K = tile_rows(PAIRS + n), Pt = tile_cols(n), Kt = tile_cols(PAIRS + n);
+      f32x4 xq = dq[x][0] * pre[x], xr = dkr[x][0] * pre[x], xw = dkw[x][0] * post[x];
+      xq += mfma_split(only(P, runs), kw4, mfma_split(only(P, half), kw8, none) * far2);
+      xr += mfma_split(only(K, runs), kw4, mfma_split(only(K, half), kw8, none) * far2);
+      const f32x4 w = mfma_split(only(Kt, halfT), kr8, mfma_split(only(Pt, halfT), qr8, none)) * far1;
+      xw += mfma_split(only(Kt, runsT), kr4, mfma_split(only(Pt, runsT), qr4, w));
+      xq *= in4[x];
+      xr *= in4[x];
+      xw *= out4[x];
+      f32x4 dP[4], dK[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dP[i] = *reinterpret_cast<const f32x4*>(diagP + (x * SB + 4 * g + i) * LP + 4 * g);
+        dK[i] = *reinterpret_cast<const f32x4*>(diagK + (x * SB + 4 * g + i) * LP + 4 * g);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
         float p = 1.f;
 #pragma unroll
-        for (int l = 0; l < SB; ++l) {
-          p *= ac[l];
-          if (l >> 2 == g) {
-            in[l & 3] = p;
-            qr[l & 3] = qc[l];
-            kr[l & 3] = kc[l];
+        for (int i = j; i < 4; ++i) {
+          if (i > j) p *= ax[x][i];
+          const float t = p * kx[x][j];
+          xq[i] += dP[i][j] * t;
+          float s = dP[i][j] * qx[x][i];
+          if (i > j) {
+            xr[i] += dK[i][j] * t;
+            s += dK[i][j] * kx[x][i];
           }
+          xw[j] += p * s;
         }
-        p = 1.f;
-#pragma unroll
-        for (int l = SB - 1; l >= 0; --l) {
-          if (l >> 2 == g) out[l & 3] = p;
-          p *= ac[l];
-        }
-        f32x4 xq = dq[blk][u] * in, xr = dkr[blk][u] * in, xw = dkw[blk][u] * out;
-        const float* dP = diagP + blk * SB * LP;
-        const float* dK = diagK + blk * SB * LP;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 4 * g + i;
-          __builtin_amdgcn_sched_barrier(0);
-          p = 1.f;
-#pragma unroll
-          for (int j = SB - 1; j >= 0; --j) {  // keys r, r - 1, .. decayed on the way
-            const float t = j <= r ? p * kc[j] : 0.f;
-            xq[i] += dP[r * LP + j] * t;
-            xr[i] += dK[r * LP + j] * t;
-            if (j <= r) p *= ac[j];
-          }
-          __builtin_amdgcn_sched_barrier(0);
-          p = 1.f;
-#pragma unroll
-          for (int j = 0; j < SB; ++j) {  // readers r, r + 1, ..
-            if (j > r) p *= ac[j];
-            const float t = dP[j * LP + r] * qc[j] + dK[j * LP + r] * kc[j];
-            xw[i] += j >= r ? p * t : 0.f;
-          }
-        }
-        store(a.dq, blk, u, xq);
-        store(a.dk, blk, u, xr + xw);
-        f32x4 s = qr * xq + kr * (xr - xw);
-#pragma unroll
-        for (int i = 2; i >= 0; --i) s[i] += s[i + 1];
-        float after, total;
-        above(s[0], lane, g, after, total);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (SB * blk + 4 * g + i < count)
-            a.dlog[(base + (size_t)(SB * blk + 4 * g + i) * H) * DK + d0 + 16 * u] = carry[u] + after + s[i];
-        carry[u] += total;
       }
+      store(a.dq, x, 0, xq);
+      store(a.dk, x, 0, xr + xw);
+      f32x4 s = qx[x] * xq + kx[x] * (xr - xw);
+#pragma unroll
+      for (int i = 2; i >= 0; --i) s[i] += s[i + 1];
+      float later, total;
+      above(s[0], lane, g, later, total);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (SB * x + 4 * g + i < count)
+          a.dlog[(base + (size_t)(SB * x + 4 * g + i) * H) * DK + d0] = carry + later + s[i];
+      carry += total;
     }
   }
 }
