@@ -199,7 +199,7 @@ Sizes pool_sizes(const ssm_dims& d, int32_t num_slots) {
 }
 
 // Whole-sequence calls: the cells (chunk, head) of a packed batch bound every grid of the scan
-// (at most 512 threads a cell), so this keeps them below 2^32 threads.
+// (at most 1,024 threads a cell), so this keeps them below 2^32 threads.
 constexpr long long kMaxCells = 1LL << 22;
 constexpr int kMaxScanHeads = 1 << 16;
 

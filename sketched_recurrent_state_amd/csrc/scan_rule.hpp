@@ -48,7 +48,7 @@ hipError_t launch_scan_rule(const ssm_dims& d, const ScanArgs& a, bool backward,
     const long long units = (long long)d.batch * d.heads;
     auto prep = [&](auto B) {
       hipLaunchKernelGGL((scan_prep_kernel<RULE, kDK, TIN, decltype(B)::value>), dim3(cells * NB),
-                         dim3(64), 0, stream, a);
+                         dim3(64 * kPrepWaves<RULE, kDK>), 0, stream, a);
     };
     auto state = [&](auto B) {
       split_shape<RULE, kDK, kDV, TIN, decltype(B)::value>(d, [&](auto NW, auto NARROW) {
