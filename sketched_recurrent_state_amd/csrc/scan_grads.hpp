@@ -20,8 +20,9 @@
 // registers; dy, e and r pass through LDS 32 values of d_v at a time, split there once for all
 // waves. The 20 tiles of dP and dK are dealt over the waves.
 //
-// Bound by HBM, nearly: a GDN cell of 128 x 128 reads 128 KB of S and G, 96 KB of dy, r and e and
-// writes 33 KB, 1.2 GB for 4,096 cells (2 x 4096 tokens x 32 heads), in 268 us.
+// A GDN cell of 128 x 128 reads 128 KB of S and G, 96 KB of dy, r and e and 32 KB of keys and
+// queries and writes 33 KB: 0.6 GB for the 2,048 cells of 4096 tokens x 32 heads, in GRADUS us. Its
+// eight waves fill a CU's registers, so what bounds it is the latency between its barriers.
 #pragma once
 
 #include "scan.hpp"
@@ -60,7 +61,7 @@ __device__ __forceinline__ f32x4 mfma_parts(const Split8& a, const Split8& b, f3
 }
 
 // Channel tiles of a wave: two with Mamba-2's two products; the delta rules' three leave no
-// registers for a second tile (GDN, 4,096 cells of 128 x 128: two 301 us, 367 us held to half the registers, one 269 us).
+// registers for a second tile (GDN, 2,048 cells of 128 x 128: two 301 us, 367 us held to half the registers, one 269 us).
 template <int RULE, int DK>
 constexpr int kGradTiles = RULE == MAMBA2 && DK >= 32 ? 2 : 1;
 template <int RULE, int DK>
