@@ -173,3 +173,14 @@ def test_reference_gradients_match_differences(rule):
         lo = loss(*[a if j != i else a - eps * d for j, a in enumerate(args)])
         want = (got[name] * d).sum()
         assert abs((hi - lo) / (2 * eps) - want) <= 1e-7 * (np.abs(got[name] * d).sum() + 1)
+
+
+def test_prefill_refuses_lengths_that_do_not_fit():
+    import torch
+    from sketched_recurrent_state_amd.decoder import RecurrentDecoder
+    d = ssm.Dims.make("mamba2", "f32", 2, 1, 16, 16, 4, 4)
+    dec = RecurrentDecoder(d, torch.zeros(2, 1, 16, 16))
+    q, decay = torch.zeros(5, 1, 16), torch.ones(5, 1)
+    for lengths in ([5], [2, 2], [3, 3], [6, -1], torch.tensor([2, 2]), []):
+        with pytest.raises(ValueError):
+            dec.prefill(lengths, q, q, q, decay)
