@@ -601,7 +601,8 @@ def _packed(d: Dims, total: int, plan, q, k, v, decay, beta):
 
 
 def _scan_workspace(workspace, d: Dims, total: int, which: int, args, stream):
-    """A workspace and its bytes: the caller's, or one of the size needed from PyTorch."""
+    """A workspace and its bytes: the caller's, or one of the size needed from PyTorch, which owns
+    it again, in the call's stream's order, when the call returns."""
     if isinstance(workspace, int):
         raise ValueError("workspace: expected a device tensor or None")
     if workspace is not None:
@@ -613,10 +614,19 @@ def _scan_workspace(workspace, d: Dims, total: int, which: int, args, stream):
     need = ctypes.c_int64()
     out = (None, ctypes.byref(need), None) if which == 1 else (None, None, ctypes.byref(need))
     _check(_lib.ssm_scan_sizes(ctypes.byref(d), total, *out))
-    ws = _torch.empty(need.value, dtype=_torch.uint8, device=dev)
-    if stream is not None and need.value:  # used there, allocated on the current stream
-        ws.record_stream(_torch.cuda.ExternalStream(stream, device=dev)
-                         if isinstance(stream, int) else stream)
+    if stream is None:
+        ws = _torch.empty(need.value, dtype=_torch.uint8, device=dev)
+    else:
+        # from the pool of the stream that uses it: a free block of another stream's may still be
+        # in use by what is queued there
+        if not isinstance(stream, _torch.cuda.Stream):
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
+            stream = (_torch.cuda.ExternalStream(handle, device=dev) if handle
+                      else _torch.cuda.default_stream(dev))
+        if stream.device != dev:
+            raise ValueError(f"stream on device {stream.device}, tensors on {dev}")
+        with _torch.cuda.stream(stream):
+            ws = _torch.empty(need.value, dtype=_torch.uint8, device=dev)
     return ws, need.value
 
 

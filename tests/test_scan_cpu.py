@@ -184,3 +184,70 @@ def test_prefill_refuses_lengths_that_do_not_fit():
     for lengths in ([5], [2, 2], [3, 3], [6, -1], torch.tensor([2, 2]), []):
         with pytest.raises(ValueError):
             dec.prefill(lengths, q, q, q, decay)
+
+
+class _Streams:
+    """What the binding uses of torch.cuda, without a device: notes the stream that is current when
+    memory is taken."""
+
+    class Stream:
+        def __init__(self, handle, device):
+            self.cuda_stream, self.device = handle, device
+
+    def __init__(self, device):
+        self.device, self.now, self.took = device, self.Stream(0x100, device), []
+        self.uint8 = "uint8"
+        self.cuda = self
+
+    def ExternalStream(self, handle, device=None):
+        assert handle != 0, "the default stream has no external handle"
+        return self.Stream(handle, device)
+
+    def default_stream(self, device=None):
+        return self.Stream(0, device)
+
+    def current_stream(self, device=None):
+        return self.now
+
+    def stream(self, s):
+        import contextlib
+
+        @contextlib.contextmanager
+        def switched():
+            before, self.now = self.now, s
+            yield
+            self.now = before
+        return switched()
+
+    def empty(self, n, dtype=None, device=None):
+        self.took.append(self.now.cuda_stream)
+
+        class Block:
+            def record_stream(self, stream):
+                pass
+        return Block()
+
+
+@pytest.mark.parametrize("kind", ["current", "stream", "address", "default", "foreign object"])
+def test_workspace_is_taken_on_the_calls_stream(monkeypatch, kind):
+    """A block from another stream's pool may still be in use by work queued on that stream."""
+    import types
+    fake = _Streams("cuda:0")
+    monkeypatch.setattr(ssm, "_torch", fake)
+    tensor = types.SimpleNamespace(device="cuda:0")
+    stream, want = {"current": (None, 0x100), "stream": (fake.Stream(0x200, "cuda:0"), 0x200),
+                    "address": (0x300, 0x300), "default": (0, 0),
+                    "foreign object": (types.SimpleNamespace(cuda_stream=0x400), 0x400)}[kind]
+    for which in (1, 2):
+        ssm._scan_workspace(None, dims(), 100, which, (None, tensor), stream)
+    assert fake.took == [want, want] and fake.now.cuda_stream == 0x100
+
+
+def test_workspace_of_a_stream_on_another_device_is_refused(monkeypatch):
+    import types
+    fake = _Streams("cuda:0")
+    monkeypatch.setattr(ssm, "_torch", fake)
+    with pytest.raises(ValueError, match="device"):
+        ssm._scan_workspace(None, dims(), 100, 1, (types.SimpleNamespace(device="cuda:0"),),
+                            fake.Stream(0x200, "cuda:1"))
+    assert fake.took == []

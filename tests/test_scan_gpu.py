@@ -514,3 +514,31 @@ def test_every_shape_of_the_passes(rule, n, H, dk, dv):
         few.t = {x: pick(t, 1) for x, t in b.t.items()}
         check_forward(few, pick(y, 1), pick(state, 1))
         check_backward(few, {x: pick(t, 1) for x, t in o.items()})
+
+
+def test_other_stream_beside_unfinished_work():
+    """A call on a stream of its own, without a workspace, while the current stream still writes
+    to memory that has been freed there."""
+    b = Batch("gdn", "bf16", [100, 60], 2, 64, 64)
+    y, s = b.forward()
+    o = b.backward()
+    st = torch.cuda.Stream()
+    _, fb, bb = ssm.scan_sizes(b.d, b.T)
+    y2, s2 = torch.empty_like(y), torch.empty_like(s)
+    o2 = {x: None if t is None else torch.empty_like(t) for x, t in o.items()}
+    t = b.t
+    torch.cuda.synchronize()
+    for stream in (st, st.cuda_stream):
+        for size in (fb, bb):
+            busy = torch.empty(size, dtype=torch.uint8, device="cuda")
+            for _ in range(300):
+                busy.fill_(255)
+            del busy
+            if size == fb:
+                ssm.scan_forward(*b.args(), s2, y2, state_in=t["state_in"], stream=stream)
+            else:
+                ssm.scan_backward(*b.args(), t["dy"], o2["dq"], o2["dk"], o2["dv"], o2["dlog"], o2["dbeta"],
+                                  state_in=t["state_in"], dstate=t["dstate"], dstate_in=o2["dS0"], stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(y2, y) and torch.equal(s2, s)
+        assert all(torch.equal(o2[x], o[x]) for x in o)
