@@ -393,8 +393,11 @@ ssm_status ssm_scan_forward(const ssm_dims* d, int32_t total_tokens, const int32
  * NULL: zero). dq, dk, dv have the inputs' type (bf16: rounded once, to nearest);
  * dbeta (NULL for Mamba-2) and dstate_in (NULL: not wanted) are fp32;
  * dlog_decay is fp32 in decay's shape and holds decay * dL/d(decay), the gradient
- * with respect to ln(decay), which stays finite at decay = 0 (where it is 0). The
- * states are computed again from the inputs: nothing is kept from the forward call.
+ * with respect to ln(decay), which stays finite at decay = 0 (where it is exactly 0).
+ * It is the difference of sums over up to 64 tokens, so its rounding is relative to
+ * their terms, |state * dL/d(state)| + |q dq| + |k dk|, not to the value: divided by a
+ * small decay it is no accurate dL/d(decay). The states are computed again from the
+ * inputs: nothing is kept from the forward call.
  * Gradients of tokens behind the last sequence are not written. The workspace as
  * in ssm_scan_forward, with backward_bytes.
  * Outputs: dq, dk, dv, dlog_decay, dbeta, dstate_in, workspace.

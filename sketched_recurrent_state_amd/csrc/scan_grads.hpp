@@ -14,7 +14,9 @@
 // so that all but the last are matrix products (2 x 4096 tokens x 32 heads of 128 x 128, bf16:
 // 2,412 -> 564 us against the whole 16-token diagonal term by term). And
 //   rowsum(S_end * G) = F rowsum(S * G) + sum_j k_j (state part of the writer's dk_j)
-// starts the sums of the gates' gradients without the state at the chunk's end.
+// starts the sums of the gates' gradients without the state at the chunk's end. What passes a
+// gate is so the difference of sums over the chunk's tokens: its rounding is relative to their
+// terms, not to itself, and it is written as 0 where the gate is exactly 0.
 //
 // A wave owns 16 or 32 key channels, so the contractions over d_v stay in its
 // registers; dy, e and r pass through LDS 32 values of d_v at a time, split there once for all
@@ -426,7 +428,10 @@ scan_grads_kernel(const ScanArgs a) {
         const float t = __shfl_down(s, o);
         if (lane + o < 64) s += t;
       }
-      if (lane < count) a.dlog[base + (size_t)lane * H] = last + s;
+      if (lane < count) {  // a gate of 0 lets nothing through: what the sums leave is rounding
+        const size_t t = base + (size_t)lane * H;
+        a.dlog[t] = a.decay[t] == 0.f ? 0.f : last + s;
+      }
     }
   } else {
     static_assert(!CH || TD == 1, "a channel tile a wave");
@@ -562,7 +567,8 @@ scan_grads_kernel(const ScanArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (SB * x + 4 * g + i < count)
-          a.dlog[(base + (size_t)(SB * x + 4 * g + i) * H) * DK + d0] = carry + later + s[i];
+          a.dlog[(base + (size_t)(SB * x + 4 * g + i) * H) * DK + d0] =
+              ax[x][i] == 0.f ? 0.f : carry + later + s[i];
       carry += total;
     }
   }

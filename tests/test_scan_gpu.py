@@ -542,3 +542,15 @@ def test_other_stream_beside_unfinished_work():
         torch.cuda.synchronize()
         assert torch.equal(y2, y) and torch.equal(s2, s)
         assert all(torch.equal(o2[x], o[x]) for x in o)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rule", RULES)
+def test_gate_gradient_is_zero_where_the_gate_is(rule, dtype):
+    """decay * dL/d(decay) at decay = 0 is 0, not what rounding leaves of the sums it comes from."""
+    for lens, dk, dv in (([70, 0, 33], 64, 32), ([1, 130], 16, 64), ([65], 128, 128)):
+        b = Batch(rule, dtype, lens, 3, dk, dv, gates=lambda rng, s: rng.choice([0.0, -0.0, 0.7, 1.0], s))
+        o = b.backward()
+        check_backward(b, o)
+        assert (o["dlog"][b.t["decay"] == 0] == 0).all()
+        assert (o["dlog"][b.t["decay"] != 0] != 0).any()
