@@ -27,23 +27,28 @@ from . import (Dims, IN_BF16, KDA, MAMBA2, SKETCH_BF16, buffer_append, full_read
                window_update_refresh_ranked)
 
 
+def _on_device(lengths) -> bool:
+    return isinstance(lengths, torch.Tensor) and lengths.is_cuda
+
+
 def _check_lengths(d: Dims, lengths, q) -> None:
     if len(lengths) != d.batch:
         raise ValueError(f"{len(lengths)} lengths for a batch of {d.batch}")
-    if not (isinstance(lengths, torch.Tensor) and lengths.is_cuda):  # on the device: not read back
+    if not _on_device(lengths):  # those are not read back
         if min(lengths, default=0) < 0 or sum(lengths) != q.shape[0]:
             raise ValueError(f"lengths sum to {int(sum(lengths))}, the token arrays hold {q.shape[0]}")
 
 
 def _prefill(d: Dims, state: torch.Tensor, lengths, q, k, v, decay, beta) -> torch.Tensor:
     """A packed batch of d.batch prompts (lengths [N]; token arrays [sum][H][..]) through the
-    recurrence, from `state` and into it; returns y [sum][H][d_v]. (Lengths on the device that sum
-    to less leave the last rows of y unset.)"""
+    recurrence, from `state` and into it; returns y [sum][H][d_v]."""
     total = q.shape[0]
+    # lengths that are not read back may sum to less: the rows behind them are not written
+    new = torch.zeros if _on_device(lengths) else torch.empty
     lengths = torch.as_tensor(lengths, dtype=torch.int32, device=state.device)
     plan = torch.empty(scan_sizes(d, total)[0], dtype=torch.int32, device=state.device)
     scan_plan(lengths, total, plan)
-    y = torch.empty((total, d.heads, d.d_v), device=state.device, dtype=torch.float32)
+    y = new((total, d.heads, d.d_v), device=state.device, dtype=torch.float32)
     scan_forward(d, total, plan, q, k, v, decay, beta, state, y, state_in=state)
     return y
 
@@ -140,7 +145,9 @@ class WindowedDecoder:
     def prefill(self, lengths, q, k, v, decay, beta=None) -> torch.Tensor:
         """Take a packed batch of prompts (lengths [N], zero for a sequence with no new tokens;
         token arrays [sum of lengths][H][..]) into the state and refresh the sketch; returns the
-        outputs [sum of lengths][H][d_v]. Tokens still in the window are written first."""
+        outputs [sum of lengths][H][d_v]. Tokens still in the window are written first. Lengths on
+        the device are not read back: prompts are cut where the token arrays end, and outputs
+        behind the last prompt are zero."""
         _check_lengths(self.d, lengths, q)
         if self.tau:
             self.flush()
@@ -194,6 +201,7 @@ class RecurrentDecoder:
         return y
 
     def prefill(self, lengths, q, k, v, decay, beta=None) -> torch.Tensor:
-        """Take a packed batch of prompts into the state; returns their outputs."""
+        """Take a packed batch of prompts into the state; returns their outputs (lengths and
+        outputs as in WindowedDecoder.prefill)."""
         _check_lengths(self.d, lengths, q)
         return _prefill(self.d, self.state, lengths, q, k, v, decay, beta)

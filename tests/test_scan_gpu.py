@@ -554,3 +554,23 @@ def test_gate_gradient_is_zero_where_the_gate_is(rule, dtype):
         check_backward(b, o)
         assert (o["dlog"][b.t["decay"] == 0] == 0).all()
         assert (o["dlog"][b.t["decay"] != 0] != 0).any()
+
+
+def test_prefill_with_lengths_on_the_device():
+    """Lengths that are not read back: rows behind their sum are zero, and a prompt that does not
+    fit is cut where the arrays end."""
+    from sketched_recurrent_state_amd.decoder import RecurrentDecoder
+    b = Batch("gdn", "f32", [21, 40], 2, 16, 32, spare=7)
+    names = ("q", "k", "v", "decay", "beta")
+    want, state = b.forward()
+    for dtype in (torch.int32, torch.int64):
+        torch.full((b.T, b.H, b.dv), float("nan"), device="cuda")  # what new memory may hold
+        dec = RecurrentDecoder(b.d, b.t["state_in"].clone())
+        y = dec.prefill(b.lengths.to(dtype), *[b.t[x] for x in names])
+        assert torch.equal(y[:61], want[:61]) and (y[61:] == 0).all()
+        assert torch.equal(dec.state, state)
+    cut = RecurrentDecoder(b.d, b.t["state_in"].clone())
+    y = cut.prefill(torch.tensor([21, 100], dtype=torch.int32, device="cuda"), *[b.t[x] for x in names])
+    whole = RecurrentDecoder(b.d, b.t["state_in"].clone())
+    assert torch.equal(y, whole.prefill([21, 47], *[b.t[x] for x in names]))
+    assert torch.equal(cut.state, whole.state)
