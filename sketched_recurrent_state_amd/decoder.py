@@ -16,6 +16,7 @@ library's kernels.
 """
 from __future__ import annotations
 
+import operator
 from typing import Optional
 
 import torch
@@ -27,24 +28,33 @@ from . import (Dims, IN_BF16, KDA, MAMBA2, SKETCH_BF16, buffer_append, full_read
                window_update_refresh_ranked)
 
 
-def _on_device(lengths) -> bool:
-    return isinstance(lengths, torch.Tensor) and lengths.is_cuda
-
-
-def _check_lengths(d: Dims, lengths, q) -> None:
+def _checked_lengths(d: Dims, lengths, q):
+    """Prompt lengths as Python integers that sum to q's tokens, or the device tensor, which is
+    not read back."""
+    if isinstance(lengths, torch.Tensor) and lengths.is_cuda:
+        if lengths.is_floating_point() or lengths.is_complex() or lengths.numel() != d.batch:
+            raise ValueError(f"lengths: {lengths.dtype} {tuple(lengths.shape)}, "
+                             f"expected integers ({d.batch},)")
+        return lengths
+    if hasattr(lengths, "reshape"):  # a tensor or an array: its numbers, of whatever width
+        lengths = lengths.reshape(-1).tolist()
+    lengths = [operator.index(n) for n in lengths]
     if len(lengths) != d.batch:
         raise ValueError(f"{len(lengths)} lengths for a batch of {d.batch}")
-    if not _on_device(lengths):  # those are not read back
-        if min(lengths, default=0) < 0 or sum(lengths) != q.shape[0]:
-            raise ValueError(f"lengths sum to {int(sum(lengths))}, the token arrays hold {q.shape[0]}")
+    if min(lengths, default=0) < 0 or sum(lengths) != q.shape[0]:
+        raise ValueError(f"lengths sum to {sum(lengths)}, the token arrays hold {q.shape[0]}")
+    return lengths
 
 
 def _prefill(d: Dims, state: torch.Tensor, lengths, q, k, v, decay, beta) -> torch.Tensor:
-    """A packed batch of d.batch prompts (lengths [N]; token arrays [sum][H][..]) through the
+    """A packed batch of d.batch prompts (checked lengths; token arrays [sum][H][..]) through the
     recurrence, from `state` and into it; returns y [sum][H][d_v]."""
     total = q.shape[0]
     # lengths that are not read back may sum to less: the rows behind them are not written
-    new = torch.zeros if _on_device(lengths) else torch.empty
+    on_device = isinstance(lengths, torch.Tensor)
+    new = torch.zeros if on_device else torch.empty
+    if on_device and lengths.dtype != torch.int32:
+        lengths = lengths.long().clamp(0, total)  # so that the cast cannot wrap
     lengths = torch.as_tensor(lengths, dtype=torch.int32, device=state.device)
     plan = torch.empty(scan_sizes(d, total)[0], dtype=torch.int32, device=state.device)
     scan_plan(lengths, total, plan)
@@ -143,12 +153,12 @@ class WindowedDecoder:
 
     # -- prompts -----------------------------------------------------------------
     def prefill(self, lengths, q, k, v, decay, beta=None) -> torch.Tensor:
-        """Take a packed batch of prompts (lengths [N], zero for a sequence with no new tokens;
-        token arrays [sum of lengths][H][..]) into the state and refresh the sketch; returns the
-        outputs [sum of lengths][H][d_v]. Tokens still in the window are written first. Lengths on
+        """Take a packed batch of prompts (integer lengths [N], zero for a sequence with no new
+        tokens; token arrays [sum of lengths][H][..]) into the state and refresh the sketch; returns
+        the outputs [sum of lengths][H][d_v]. Tokens still in the window are written first. Lengths on
         the device are not read back: prompts are cut where the token arrays end, and outputs
         behind the last prompt are zero."""
-        _check_lengths(self.d, lengths, q)
+        lengths = _checked_lengths(self.d, lengths, q)
         if self.tau:
             self.flush()
         y = _prefill(self.d, self.state, lengths, q, k, v, decay, beta)
@@ -203,5 +213,5 @@ class RecurrentDecoder:
     def prefill(self, lengths, q, k, v, decay, beta=None) -> torch.Tensor:
         """Take a packed batch of prompts into the state; returns their outputs (lengths and
         outputs as in WindowedDecoder.prefill)."""
-        _check_lengths(self.d, lengths, q)
+        lengths = _checked_lengths(self.d, lengths, q)
         return _prefill(self.d, self.state, lengths, q, k, v, decay, beta)

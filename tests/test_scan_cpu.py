@@ -251,3 +251,42 @@ def test_workspace_of_a_stream_on_another_device_is_refused(monkeypatch):
         ssm._scan_workspace(None, dims(), 100, 1, (types.SimpleNamespace(device="cuda:0"),),
                             fake.Stream(0x200, "cuda:1"))
     assert fake.took == []
+
+
+def _prefill_cpu(monkeypatch, lengths, tokens):
+    """prefill with the library calls noted instead of made: the lengths that reach the plan."""
+    import torch
+    from sketched_recurrent_state_amd import decoder
+    seen = []
+    monkeypatch.setattr(decoder, "scan_plan", lambda lens, total, plan: seen.append((lens.tolist(), total)))
+    monkeypatch.setattr(decoder, "scan_forward", lambda *a, **kw: None)
+    d = ssm.Dims.make("mamba2", "f32", 2, 1, 16, 16, 4, 4)
+    q, decay = torch.zeros(tokens, 1, 16), torch.ones(tokens, 1)
+    decoder.RecurrentDecoder(d, torch.zeros(2, 1, 16, 16)).prefill(lengths, q, q, q, decay)
+    return seen
+
+
+def test_prefill_counts_lengths_of_any_integer_type(monkeypatch):
+    """The sum of lengths is that of the numbers, whatever the width of their type."""
+    import torch
+    assert _prefill_cpu(monkeypatch, torch.tensor([[1], [2]]), 3) == [([1, 2], 3)]
+    narrow = [torch.tensor([100, 100], dtype=torch.int8), np.array([100, 100], np.int8),
+              torch.tensor([100, 100], dtype=torch.uint8), np.array([100, 100], np.uint16), (100, np.int8(100))]
+    for lengths in narrow:
+        with pytest.MonkeyPatch.context() as m:
+            assert _prefill_cpu(m, lengths, 200) == [([100, 100], 200)]
+    for lengths in (torch.tensor([200, 100], dtype=torch.uint8), np.array([200, 100], np.uint8)):
+        with pytest.raises(ValueError):  # 300 modulo 2^8 is 44
+            _prefill_cpu(monkeypatch, lengths, 44)
+    with pytest.raises(ValueError):  # 2^32 tokens; the numbers modulo 2^32 sum to 0
+        _prefill_cpu(monkeypatch, np.array([2 ** 31, 2 ** 31], np.uint32), 0)
+    with pytest.raises(ValueError):
+        _prefill_cpu(monkeypatch, np.array([2 ** 32 + 1, 0]), 1)
+
+
+def test_prefill_refuses_lengths_that_are_no_counts(monkeypatch):
+    import torch
+    for lengths in ([1.5, 1.5], torch.tensor([1.5, 1.5]), np.array([2.5, 0.5]), ["1", "2"], [None, 3],
+                    torch.tensor([[1, 2], [0, 0]]), np.array([3]), [[1], [2]], 3, torch.tensor(3)):
+        with pytest.raises((TypeError, ValueError)):
+            _prefill_cpu(monkeypatch, lengths, 3)

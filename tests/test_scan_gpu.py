@@ -574,3 +574,18 @@ def test_prefill_with_lengths_on_the_device():
     whole = RecurrentDecoder(b.d, b.t["state_in"].clone())
     assert torch.equal(y, whole.prefill([21, 47], *[b.t[x] for x in names]))
     assert torch.equal(cut.state, whole.state)
+
+
+def test_prefill_with_wide_lengths_on_the_device():
+    """64-bit lengths beyond 32 bits are cut where the arrays end, as any other; fractions are refused."""
+    from sketched_recurrent_state_amd.decoder import RecurrentDecoder
+    b = Batch("mamba2", "f32", [5, 30], 2, 16, 16)
+    tokens = [b.t[x] for x in ("q", "k", "v", "decay", "beta")]
+    want, state = b.forward()
+    for lens in ([5, 2 ** 32 + 1], [5, 2 ** 31], [5, 30]):
+        dec = RecurrentDecoder(b.d, b.t["state_in"].clone())
+        assert torch.equal(dec.prefill(torch.tensor(lens, device="cuda"), *tokens), want)
+        assert torch.equal(dec.state, state)
+    for lens in (torch.tensor([5.0, 30.0]), torch.tensor([5, 30, 0])):
+        with pytest.raises(ValueError, match="lengths"):
+            dec.prefill(lens.cuda(), *tokens)
