@@ -571,10 +571,19 @@ def _on_device(args, stream, call) -> None:
         call(stream)
 
 
+def _count(x, name: str) -> int:
+    """A 32-bit argument (ctypes would keep the low 32 bits of a larger one)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}: {x} is beyond 32 bits")
+    return x
+
+
 def scan_sizes(d: Dims, total_tokens: int) -> tuple:
     """(int32 elements of the plan, workspace bytes of scan_forward, of scan_backward)."""
     got = [ctypes.c_int64() for _ in range(3)]
-    _check(_lib.ssm_scan_sizes(ctypes.byref(d), int(total_tokens), *map(ctypes.byref, got)))
+    total = _count(total_tokens, "total_tokens")
+    _check(_lib.ssm_scan_sizes(ctypes.byref(d), total, *map(ctypes.byref, got)))
     return tuple(int(x.value) for x in got)
 
 
@@ -582,8 +591,8 @@ def scan_plan(lengths, total_tokens: int, plan, *, n_seqs: Optional[int] = None,
               stream=None) -> None:
     """ssm_scan_plan: the plan of a packed batch from its sequences' lengths (int32 [n]).
     plan: int32, 2 (n + 1) + total_tokens // 64 + n elements. n_seqs is needed with raw addresses."""
-    n = int(lengths.numel() if n_seqs is None else n_seqs)
-    total = int(total_tokens)
+    n = _count(lengths.numel() if n_seqs is None else n_seqs, "n_seqs")
+    total = _count(total_tokens, "total_tokens")
     a = _addr(lengths, "lengths", _I32_T, n)
     b = _addr(plan, "plan", _I32_T, 2 * (n + 1) + total // 64 + n)
     _on_device((lengths, plan), stream,
@@ -637,7 +646,8 @@ def scan_forward(d: Dims, total_tokens: int, plan, q, k, v, decay, beta, state, 
     [total_tokens][H][d_v] and the final states [num_slots][H][d_k][d_v] (num_slots defaults to
     d.batch), from state_in (None: zero; may be `state` itself). workspace: a device tensor of
     scan_sizes(...)[1] bytes, or None to take one from PyTorch for the call."""
-    total, ns = int(total_tokens), d.batch if num_slots is None else int(num_slots)
+    total = _count(total_tokens, "total_tokens")
+    ns = d.batch if num_slots is None else _count(num_slots, "num_slots")
     p = _packed(d, total, plan, q, k, v, decay, beta)
     states = ns * d.heads * d.d_k * d.d_v
     a = (_addr(slot, "slot", _I32_T, d.batch), _addr(state_in, "state_in", _F32_T, states))
@@ -653,7 +663,7 @@ def scan_backward(d: Dims, total_tokens: int, plan, q, k, v, decay, beta, dy, dq
                   workspace=None, stream=None) -> None:
     """ssm_scan_backward: the gradients of scan_forward (dlog_decay is decay * dL/d(decay)).
     workspace: a device tensor of scan_sizes(...)[2] bytes, or None."""
-    total = int(total_tokens)
+    total = _count(total_tokens, "total_tokens")
     p = _packed(d, total, plan, q, k, v, decay, beta)
     rows, tin = total * d.heads, _IN_T.get(d.in_dtype)
     states = d.batch * d.heads * d.d_k * d.d_v

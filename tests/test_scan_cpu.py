@@ -290,3 +290,24 @@ def test_prefill_refuses_lengths_that_are_no_counts(monkeypatch):
                     torch.tensor([[1, 2], [0, 0]]), np.array([3]), [[1], [2]], 3, torch.tensor(3)):
         with pytest.raises((TypeError, ValueError)):
             _prefill_cpu(monkeypatch, lengths, 3)
+
+
+def test_counts_beyond_32_bits_are_refused():
+    """The library takes 32-bit counts: one of 2^32 + 100 must not arrive as 100."""
+    torch = pytest.importorskip("torch")
+    big, d, p = 2 ** 32 + 100, dims(), addrs(20)
+    ws = torch.empty(16)
+    for total in (big, -big, 2 ** 31):
+        with pytest.raises(ValueError, match="total_tokens"):
+            ssm.scan_sizes(d, total)
+        with pytest.raises(ValueError, match="total_tokens"):
+            ssm.scan_plan(A, total, 2 * A, n_seqs=2)
+        with pytest.raises(ValueError, match="total_tokens"):
+            ssm.scan_forward(d, total, *p[:8], workspace=ws, stream=0)
+        with pytest.raises(ValueError, match="total_tokens"):
+            ssm.scan_backward(d, total, *p[:12], workspace=ws, stream=0)
+    with pytest.raises(ValueError, match="n_seqs"):
+        ssm.scan_plan(A, 100, 2 * A, n_seqs=2 ** 32 + 2)
+    with pytest.raises(ValueError, match="num_slots"):
+        ssm.scan_forward(d, 100, *p[:8], num_slots=2 ** 32 + 2, workspace=ws, stream=0)
+    assert ssm.scan_sizes(d, 100)[0] == 2 * 3 + 1 + 2
