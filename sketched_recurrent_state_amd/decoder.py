@@ -159,10 +159,11 @@ class WindowedDecoder:
         the device are not read back: prompts are cut where the token arrays end, and outputs
         behind the last prompt are zero."""
         lengths = _checked_lengths(self.d, lengths, q)
-        if self.tau:
-            self.flush()
-        y = _prefill(self.d, self.state, lengths, q, k, v, decay, beta)
-        self.refresh()
+        with torch.cuda.device_of(self.state):  # the flush and the refresh on the scan's stream
+            if self.tau:
+                self.flush()
+            y = _prefill(self.d, self.state, lengths, q, k, v, decay, beta)
+            self.refresh()
         return y
 
     # -- one decode step -----------------------------------------------------------
@@ -214,4 +215,5 @@ class RecurrentDecoder:
         """Take a packed batch of prompts into the state; returns their outputs (lengths and
         outputs as in WindowedDecoder.prefill)."""
         lengths = _checked_lengths(self.d, lengths, q)
-        return _prefill(self.d, self.state, lengths, q, k, v, decay, beta)
+        with torch.cuda.device_of(self.state):
+            return _prefill(self.d, self.state, lengths, q, k, v, decay, beta)

@@ -311,3 +311,32 @@ def test_counts_beyond_32_bits_are_refused():
     with pytest.raises(ValueError, match="num_slots"):
         ssm.scan_forward(d, 100, *p[:8], num_slots=2 ** 32 + 2, workspace=ws, stream=0)
     assert ssm.scan_sizes(d, 100)[0] == 2 * 3 + 1 + 2
+
+
+@pytest.mark.parametrize("open_window", [False, True])
+def test_prefill_runs_on_the_states_device(monkeypatch, open_window):
+    """All of a prefill's calls, the window's flush and the sketch's refresh with it, are made on the
+    state's device, whichever is the current one: the scan's own stream is that device's."""
+    import contextlib
+    import torch
+    from sketched_recurrent_state_amd import decoder
+    now, made = ["cuda:0"], []
+
+    @contextlib.contextmanager
+    def switched(device):
+        before, now[0] = now[0], str(device)
+        yield
+        now[0] = before
+
+    monkeypatch.setattr(torch.cuda, "device_of", lambda x: switched("the state's"))
+    for name in ("scan_plan", "scan_forward", "window_update_refresh"):
+        monkeypatch.setattr(decoder, name, lambda *a, name=name, **kw: made.append((name, now[0])))
+    d = ssm.Dims.make("mamba2", "f32", 2, 1, 16, 16, 4, 4)
+    q, decay = torch.zeros(5, 1, 16), torch.ones(5, 1)
+    dec = decoder.WindowedDecoder(d, torch.zeros(2, 1, 16, 16), torch.zeros(1, 4, 16))
+    dec.tau = 1 if open_window else 0
+    dec.prefill([2, 3], q, q, q, decay)
+    decoder.RecurrentDecoder(d, dec.state).prefill([2, 3], q, q, q, decay)
+    names = ["scan_plan", "scan_forward"]
+    want = ["window_update_refresh"] * open_window + names + ["window_update_refresh"] + names
+    assert made == [(x, "the state's") for x in want] and now == ["cuda:0"]
