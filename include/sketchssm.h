@@ -348,7 +348,8 @@ ssm_status ssm_recurrent_decode_step(const ssm_dims* d,
  * A non-finite value of a token may reach outputs of its own sequence up to 15
  * tokens before it (tokens are taken 16 at a time), in the backward pass any gradient of
  * its own sequence; never another sequence or head. An infinity may come out as NaN.
- * Sums and states are fp32. d->window and d->rank are checked but not used.
+ * Sums and states are fp32; a product of two fp32 values is taken to 2^-21 of itself, one
+ * with a bf16 input exactly. d->window and d->rank are checked but not used.
  * heads <= 65536; (total_tokens/64 + batch)*heads < 2^22. Results are the same bits from run
  * to run. A sequence's depend on the rest of the batch only by rounding: batch*heads chooses
  * how a sum over d_k is divided.

@@ -95,8 +95,10 @@ struct Quad<uint16_t> {
 // ---------------------------------------------------------------------------
 // x = h + m + l: three bf16 values of 8 bits each. A product with
 // an exact bf16 operand takes three matrix products, one with another split operand six
-// (hh, hm, mh, hl, lh, mm; the dropped ones are below 2^-24), with fp32 sums. bf16 products
-// run 16 times faster than fp32 ones, so three cost a fifth and six three eighths.
+// (hh, hm, mh, hl, lh, mm), with fp32 sums. The dropped ones are below 2^-21 of the product
+// (m < 2^-7 and l < 2^-15 of the value's power of two, which they share a sign with): 0.6 * 2^-24
+// of it in the mean, always toward zero, where an fp32 product is off by up to 2^-24 either way.
+// bf16 products run 16 times faster than fp32 ones, so three cost a fifth and six three eighths.
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 

@@ -340,3 +340,31 @@ def test_prefill_runs_on_the_states_device(monkeypatch, open_window):
     names = ["scan_plan", "scan_forward"]
     want = ["window_update_refresh"] * open_window + names + ["window_update_refresh"] + names
     assert made == [(x, "the state's") for x in want] and now == ["cuda:0"]
+
+
+def _parts(x):
+    """An fp32 value cut into three bf16 ones, as the scan cuts it."""
+    cut = lambda x: (x.view(np.uint32) & np.uint32(0xFFFF0000)).view(np.float32)
+    h = cut(x)
+    m = cut(x - h)
+    return h, m, x - h - m
+
+
+def test_three_parts_hold_an_fp32_value():
+    """Parts of 8 bits that add up to the value, and what the six products of parts that are taken
+    leave of a product of two values: below 2 * 2^-22 + 2^-30, toward zero, 0.6 * 2^-24 in the mean."""
+    rng = np.random.default_rng(0)
+    x = np.concatenate([rng.standard_normal(200000), rng.uniform(1, 2, 200000),
+                        np.ldexp(1.0, rng.integers(-90, 90, 1000)), [1 + 2 ** -7 - 2 ** -23] * 2])
+    a, b = (v.astype(np.float32) for v in (x, np.roll(x, 1)))
+    pa, pb = _parts(a), _parts(b)
+    for v, parts in ((a, pa), (b, pb)):
+        assert all(np.array_equal(p, (p.view(np.uint32) >> 16 << 16).view(np.float32)) for p in parts)
+        assert np.array_equal(sum(p.astype(np.float64) for p in parts), v.astype(np.float64))
+    ha, ma, la, hb, mb, lb = (p.astype(np.float64) for p in pa + pb)
+    taken = la * hb + ha * lb + ma * mb + ma * hb + ha * mb + ha * hb
+    product = a.astype(np.float64) * b.astype(np.float64)
+    lost = (product - taken) / product
+    assert lost.min() > -2.0 ** -50 and lost.max() < 2.0 ** -21 + 2.0 ** -30
+    assert lost.max() > 7.5 * 2.0 ** -24  # of 1 + 2^-7 - 2^-23, squared
+    assert 0.55 < lost[:200000].mean() * 2.0 ** 24 < 0.7
