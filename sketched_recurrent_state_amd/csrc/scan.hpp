@@ -34,11 +34,11 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "scan_table.hpp"
 
 namespace ssm {
 
 constexpr int SB = 16;          // tokens of a block
-constexpr int CT = 64;          // tokens of a chunk (an entry of the chunk table)
 constexpr int NB = CT / SB;     // blocks of a chunk
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -160,37 +160,6 @@ __device__ __forceinline__ f32x4 mfma_exact(uint2 a, const Split4& b, f32x4 c) {
 // fp32 ones are split.
 template <int RULE, typename TIN>
 constexpr bool kExact = RULE != KDA && sizeof(TIN) == 2;
-
-// The plan of ssm_scan_plan: [seq_start (n + 1) | chunk_start (n + 1) | chunk_seq (cap)].
-struct ScanPlan {
-  const int32_t* p;
-  int seqs, total, cap;
-  __device__ __forceinline__ int start(int s) const { return p[s]; }
-  __device__ __forceinline__ int chunk(int s) const { return p[seqs + 1 + s]; }
-  // Chunk c's first token and token count; false where c holds none. Whatever the
-  // table holds, the tokens named are inside [0, total).
-  __device__ __forceinline__ bool cell(int c, int& tok, int& count) const {
-    const int s = p[2 * (seqs + 1) + c];
-    if (s < 0 || s >= seqs) return false;
-    const long long k = (long long)c - chunk(s);
-    const long long b = start(s) + CT * k, e = start(s + 1);
-    if (k < 0 || b < 0 || b >= e || e > total || start(s) < 0) return false;
-    tok = (int)b;
-    count = (int)(e - b < CT ? e - b : CT);
-    return true;
-  }
-  // Sequence s's first token, length and first chunk; false where the table is not a plan's.
-  __device__ __forceinline__ bool sequence(int s, int& tok, int& len, int& first) const {
-    const int b = start(s), e = start(s + 1);
-    first = chunk(s);
-    if (b < 0 || e < b || e > total || first < 0) return false;
-    tok = b;
-    len = e - b;
-    return (long long)first + (len + CT - 1) / CT <= cap;
-  }
-};
-
-inline int scan_capacity(int total, int seqs) { return total / CT + seqs; }
 
 // Workspace: fp32 arrays with one part per cell (head, chunk), cell = head * cap + chunk, so that
 // a unit's blocks follow one another.

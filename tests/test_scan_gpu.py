@@ -589,3 +589,63 @@ def test_prefill_with_wide_lengths_on_the_device():
     for lens in (torch.tensor([5.0, 30.0]), torch.tensor([5, 30, 0])):
         with pytest.raises(ValueError, match="lengths"):
             dec.prefill(lens.cuda(), *tokens)
+
+
+class Banded:
+    """Tensors with guard bands before and behind them."""
+
+    def __init__(self):
+        self.whole = []
+
+    def __call__(self, like_or_shape, dtype=torch.float32, fill=7):
+        shape = getattr(like_or_shape, "shape", like_or_shape)
+        dtype = getattr(like_or_shape, "dtype", dtype)
+        n = int(np.prod(shape))
+        buf = torch.full((n + 8192,), fill, dtype=dtype, device="cuda")
+        self.whole.append((buf, n, fill))
+        return buf[4096:4096 + n].view(shape)
+
+    def intact(self):
+        return all((b[:4096] == f).all() and (b[4096 + n:] == f).all() for b, n, f in self.whole)
+
+
+# changes to the plan of lengths 100, 70, 30 (starts 0 100 170 200, chunks 0 2 4 5, table 0 0 1 1 2 -1): index, value,
+# and the sequences that the change leaves as they were; tests/test_scan_table_cpu.py shows each of them accepted or
+# skipped within the arrays
+WRONG_PLANS = {
+    "a sequence that ends past the arrays": (3, 201, [0, 1]),
+    "far past the arrays": (3, 2 ** 31 - 1, [0, 1]),
+    "starts in descending order": (1, 180, []),
+    "a start below zero": (0, -1, [1, 2]),
+    "an end below zero": (1, -5, [2]),
+    "chunks past the table": (4 + 1, 5, [0, 2]),
+    "chunks below zero": (4 + 2, -1, [0, 1]),
+    "a chunk of a sequence that starts later": (8 + 3, 2, [0, 2]),
+    "a chunk of a sequence that has ended": (8 + 4, 0, [0, 1]),
+    "a chunk of no sequence": (8 + 1, 3, [1, 2]),
+    "a chunk of a sequence far off": (8 + 1, 2 ** 31 - 1, [1, 2]),
+}
+
+
+@pytest.mark.parametrize("rule", RULES)
+@pytest.mark.parametrize("name", WRONG_PLANS)
+def test_wrong_plans_stay_in_their_arrays(rule, name):
+    index, value, kept = WRONG_PLANS[name]
+    b = Batch(rule, "bf16", [100, 70, 30], 2, 64, 32)
+    want_y, want_s = b.forward()
+    want = b.backward()
+    b.plan[index] = value
+    _, fb, bb = ssm.scan_sizes(b.d, b.T)
+    t, new = b.t, Banded()
+    y, s = new(want_y), new(want_s)
+    ssm.scan_forward(*b.args(), s, y, state_in=t["state_in"], workspace=new((fb,), torch.uint8))
+    o = {x: None if w is None else new(w) for x, w in want.items()}
+    ssm.scan_backward(*b.args(), t["dy"], o["dq"], o["dk"], o["dv"], o["dlog"], o["dbeta"], state_in=t["state_in"],
+                      dstate=t["dstate"], dstate_in=o["dS0"], workspace=new((bb,), torch.uint8))
+    torch.cuda.synchronize()
+    assert new.intact()
+    for i, sl in b.parts():
+        if i in kept:
+            assert torch.equal(y[sl], want_y[sl]) and torch.equal(s[i], want_s[i])
+            assert torch.equal(o["dS0"][i], want["dS0"][i])
+            assert all(o[x] is None or torch.equal(o[x][sl], want[x][sl]) for x in o if x != "dS0")
