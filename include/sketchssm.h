@@ -421,7 +421,9 @@ ssm_status ssm_scan_backward(const ssm_dims* d, int32_t total_tokens, const int3
  * d->batch rows; W = d->window; the other dims are checked but not used. All arrays
  * DEVICE int32 [batch] (n_update: one element), 4-byte aligned. A step that takes
  * n_update = d->batch with these update_rows updates exactly the listed rows: the
- * entries of -1 are skipped. One launch.
+ * entries of -1 are skipped, but the listed rows, the first of a longer list, then share
+ * fewer of the GPU's parts (256 rows of 32 heads, 128 x 128, W = 8, 32 rows listed: 125 us
+ * a step, 40 us with n_update = 32). Where the host knows the count, pass it. One launch.
  */
 ssm_status ssm_window_plan(const ssm_dims* d, const int32_t* lengths, int32_t* tau,
                            int32_t* parity, int32_t* update_rows, int32_t* n_update,

@@ -649,3 +649,62 @@ def test_wrong_plans_stay_in_their_arrays(rule, name):
             assert torch.equal(y[sl], want_y[sl]) and torch.equal(s[i], want_s[i])
             assert torch.equal(o["dS0"][i], want["dS0"][i])
             assert all(o[x] is None or torch.equal(o[x][sl], want[x][sl]) for x in o if x != "dS0")
+
+
+@pytest.mark.parametrize("rule", RULES)
+def test_captured_serving_loop(rule):
+    """A serving loop in one graph: positions planned on the device, the step, and the lengths'
+    increment. Replays equal a loop that the host plans with exact counts, bit for bit."""
+    n, H, dk, dv, W, pool, steps = 6, 3, 64, 64, 4, 9, 13
+    d = ssm.Dims.make(rule, "bf16", n, H, dk, dv, W, 8)
+    slot = torch.tensor([8, 0, 3, 7, 2, 5], dtype=torch.int32, device="cuda")
+    start = [0, 3, -1, 2, 7, 3]  # tokens decoded so far; row 2 is padding
+    toks = [Batch(rule, "bf16", [1] * n, H, dk, dv, seed=t) for t in range(steps)]
+    names = ("q", "k", "v", "decay", "beta")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    basis = torch.linalg.qr(rand(H, dk, 8)).Q.transpose(1, 2).contiguous()
+    t0 = toks[0].t
+    first = {"state": rand(pool, H, dk, dv), "sk0": rand(pool, H, 8, dv), "sk1": rand(pool, H, 8, dv),
+             "k": rand(pool, H, W, dk).bfloat16(), "v": rand(pool, H, W, dv).bfloat16(),
+             "decay": torch.rand(pool, H, W, *t0["decay"].shape[2:], device="cuda", generator=gen),
+             "beta": None if rule == "mamba2" else torch.rand(pool, H, W, device="cuda", generator=gen)}
+    copy = lambda x: {k: None if v is None else v.clone() for k, v in x.items()}
+
+    def step(m, cur, tau, parity, n_update, rows, y):
+        ssm.decode_step_varlen(d, pool, slot, tau, parity, n_update, rows, m["state"], m["sk0"], m["sk1"],
+                               basis, *[cur[x] for x in names], m["k"], m["v"], m["decay"], m["beta"], y)
+
+    host, want = copy(first), []
+    for i, t in enumerate(toks):
+        done = [s + i if s >= 0 else -1 for s in start]
+        tau = [x % W + 1 if x >= 0 else 0 for x in done]
+        rows = [r for r in range(n) if tau[r] == W]
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        y = torch.full((n, H, dv), 7.0, device="cuda")
+        step(host, t.t, ints(tau), ints([x // W % 2 if x >= 0 else 0 for x in done]), len(rows),
+             ints(rows) if rows else None, y)
+        want.append(y)
+
+    m, cur = copy(first), copy({x: t0[x] for x in names})
+    lengths = torch.tensor(start, dtype=torch.int32, device="cuda")
+    tau, parity, rows = torch.zeros(3, n, dtype=torch.int32, device="cuda")
+    count = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = torch.full((n, H, dv), 7.0, device="cuda")
+    graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=st):
+        ssm.window_plan(d, lengths, tau, parity, rows, count)
+        step(m, cur, tau, parity, n, rows, y)
+        lengths += (lengths >= 0).int()
+    for t, w in zip(toks, want):
+        for x in names:
+            if cur[x] is not None:
+                cur[x].copy_(t.t[x])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, w)
+        assert (y[2] == 7).all()
+        torch.randn(1000, device="cuda").sum().item()
+    for x in m:
+        assert m[x] is None or torch.equal(m[x], host[x]), x
