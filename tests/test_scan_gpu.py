@@ -708,3 +708,70 @@ def test_captured_serving_loop(rule):
         torch.randn(1000, device="cuda").sum().item()
     for x in m:
         assert m[x] is None or torch.equal(m[x], host[x]), x
+
+
+def test_two_graphs_and_eager_calls_without_workspaces():
+    """Two graphs, each with workspaces that PyTorch gave its calls, replayed in turn beside eager calls."""
+    batches = [Batch("gdn", "bf16", [100, 61], 2, 64, 64), Batch("kda", "f32", [33, 90, 7], 3, 32, 64)]
+    graphs = []
+    for b in batches:
+        b.want = b.forward(), b.backward()
+        graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=st):
+            got = b.forward(), b.backward()
+        graphs.append((graph, got))
+    for _ in range(3):
+        for b, (graph, got) in zip(batches, graphs):
+            for t in (*got[0], *got[1].values()):
+                t.zero_()
+            graph.replay()
+            eager = b.forward(), b.backward()
+            torch.randn(1 << 20, device="cuda").sum().item()
+            for y, o in (got, eager):
+                assert all(torch.equal(x, w) for x, w in zip(y, b.want[0]))
+                assert all(torch.equal(o[x], b.want[1][x]) for x in o)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own stream's."""
+    a, b = Batch("gdn", "bf16", [700], 4, 128, 128), Batch("gdn", "bf16", [650, 3], 4, 128, 128, seed=1)
+    want = [(x.forward(), x.backward()) for x in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for x, st in zip((a, b), streams):
+            with torch.cuda.stream(st):
+                got.append((x.forward(), x.backward()))
+        torch.cuda.synchronize()
+        for (y, o), (wy, wo) in zip(got, want):
+            assert torch.equal(y[0], wy[0]) and torch.equal(y[1], wy[1])
+            assert all(torch.equal(o[x], wo[x]) for x in o)
+
+
+@pytest.mark.parametrize("read", ["sketch", "full"])
+def test_captured_prefill(read):
+    """A decoder's prefill with lengths on the device, captured: replays with other lengths and states."""
+    from sketched_recurrent_state_amd.decoder import WindowedDecoder
+    names = ("q", "k", "v", "decay", "beta")
+    b = Batch("gdn", "bf16", [40, 20, 4], 2, 64, 32)
+    d = ssm.Dims.make("gdn", "bf16", 3, 2, 64, 32, 4, 8)
+    basis = torch.linalg.qr(torch.randn(2, 64, 8, device="cuda")).Q.transpose(1, 2).contiguous()
+    make = lambda: WindowedDecoder(d, b.t["state_in"].clone(), basis, read=read)
+    dec = make()
+    graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=st):
+        y = dec.prefill(b.lengths, *[b.t[x] for x in names])
+    for lens in ([40, 20, 4], [1, 63, 0], [0, 0, 5], [64, 64, 64]):
+        b.lengths.copy_(torch.tensor(lens, dtype=torch.int32))
+        dec.state.copy_(b.t["state_in"])
+        graph.replay()
+        torch.cuda.synchronize()
+        other = make()
+        want = other.prefill(b.lengths.clone(), *[b.t[x] for x in names])
+        assert torch.equal(y, want) and torch.equal(dec.state, other.state)
+        assert read == "full" or torch.equal(dec.sketch, other.sketch)
+        assert (y[min(sum(lens), 64):] == 0).all()
+        torch.randn(1000, device="cuda").sum().item()
