@@ -468,6 +468,202 @@ ssm_status ssm_fit_basis(const ssm_dims* d, const void* samples, int32_t n_sampl
  */
 ssm_status ssm_stream_probe(float* buf, int64_t n_tiles, int32_t shape, void* stream);
 
+/*
+ * What a layer does around its recurrence: the short convolution of its inputs, a recurrence whose
+ * decay goes by channel and state, and the norm of its outputs, each for packed prompts (the plan of
+ * ssm_scan_plan), for their gradients and for a batch of single tokens. (Not on the pages, which
+ * start at the recurrence's inputs.)
+ *
+ * Token arrays are rows: row t is `width` elements from data + t * stride elements on, so that
+ * an array may be a column range of a larger one (a fused projection, its gradient). A stride is at
+ * least the width, a multiple of 8 and below 2^31. Outputs must not overlap inputs or each other;
+ * column ranges of one array (the same stride) do not overlap. Weights are fp32.
+ * Sums, states and statistics are fp32; results in bf16 are rounded once, to nearest. Results are the
+ * same bits from run to run.
+ */
+typedef struct {
+  void* data;
+  int64_t stride; /* elements from row to row */
+} ssm_rows;
+
+/*
+ * The short causal convolution. Its channels come in 1 to 4 parts (queries, keys, values), each with
+ * rows of its own; weights, bias and kept inputs hold the parts' channels one after another,
+ * C = sum of channels[]. For token t of a sequence and channel c, with K = taps:
+ *   u_t = bias[c] + sum_j weight[c][j] x_{t-(K-1)+j}[c],   a = silu(u) or u,
+ * where x before the sequence is the kept state's (zero without one), and
+ *   y = a,  or with norm[p] = n > 0, over each run of n channels of part p:
+ *   y = scale[p] * a / sqrt(sum a^2 + eps)
+ * (the l2 norm of queries and keys per head, n = d_k).
+ *   x, y, dy, dx: parts arrays of rows, in_dtype;   weight fp32 [C][K], bias fp32 [C] or NULL;
+ *   state: in_dtype [slots][K-1][C], a sequence's last K-1 inputs, oldest first.
+ * A NaN or infinity in a token reaches the K tokens from it on (in the gradients the K-1 before them
+ * too) of its own channel, or of its norm's run; dweight and dbias of the channel.
+ * 2 <= K <= 4; channels[p] a multiple of 8, of norm[p] where that is set; norm[p] in {0, 16, 32, 64,
+ * 128}; C <= 2^20; batch < 2^24; (total_tokens/64 + batch) * ceil(C/512) < 2^24.
+ */
+#define SSM_CONV_PARTS 4
+typedef enum { SSM_ACT_NONE = 0, SSM_ACT_SILU = 1, SSM_ACT_SIGMOID = 2 } ssm_activation;
+typedef struct {
+  int32_t in_dtype;   /* ssm_in_dtype of x, y, the state and their gradients */
+  int32_t batch;      /* sequences, or rows of a step                       */
+  int32_t taps;       /* K                                                  */
+  int32_t activation; /* SSM_ACT_NONE or SSM_ACT_SILU                       */
+  int32_t parts;
+  int32_t channels[SSM_CONV_PARTS];
+  int32_t norm[SSM_CONV_PARTS];
+  float scale[SSM_CONV_PARTS];
+  float eps;          /* added to a run's sum of squares: > 0 with a norm   */
+} ssm_conv_dims;
+
+/* Bytes of the workspace of ssm_conv_backward. */
+ssm_status ssm_conv_sizes(const ssm_conv_dims* d, int32_t total_tokens, int64_t* backward_bytes);
+
+/*
+ * A packed batch of d->batch sequences. state_in (NULL: zero) and state (NULL: not wanted) are pools of
+ * num_slots, indexed by slot[s] (DEVICE int32 [batch], NULL: slot s); state_in may be state itself,
+ * which continues prompts in place. A sequence whose slot is outside [0, num_slots) is skipped; the
+ * sequences must map to distinct slots. An empty sequence's state is its state_in. Rows behind the
+ * last sequence are neither read nor written. num_slots and slot are ignored without a state.
+ * Outputs: y, state.
+ */
+ssm_status ssm_conv_forward(const ssm_conv_dims* d, int32_t total_tokens, const int32_t* plan,
+                            int32_t num_slots, const int32_t* slot, const void* state_in,
+                            const ssm_rows* x, const float* weight, const float* bias, void* state,
+                            const ssm_rows* y, void* stream);
+
+/*
+ * Gradients of ssm_conv_forward (slots 0 .. batch-1) for a loss whose gradients with respect to y and
+ * the final states are dy and dstate (in_dtype [batch][K-1][C], NULL: zero). dweight, dbias (NULL:
+ * not wanted) are fp32, sums over all tokens; dstate_in (NULL: not wanted) is in_dtype. Nothing is kept from
+ * the forward call. dx behind the last sequence is not written.
+ * Outputs: dx, dweight, dbias, dstate_in, workspace (16-byte aligned, ssm_conv_sizes' bytes; calls
+ * that may run at the same time need one each).
+ */
+ssm_status ssm_conv_backward(const ssm_conv_dims* d, int32_t total_tokens, const int32_t* plan,
+                             const void* state_in, const ssm_rows* x, const float* weight,
+                             const float* bias, const ssm_rows* dy, const void* dstate,
+                             const ssm_rows* dx, float* dweight, float* dbias, void* dstate_in,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * One token of every row: rows d->batch, the state (in/out) a pool as above. Outputs: y, state.
+ */
+ssm_status ssm_conv_step(const ssm_conv_dims* d, int32_t num_slots, const int32_t* slot,
+                         const ssm_rows* x, const float* weight, const float* bias, void* state,
+                         const ssm_rows* y, void* stream);
+
+/*
+ * The selective recurrence: a state of N = d_state values per channel, whose decay goes by channel and
+ * state. For every token and channel d, with g the channel's group (channels/groups consecutive ones):
+ *   delta = softplus(dt[d] + dt_bias[d])   (softplus = 0: dt[d] + dt_bias[d] itself)
+ *   h[n] <- exp(delta A[d][n]) h[n] + delta x[d] B[g][n],     n = 0 .. N-1
+ *   y[d] = sum_n C[g][n] h[n] + D[d] x[d],      out[d] = y[d] silu(z[d])
+ *   x, dt, z, out   in_dtype rows of `channels`;  B, C  in_dtype rows of groups * d_state
+ *   A  fp32 [channels][d_state] (negative, so that the state decays);  D, dt_bias fp32 [channels]
+ *   states  fp32 [slots][channels][d_state]
+ * z.data, D and dt_bias may be NULL (no gate, no skip, no bias).
+ * A NaN or infinity reaches what follows it in its own sequence (in the gradients all of its
+ * sequence, and the sums over tokens); one in B or C every channel of its group.
+ * d_state in {8, 16, 32, 64}; channels/groups a multiple of 16; channels <= 2^20; batch < 2^24;
+ * (total_tokens/64 + batch) * channels/16 < 2^31; num_slots * channels < 2^38.
+ */
+typedef struct {
+  int32_t in_dtype; /* ssm_in_dtype of x, dt, z, B, C, out */
+  int32_t batch;    /* sequences, or rows of a step        */
+  int32_t channels;
+  int32_t d_state;
+  int32_t groups;
+  int32_t softplus; /* 0 or 1                              */
+} ssm_selective_dims;
+
+typedef struct {
+  ssm_rows x, dt, z, B, C;
+  const float *A, *D, *dt_bias;
+} ssm_selective_inputs;
+
+typedef struct {
+  ssm_rows dx, ddt, dz, dB, dC;
+  float *dA, *dD, *ddt_bias;
+} ssm_selective_grads;
+
+/* Bytes of the workspaces of ssm_selective_forward and ssm_selective_backward. Either may be NULL. */
+ssm_status ssm_selective_sizes(const ssm_selective_dims* d, int32_t total_tokens,
+                               int64_t* forward_bytes, int64_t* backward_bytes);
+
+/*
+ * A packed batch; plan, slots and states as in ssm_conv_forward, but the final states are always
+ * written. The workspace holds nothing between calls; calls that may run at the same time need one
+ * each. Outputs: state, out, workspace.
+ */
+ssm_status ssm_selective_forward(const ssm_selective_dims* d, int32_t total_tokens,
+                                 const int32_t* plan, int32_t num_slots, const int32_t* slot,
+                                 const float* state_in, const ssm_selective_inputs* in, float* state,
+                                 const ssm_rows* out, void* workspace, int64_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * Gradients of ssm_selective_forward (slots 0 .. batch-1) for a loss whose gradients with respect to out
+ * and the final states are dout and dstate (fp32 [batch][channels][d_state], NULL: zero). dx, ddt, dz,
+ * dB, dC are in_dtype; dA [channels][d_state], dD, ddt_bias [channels] fp32, sums over all tokens, and
+ * dstate_in (NULL: not wanted) fp32. dz, dD, ddt_bias are given where z, D, dt_bias are. The
+ * states are computed again: nothing is kept from the forward call.
+ * Outputs: the gradients, workspace.
+ */
+ssm_status ssm_selective_backward(const ssm_selective_dims* d, int32_t total_tokens,
+                                  const int32_t* plan, const float* state_in,
+                                  const ssm_selective_inputs* in, const ssm_rows* dout,
+                                  const float* dstate, const ssm_selective_grads* grads,
+                                  float* dstate_in, void* workspace, int64_t workspace_bytes,
+                                  void* stream);
+
+/* One token of every row: rows d->batch, the state (in/out) a pool. Outputs: state, out. */
+ssm_status ssm_selective_step(const ssm_selective_dims* d, int32_t num_slots, const int32_t* slot,
+                              const ssm_selective_inputs* in, float* state, const ssm_rows* out,
+                              void* stream);
+
+/*
+ * The norm of a layer's outputs in groups of channels, with a gate. For every row and group of `width`
+ * channels, with s(z) the activation z sigmoid(z) (SSM_ACT_SILU) or sigmoid(z) (SSM_ACT_SIGMOID):
+ *   u = x (SSM_GATE_NONE, SSM_GATE_AFTER) or x s(z) (SSM_GATE_BEFORE)
+ *   n = (u - mean) / sqrt(var + eps)      (centred = 0: the mean taken as zero)
+ *   o = n weight + bias,     out = o, or o s(z) (SSM_GATE_AFTER)
+ *   x        x_dtype, rows of groups * width;   z, out  in_dtype, the same shape
+ *   weight   fp32 [groups][width], or [width] for all groups (shared = 1);  bias the same or NULL
+ * width a multiple of 8, at most 8192; groups * width <= 2^20; rows * groups < 2^31; eps > 0.
+ */
+typedef enum { SSM_GATE_NONE = 0, SSM_GATE_AFTER = 1, SSM_GATE_BEFORE = 2 } ssm_gate;
+typedef struct {
+  int32_t x_dtype;  /* ssm_in_dtype of x and dx              */
+  int32_t in_dtype; /* ssm_in_dtype of z, out, dout and dz   */
+  int32_t groups;
+  int32_t width;
+  int32_t gate;       /* ssm_gate                            */
+  int32_t activation; /* of the gate                         */
+  int32_t shared;     /* 1: one weight row for all groups    */
+  int32_t centred;    /* 1: the mean is subtracted           */
+  float eps;
+} ssm_norm_dims;
+
+ssm_status ssm_gated_norm(const ssm_norm_dims* d, int32_t rows, const ssm_rows* x, const ssm_rows* z,
+                          const float* weight, const float* bias, const ssm_rows* out, void* stream);
+
+/* Bytes of the workspace of ssm_gated_norm_backward. */
+ssm_status ssm_gated_norm_sizes(const ssm_norm_dims* d, int32_t rows, int64_t* backward_bytes);
+
+/*
+ * Gradients of ssm_gated_norm for dout. dx is x_dtype, dz (NULL without a gate) in_dtype; dweight
+ * and dbias (NULL: not wanted; bias, which they do without, is needed for dz with SSM_GATE_AFTER) fp32 in
+ * the weights' shape, sums over all rows (shared: and groups).
+ * Outputs: dx, dz, dweight, dbias, workspace (16-byte aligned; calls that may run at the same time
+ * need one each).
+ */
+ssm_status ssm_gated_norm_backward(const ssm_norm_dims* d, int32_t rows, const ssm_rows* x,
+                                   const ssm_rows* z, const float* weight, const float* bias,
+                                   const ssm_rows* dout, const ssm_rows* dx, const ssm_rows* dz,
+                                   float* dweight, float* dbias, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

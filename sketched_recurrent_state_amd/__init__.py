@@ -24,7 +24,10 @@ __all__ = [
     "sketch_decode_step_ranked", "rank_offsets", "window_update_refresh_varlen",
     "sketch_decode_step_varlen", "decode_step_varlen", "window_update_refresh_ls",
     "sketch_decode_step_ls", "scan_sizes", "scan_plan", "scan_forward", "scan_backward",
-    "window_plan", "fit_basis", "stream_probe", "SKETCH_F32", "SKETCH_BF16", "LIB_PATH", "HEADER",
+    "window_plan", "ConvDims", "conv_sizes", "conv_forward", "conv_backward", "conv_step",
+    "SelectiveDims", "selective_sizes", "selective_forward", "selective_backward",
+    "selective_step", "NormDims", "gated_norm_sizes", "gated_norm", "gated_norm_backward",
+    "fit_basis", "stream_probe", "SKETCH_F32", "SKETCH_BF16", "LIB_PATH", "HEADER",
     "declared_symbols", "numel", "library",
 ]
 
@@ -68,6 +71,91 @@ class Dims(ctypes.Structure):
 
     def __repr__(self):
         return "Dims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+_IN_DTYPES = {"bf16": IN_BF16, "f32": IN_F32}
+_ACTIVATIONS = {"none": 0, "silu": 1, "sigmoid": 2}
+_GATES = {"none": 0, "after": 1, "before": 2}
+CONV_PARTS = 4
+
+
+def _fields_repr(x):
+    vals = ((n, getattr(x, n)) for n, _ in x._fields_)
+    return type(x).__name__ + "(" + ", ".join(
+        f"{n}={list(v) if isinstance(v, ctypes.Array) else v}" for n, v in vals) + ")"
+
+
+class ConvDims(ctypes.Structure):
+    """ssm_conv_dims: the short convolution of 1 to 4 parts of a layer's inputs."""
+
+    _fields_ = ([(n, ctypes.c_int32) for n in ("in_dtype", "batch", "taps", "activation", "parts")]
+                + [("channels", ctypes.c_int32 * CONV_PARTS), ("norm", ctypes.c_int32 * CONV_PARTS),
+                   ("scale", ctypes.c_float * CONV_PARTS), ("eps", ctypes.c_float)])
+    __repr__ = _fields_repr
+
+    @classmethod
+    def make(cls, in_dtype, batch, taps, channels, *, norm=None, scale=None, activation="silu",
+             eps=1e-6) -> "ConvDims":
+        """channels: of each part. norm: channels of a head that are normalised together, per
+        part (0: no norm); scale: what a normalised part is multiplied with."""
+        channels = [channels] if isinstance(channels, int) else list(channels)
+        n = len(channels)
+        norm = [0] * n if norm is None else [int(x) for x in norm]
+        scale = [1.0] * n if scale is None else [float(x) for x in scale]
+        if not 1 <= n <= CONV_PARTS or len(norm) != n or len(scale) != n:
+            raise ValueError(f"{n} parts with {len(norm)} norms and {len(scale)} scales; 1 to {CONV_PARTS} parts")
+        d = cls(_IN_DTYPES.get(in_dtype, in_dtype), batch, taps, _ACTIVATIONS.get(activation, activation), n)
+        d.channels[:n], d.norm[:n], d.scale[:n], d.eps = channels, norm, scale, eps
+        return d
+
+
+class SelectiveDims(ctypes.Structure):
+    """ssm_selective_dims: in_dtype, batch, channels, d_state, groups, softplus."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("in_dtype", "batch", "channels", "d_state", "groups", "softplus")]
+    __repr__ = _fields_repr
+
+    @classmethod
+    def make(cls, in_dtype, batch, channels, d_state, *, groups=1, softplus=True) -> "SelectiveDims":
+        return cls(_IN_DTYPES.get(in_dtype, in_dtype), batch, channels, d_state, groups, int(softplus))
+
+
+class NormDims(ctypes.Structure):
+    """ssm_norm_dims: the norm of groups of `width` channels with a gate."""
+
+    _fields_ = ([(n, ctypes.c_int32) for n in ("x_dtype", "in_dtype", "groups", "width", "gate",
+                                               "activation", "shared", "centred")]
+                + [("eps", ctypes.c_float)])
+    __repr__ = _fields_repr
+
+    @classmethod
+    def make(cls, x_dtype, in_dtype, groups, width, *, gate="after", activation="silu", shared=False,
+             centred=False, eps=1e-5) -> "NormDims":
+        """gate: "after" or "before" the norm, or "none"; shared: one weight row for all groups."""
+        return cls(_IN_DTYPES.get(x_dtype, x_dtype), _IN_DTYPES.get(in_dtype, in_dtype), groups,
+                   width, _GATES.get(gate, gate), _ACTIVATIONS.get(activation, activation),
+                   int(shared), int(centred), eps)
+
+
+class _Rows(ctypes.Structure):
+    """ssm_rows"""
+
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
+class _SelectiveInputs(ctypes.Structure):
+    """ssm_selective_inputs"""
+
+    _fields_ = ([(n, _Rows) for n in ("x", "dt", "z", "B", "C")]
+                + [(n, ctypes.c_void_p) for n in ("A", "D", "dt_bias")])
+
+
+class _SelectiveGrads(ctypes.Structure):
+    """ssm_selective_grads"""
+
+    _fields_ = ([(n, _Rows) for n in ("dx", "ddt", "dz", "dB", "dC")]
+                + [(n, ctypes.c_void_p) for n in ("dA", "dD", "ddt_bias")])
 
 
 def _load():
@@ -124,6 +212,24 @@ def _load():
     lib.ssm_scan_backward.argtypes = [dp, i32] + [vp] * 16 + [i64, vp]
     lib.ssm_window_plan.restype = i32
     lib.ssm_window_plan.argtypes = [dp] + [vp] * 6
+    cp, sp, np_ = (ctypes.POINTER(t) for t in (ConvDims, SelectiveDims, NormDims))
+    rp, lp = ctypes.POINTER(_Rows), ctypes.POINTER(i64)
+    ins, outs = ctypes.POINTER(_SelectiveInputs), ctypes.POINTER(_SelectiveGrads)
+    lib.ssm_conv_sizes.argtypes = [cp, i32, lp]
+    lib.ssm_conv_forward.argtypes = [cp, i32, vp, i32, vp, vp, rp, vp, vp, vp, rp, vp]
+    lib.ssm_conv_backward.argtypes = [cp, i32, vp, vp, rp, vp, vp, rp, vp, rp, vp, vp, vp, vp, i64, vp]
+    lib.ssm_conv_step.argtypes = [cp, i32, vp, rp, vp, vp, vp, rp, vp]
+    lib.ssm_selective_sizes.argtypes = [sp, i32, lp, lp]
+    lib.ssm_selective_forward.argtypes = [sp, i32, vp, i32, vp, vp, ins, vp, rp, vp, i64, vp]
+    lib.ssm_selective_backward.argtypes = [sp, i32, vp, vp, ins, rp, vp, outs, vp, vp, i64, vp]
+    lib.ssm_selective_step.argtypes = [sp, i32, vp, ins, vp, rp, vp]
+    lib.ssm_gated_norm_sizes.argtypes = [np_, i32, lp]
+    lib.ssm_gated_norm.argtypes = [np_, i32, rp, rp, vp, vp, rp, vp]
+    lib.ssm_gated_norm_backward.argtypes = [np_, i32, rp, rp, vp, vp, rp, rp, rp, vp, vp, vp, i64, vp]
+    for name in ("conv_sizes", "conv_forward", "conv_backward", "conv_step", "selective_sizes",
+                 "selective_forward", "selective_backward", "selective_step", "gated_norm_sizes",
+                 "gated_norm", "gated_norm_backward"):
+        getattr(lib, "ssm_" + name).restype = i32
     lib.ssm_stream_probe.restype = i32
     lib.ssm_stream_probe.argtypes = [vp, ctypes.c_int64, i32, vp]
     return lib
@@ -609,8 +715,8 @@ def _packed(d: Dims, total: int, plan, q, k, v, decay, beta):
             _addr(beta, "beta", _F32_T, rows))
 
 
-def _scan_workspace(workspace, d: Dims, total: int, which: int, args, stream):
-    """A workspace and its bytes: the caller's, or one of the size needed from PyTorch, which owns
+def _workspace(workspace, need, args, stream):
+    """A workspace and its bytes: the caller's, or one of need() bytes from PyTorch, which owns
     it again, in the call's stream's order, when the call returns."""
     if isinstance(workspace, int):
         raise ValueError("workspace: expected a device tensor or None")
@@ -620,11 +726,9 @@ def _scan_workspace(workspace, d: Dims, total: int, which: int, args, stream):
     dev = next((a.device for a in args if a is not None and not isinstance(a, int)), None)
     if dev is None:
         raise ValueError("workspace: raw addresses need a workspace tensor")
-    need = ctypes.c_int64()
-    out = (None, ctypes.byref(need), None) if which == 1 else (None, None, ctypes.byref(need))
-    _check(_lib.ssm_scan_sizes(ctypes.byref(d), total, *out))
+    need = need()
     if stream is None:
-        ws = _torch.empty(need.value, dtype=_torch.uint8, device=dev)
+        ws = _torch.empty(need, dtype=_torch.uint8, device=dev)
     else:
         # from the pool of the stream that uses it: a free block of another stream's may still be
         # in use by what is queued there
@@ -635,8 +739,18 @@ def _scan_workspace(workspace, d: Dims, total: int, which: int, args, stream):
         if stream.device != dev:
             raise ValueError(f"stream on device {stream.device}, tensors on {dev}")
         with _torch.cuda.stream(stream):
-            ws = _torch.empty(need.value, dtype=_torch.uint8, device=dev)
-    return ws, need.value
+            ws = _torch.empty(need, dtype=_torch.uint8, device=dev)
+    return ws, need
+
+
+def _scan_workspace(workspace, d: Dims, total: int, which: int, args, stream):
+    def need():
+        got = ctypes.c_int64()
+        out = (None, ctypes.byref(got), None) if which == 1 else (None, None, ctypes.byref(got))
+        _check(_lib.ssm_scan_sizes(ctypes.byref(d), total, *out))
+        return got.value
+
+    return _workspace(workspace, need, args, stream)
 
 
 def scan_forward(d: Dims, total_tokens: int, plan, q, k, v, decay, beta, state, y, *,
@@ -689,3 +803,238 @@ def window_plan(d: Dims, lengths, tau, parity, update_rows, n_update, stream=Non
          _addr(n_update, "n_update", _I32_T, 1))
     _on_device((lengths, tau, parity, update_rows, n_update), stream,
                lambda s: _check(_lib.ssm_window_plan(ctypes.byref(d), *a, s)))
+
+
+# ----------------------------------------------------------------------------
+# around the recurrence: short convolution, selective recurrence, output norm
+# ----------------------------------------------------------------------------
+def _row_addr(x, name: str, types, rows: int, width: int) -> _Rows:
+    """Rows of `width` elements: a contiguous tensor, one whose first dimension alone is strided (a
+    column range of a larger one), an address of contiguous rows, or None."""
+    if x is None:
+        return _Rows(None, width)
+    if isinstance(x, int):
+        return _Rows(x, width)
+    if not x.is_cuda:
+        raise ValueError(f"{name}: expected a device tensor")
+    if types is not None and x.dtype not in types:
+        raise TypeError(f"{name}: dtype {x.dtype} not in {types}")
+    if x.numel() != rows * width:
+        raise ValueError(f"{name}: {x.numel()} elements, the dimensions need {rows} x {width}")
+    if x.is_contiguous():
+        return _Rows(x.data_ptr(), width)
+    inner = 1
+    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if size != 1 and stride != inner:
+            raise ValueError(f"{name}: expected rows of contiguous elements, got strides {x.stride()}")
+        inner *= size
+    if x.shape[0] != rows:
+        raise ValueError(f"{name}: expected {rows} rows of {width}, got {tuple(x.shape)}")
+    return _Rows(x.data_ptr(), x.stride(0) if rows > 1 else width)
+
+
+def _bytes_of(call, *args) -> int:
+    got = ctypes.c_int64()
+    _check(call(*args, ctypes.byref(got)))
+    return int(got.value)
+
+
+def _conv_parts(d: ConvDims, xs, name: str, types, rows: int):
+    """The parts' rows as an array, and their tensors."""
+    if xs is None:
+        raise ValueError(f"{name}: expected {d.parts} parts")
+    xs = list(xs) if isinstance(xs, (list, tuple)) else [xs]
+    if len(xs) != d.parts:
+        raise ValueError(f"{name}: {len(xs)} parts, the dimensions have {d.parts}")
+    return (_Rows * CONV_PARTS)(*[_row_addr(x, f"{name}[{p}]", types, rows, d.channels[p])
+                                  for p, x in enumerate(xs)]), xs
+
+
+def _conv_width(d: ConvDims) -> int:
+    return sum(d.channels[:d.parts])
+
+
+def conv_sizes(d: ConvDims, total_tokens: int) -> int:
+    """Workspace bytes of conv_backward."""
+    return _bytes_of(_lib.ssm_conv_sizes, ctypes.byref(d), _count(total_tokens, "total_tokens"))
+
+
+def _plan_ints(total: int, n: int) -> int:
+    return 2 * (n + 1) + total // 64 + n
+
+
+def conv_forward(d: ConvDims, total_tokens: int, plan, x, weight, bias, y, state=None, *, state_in=None,
+                 slot=None, num_slots: Optional[int] = None, stream=None) -> None:
+    """ssm_conv_forward: a packed batch of d.batch sequences through the convolution. x, y: a tensor of
+    rows per part ([total_tokens][channels]; column ranges of a larger tensor are taken as they are),
+    or one tensor for one part. weight [C][taps] fp32, bias [C] fp32 or None. state, state_in: the
+    last taps - 1 inputs [num_slots][taps - 1][C] after and before (None: not wanted; zero)."""
+    total = _count(total_tokens, "total_tokens")
+    ns = d.batch if num_slots is None else _count(num_slots, "num_slots")
+    tin, C = _IN_T.get(d.in_dtype), _conv_width(d)
+    xr, xs = _conv_parts(d, x, "x", tin, total)
+    yr, ys = _conv_parts(d, y, "y", tin, total)
+    kept = ns * (d.taps - 1) * C
+    a = (_addr(plan, "plan", _I32_T, _plan_ints(total, d.batch)), ns,
+         _addr(slot, "slot", _I32_T, d.batch), _addr(state_in, "state_in", tin, kept))
+    b = (_addr(weight, "weight", _F32_T, C * d.taps), _addr(bias, "bias", _F32_T, C),
+         _addr(state, "state", tin, kept))
+    _on_device((plan, weight, bias, state, state_in, slot, *xs, *ys), stream,
+               lambda s: _check(_lib.ssm_conv_forward(ctypes.byref(d), total, *a, xr, *b, yr, s)))
+
+
+def conv_backward(d: ConvDims, total_tokens: int, plan, x, weight, bias, dy, dx, dweight, dbias=None, *,
+                  state_in=None, dstate=None, dstate_in=None, workspace=None, stream=None) -> None:
+    """ssm_conv_backward: the gradients of conv_forward for dy (and dstate, of the final states).
+    workspace: a device tensor of conv_sizes(...) bytes, or None to take one from PyTorch for the call."""
+    total = _count(total_tokens, "total_tokens")
+    tin, C = _IN_T.get(d.in_dtype), _conv_width(d)
+    xr, xs = _conv_parts(d, x, "x", tin, total)
+    gr, gs = _conv_parts(d, dy, "dy", tin, total)
+    dr, ds = _conv_parts(d, dx, "dx", tin, total)
+    kept = d.batch * (d.taps - 1) * C
+    a = (_addr(plan, "plan", _I32_T, _plan_ints(total, d.batch)), _addr(state_in, "state_in", tin, kept))
+    w = (_addr(weight, "weight", _F32_T, C * d.taps), _addr(bias, "bias", _F32_T, C))
+    end = _addr(dstate, "dstate", tin, kept)
+    b = (_addr(dweight, "dweight", _F32_T, C * d.taps), _addr(dbias, "dbias", _F32_T, C),
+         _addr(dstate_in, "dstate_in", tin, kept))
+    args = (plan, weight, bias, state_in, dstate, dweight, dbias, dstate_in, *xs, *gs, *ds)
+    ws, have = _workspace(workspace, lambda: conv_sizes(d, total), args, stream)
+    _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_conv_backward(
+        ctypes.byref(d), total, *a, xr, *w, gr, end, dr, *b, ws.data_ptr(), have, s)))
+
+
+def conv_step(d: ConvDims, x, weight, bias, state, y, *, slot=None, num_slots: Optional[int] = None,
+              stream=None) -> None:
+    """ssm_conv_step: one token of each of d.batch rows; the state is updated in place."""
+    ns = d.batch if num_slots is None else _count(num_slots, "num_slots")
+    tin, C = _IN_T.get(d.in_dtype), _conv_width(d)
+    xr, xs = _conv_parts(d, x, "x", tin, d.batch)
+    yr, ys = _conv_parts(d, y, "y", tin, d.batch)
+    a = (ns, _addr(slot, "slot", _I32_T, d.batch))
+    b = (_addr(weight, "weight", _F32_T, C * d.taps), _addr(bias, "bias", _F32_T, C),
+         _addr(state, "state", tin, ns * (d.taps - 1) * C))
+    _on_device((weight, bias, state, slot, *xs, *ys), stream,
+               lambda s: _check(_lib.ssm_conv_step(ctypes.byref(d), *a, xr, *b, yr, s)))
+
+
+def _selective_in(d: SelectiveDims, rows: int, x, dt, A, B, C, D, z, dt_bias):
+    tin, ch, bc = _IN_T.get(d.in_dtype), d.channels, d.groups * d.d_state
+    return _SelectiveInputs(
+        _row_addr(x, "x", tin, rows, ch), _row_addr(dt, "dt", tin, rows, ch),
+        _row_addr(z, "z", tin, rows, ch), _row_addr(B, "B", tin, rows, bc),
+        _row_addr(C, "C", tin, rows, bc), _addr(A, "A", _F32_T, ch * d.d_state),
+        _addr(D, "D", _F32_T, ch), _addr(dt_bias, "dt_bias", _F32_T, ch))
+
+
+def selective_sizes(d: SelectiveDims, total_tokens: int) -> tuple:
+    """Workspace bytes of (selective_forward, selective_backward)."""
+    got = ctypes.c_int64(), ctypes.c_int64()
+    _check(_lib.ssm_selective_sizes(ctypes.byref(d), _count(total_tokens, "total_tokens"),
+                                    *map(ctypes.byref, got)))
+    return tuple(int(x.value) for x in got)
+
+
+def selective_forward(d: SelectiveDims, total_tokens: int, plan, x, dt, A, B, C, state, out, *, D=None,
+                      z=None, dt_bias=None, state_in=None, slot=None, num_slots: Optional[int] = None,
+                      workspace=None, stream=None) -> None:
+    """ssm_selective_forward: a packed batch of d.batch sequences. x, dt, z, out: rows of d.channels;
+    B, C: rows of groups * d_state; A [channels][d_state], D and dt_bias [channels] fp32; final
+    states [num_slots][channels][d_state] fp32, from state_in (None: zero; may be `state` itself).
+    workspace: a device tensor of selective_sizes(...)[0] bytes, or None."""
+    total = _count(total_tokens, "total_tokens")
+    ns = d.batch if num_slots is None else _count(num_slots, "num_slots")
+    states = ns * d.channels * d.d_state
+    ins = _selective_in(d, total, x, dt, A, B, C, D, z, dt_bias)
+    o = _row_addr(out, "out", _IN_T.get(d.in_dtype), total, d.channels)
+    a = (_addr(plan, "plan", _I32_T, _plan_ints(total, d.batch)), ns,
+         _addr(slot, "slot", _I32_T, d.batch), _addr(state_in, "state_in", _F32_T, states))
+    end = _addr(state, "state", _F32_T, states)
+    args = (plan, x, dt, A, B, C, D, z, dt_bias, state, out, state_in, slot)
+    ws, have = _workspace(workspace, lambda: selective_sizes(d, total)[0], args, stream)
+    _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_selective_forward(
+        ctypes.byref(d), total, *a, ctypes.byref(ins), end, ctypes.byref(o), ws.data_ptr(), have, s)))
+
+
+def selective_backward(d: SelectiveDims, total_tokens: int, plan, x, dt, A, B, C, dout, dx, ddt, dA, dB,
+                       dC, *, D=None, z=None, dt_bias=None, dD=None, dz=None, ddt_bias=None,
+                       state_in=None, dstate=None, dstate_in=None, workspace=None,
+                       stream=None) -> None:
+    """ssm_selective_backward: the gradients of selective_forward for dout (and dstate, of the final
+    states). dz, dD, ddt_bias go with z, D, dt_bias. workspace: a device tensor of
+    selective_sizes(...)[1] bytes, or None."""
+    total = _count(total_tokens, "total_tokens")
+    tin, ch, bc = _IN_T.get(d.in_dtype), d.channels, d.groups * d.d_state
+    states = d.batch * ch * d.d_state
+    ins = _selective_in(d, total, x, dt, A, B, C, D, z, dt_bias)
+    g = _row_addr(dout, "dout", tin, total, ch)
+    outs = _SelectiveGrads(
+        _row_addr(dx, "dx", tin, total, ch), _row_addr(ddt, "ddt", tin, total, ch),
+        _row_addr(dz, "dz", tin, total, ch), _row_addr(dB, "dB", tin, total, bc),
+        _row_addr(dC, "dC", tin, total, bc), _addr(dA, "dA", _F32_T, ch * d.d_state),
+        _addr(dD, "dD", _F32_T, ch), _addr(ddt_bias, "ddt_bias", _F32_T, ch))
+    a = (_addr(plan, "plan", _I32_T, _plan_ints(total, d.batch)),
+         _addr(state_in, "state_in", _F32_T, states))
+    end, start = _addr(dstate, "dstate", _F32_T, states), _addr(dstate_in, "dstate_in", _F32_T, states)
+    args = (plan, x, dt, A, B, C, dout, dx, ddt, dA, dB, dC, D, z, dt_bias, dD, dz, ddt_bias, state_in,
+            dstate, dstate_in)
+    ws, have = _workspace(workspace, lambda: selective_sizes(d, total)[1], args, stream)
+    _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_selective_backward(
+        ctypes.byref(d), total, *a, ctypes.byref(ins), ctypes.byref(g), end, ctypes.byref(outs), start,
+        ws.data_ptr(), have, s)))
+
+
+def selective_step(d: SelectiveDims, x, dt, A, B, C, state, out, *, D=None, z=None, dt_bias=None,
+                   slot=None, num_slots: Optional[int] = None, stream=None) -> None:
+    """ssm_selective_step: one token of each of d.batch rows; the state is updated in place."""
+    ns = d.batch if num_slots is None else _count(num_slots, "num_slots")
+    ins = _selective_in(d, d.batch, x, dt, A, B, C, D, z, dt_bias)
+    o = _row_addr(out, "out", _IN_T.get(d.in_dtype), d.batch, d.channels)
+    a = (ns, _addr(slot, "slot", _I32_T, d.batch))
+    s0 = _addr(state, "state", _F32_T, ns * d.channels * d.d_state)
+    _on_device((x, dt, A, B, C, state, out, D, z, dt_bias, slot), stream,
+               lambda s: _check(_lib.ssm_selective_step(ctypes.byref(d), *a, ctypes.byref(ins), s0,
+                                                        ctypes.byref(o), s)))
+
+
+def _norm_in(d: NormDims, rows: int, x, z, weight, bias):
+    wide = d.groups * d.width
+    own = d.width if d.shared else wide
+    return (_row_addr(x, "x", _IN_T.get(d.x_dtype), rows, wide),
+            _row_addr(z, "z", _IN_T.get(d.in_dtype), rows, wide),
+            _addr(weight, "weight", _F32_T, own), _addr(bias, "bias", _F32_T, own))
+
+
+def gated_norm_sizes(d: NormDims, rows: int) -> int:
+    """Workspace bytes of gated_norm_backward."""
+    return _bytes_of(_lib.ssm_gated_norm_sizes, ctypes.byref(d), _count(rows, "rows"))
+
+
+def gated_norm(d: NormDims, rows: int, x, z, weight, bias, out, stream=None) -> None:
+    """ssm_gated_norm: rows of groups * width channels (x in x_dtype, z and out in in_dtype), each group
+    normalised, weighted and gated by z (None without a gate). weight, bias (or None) fp32, [groups][width],
+    or [width] where shared."""
+    rows = _count(rows, "rows")
+    xr, zr, w, b = _norm_in(d, rows, x, z, weight, bias)
+    o = _row_addr(out, "out", _IN_T.get(d.in_dtype), rows, d.groups * d.width)
+    _on_device((x, z, weight, bias, out), stream, lambda s: _check(_lib.ssm_gated_norm(
+        ctypes.byref(d), rows, ctypes.byref(xr), ctypes.byref(zr), w, b, ctypes.byref(o), s)))
+
+
+def gated_norm_backward(d: NormDims, rows: int, x, z, weight, bias, dout, dx, dz, dweight, dbias=None, *,
+                        workspace=None, stream=None) -> None:
+    """ssm_gated_norm_backward: the gradients of gated_norm for dout. workspace: a device tensor of
+    gated_norm_sizes(...) bytes, or None."""
+    rows = _count(rows, "rows")
+    xr, zr, w, b = _norm_in(d, rows, x, z, weight, bias)
+    wide, tin = d.groups * d.width, _IN_T.get(d.in_dtype)
+    own = d.width if d.shared else wide
+    g, dxr, dzr = (_row_addr(dout, "dout", tin, rows, wide),
+                   _row_addr(dx, "dx", _IN_T.get(d.x_dtype), rows, wide),
+                   _row_addr(dz, "dz", tin, rows, wide))
+    dw, db = _addr(dweight, "dweight", _F32_T, own), _addr(dbias, "dbias", _F32_T, own)
+    args = (x, z, weight, bias, dout, dx, dz, dweight, dbias)
+    ws, have = _workspace(workspace, lambda: gated_norm_sizes(d, rows), args, stream)
+    _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_gated_norm_backward(
+        ctypes.byref(d), rows, ctypes.byref(xr), ctypes.byref(zr), w, b, ctypes.byref(g),
+        ctypes.byref(dxr), ctypes.byref(dzr), dw, db, ws.data_ptr(), have, s)))

@@ -25,7 +25,8 @@ SOURCES = ["abi.hip", "update_refresh.hip", "update_refresh_mamba2.hip", "update
            "sketch_decode_gdn.hip", "sketch_decode_kda.hip", "decode_step_mamba2.hip",
            "decode_step_gdn.hip", "decode_step_kda.hip", "append.hip", "recurrent.hip",
            "fit_basis.hip", "stream_probe.hip", "plan.hip", "scan_mamba2.hip", "scan_gdn.hip",
-           "scan_kda.hip"]
+           "scan_kda.hip", "layer_abi.hip", "conv.hip", "selective.hip", "selective_grads.hip",
+           "norm.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

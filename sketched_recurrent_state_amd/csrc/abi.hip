@@ -7,15 +7,16 @@
 
 #include <string>
 
+#include "abi_checks.hpp"
 #include "launch.hpp"
 #include "scan.hpp"
 #include "sketchssm.h"
 
+namespace ssm {
+
 namespace {
-
 thread_local std::string g_last_error;
-
-constexpr long long kMaxUnits = 1LL << 24;  // keeps every grid below 2^32 threads
+}
 
 ssm_status fail(ssm_status st, const char* fmt, ...) {
   char buf[512];
@@ -31,6 +32,64 @@ ssm_status ok() {
   g_last_error.clear();
   return SSM_OK;
 }
+
+ssm_status launched(hipError_t e, const char* fn) {
+  if (e != hipSuccess) return fail(SSM_E_LAUNCH, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  return ok();
+}
+
+ssm_status check_workspace(const void* workspace, int64_t bytes, size_t need, const char* fn) {
+  if (need > 0 && workspace == nullptr) return fail(SSM_E_NULL, "%s: workspace is NULL", fn);
+  if (bytes < 0 || (size_t)bytes < need)
+    return fail(SSM_E_RANGE, "%s: workspace of %lld bytes, %zu needed", fn, (long long)bytes, need);
+  return SSM_OK;
+}
+
+const char* last_error() { return g_last_error.c_str(); }
+
+// Whether two arrays share a byte. Rows with one stride are compared column range by column range.
+static bool overlap(const Arr& a, const Arr& b) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t a1 = a0 + (a.rows - 1) * a.stride + a.bytes;
+  const uintptr_t b1 = b0 + (b.rows - 1) * b.stride + b.bytes;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (a.stride != b.stride || a.stride == 0) return true;
+  // b's columns begin r bytes into a row that begins with a's
+  const size_t r = b0 >= a0 ? (b0 - a0) % a.stride : (a.stride - (a0 - b0) % a.stride) % a.stride;
+  return r < a.bytes || r + b.bytes > a.stride;
+}
+
+ssm_status check_arrays(const char* fn, const Arr* arrs, size_t n) {
+  for (size_t i = 0; i < n; ++i) {
+    const Arr& a = arrs[i];
+    if (a.p != nullptr && (reinterpret_cast<uintptr_t>(a.p) & (a.align - 1)) != 0)
+      return fail(SSM_E_ALIGN, "%s: %s (%p) is not %u-byte aligned", fn, a.name, a.p, a.align);
+  }
+  for (size_t i = 0; i < n; ++i) {
+    const Arr& a = arrs[i];
+    if (a.p == nullptr || a.bytes == 0 || a.rows == 0) continue;
+    for (size_t j = 0; j < n; ++j) {
+      const Arr& b = arrs[j];
+      if (i == j || b.p == nullptr || b.bytes == 0 || b.rows == 0) continue;
+      if (!a.output && !b.output) continue;
+      if (overlap(a, b)) return fail(SSM_E_ALIAS, "%s: %s overlaps %s", fn, a.name, b.name);
+    }
+  }
+  return SSM_OK;
+}
+
+}  // namespace ssm
+
+namespace {
+
+using ssm::Arr;
+using ssm::check_arrays;
+using ssm::check_workspace;
+using ssm::fail;
+using ssm::launched;
+using ssm::ok;
+
+constexpr long long kMaxUnits = 1LL << 24;  // keeps every grid below 2^32 threads
 
 bool in_set(int x, std::initializer_list<int> s) {
   for (int v : s)
@@ -61,33 +120,6 @@ ssm_status check_dims(const ssm_dims* d, const char* fn) {
   if ((long long)d->batch * d->heads >= kMaxUnits)
     return fail(SSM_E_SHAPE, "%s: batch*heads = %lld >= %lld", fn,
                 (long long)d->batch * d->heads, kMaxUnits);
-  return SSM_OK;
-}
-
-struct Arr {
-  const void* p;
-  size_t bytes;
-  bool output;
-  const char* name;
-  unsigned align = 16;
-};
-
-ssm_status check_arrays(const char* fn, std::initializer_list<Arr> arrs) {
-  for (const Arr& a : arrs) {
-    if (a.p != nullptr && (reinterpret_cast<uintptr_t>(a.p) & (a.align - 1)) != 0)
-      return fail(SSM_E_ALIGN, "%s: %s (%p) is not %u-byte aligned", fn, a.name, a.p, a.align);
-  }
-  for (const Arr& a : arrs) {
-    if (a.p == nullptr || a.bytes == 0) continue;
-    for (const Arr& b : arrs) {
-      if (&a == &b || b.p == nullptr || b.bytes == 0) continue;
-      if (!a.output && !b.output) continue;
-      const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), a1 = a0 + a.bytes;
-      const uintptr_t b0 = reinterpret_cast<uintptr_t>(b.p), b1 = b0 + b.bytes;
-      if (a0 < b1 && b0 < a1)
-        return fail(SSM_E_ALIAS, "%s: %s overlaps %s", fn, a.name, b.name);
-    }
-  }
   return SSM_OK;
 }
 
@@ -230,13 +262,6 @@ ssm_status check_packed(const ssm_dims& d, int32_t total_tokens, const int32_t* 
   return check_beta(d, beta, "beta", fn);
 }
 
-ssm_status check_workspace(const void* workspace, int64_t bytes, size_t need, const char* fn) {
-  if (need > 0 && workspace == nullptr) return fail(SSM_E_NULL, "%s: workspace is NULL", fn);
-  if (bytes < 0 || (size_t)bytes < need)
-    return fail(SSM_E_RANGE, "%s: workspace of %lld bytes, %zu needed", fn, (long long)bytes, need);
-  return SSM_OK;
-}
-
 struct PackedSizes {
   size_t plan, qk, v, gate, beta, y;
   unsigned gate_align;  // one value per token is read alone, KDA's channels four at a time
@@ -264,11 +289,6 @@ hipError_t launch_scan(const ssm_dims& d, const ssm::ScanArgs& a, bool backward,
   return ssm::launch_scan_rule<ssm::KDA>(d, a, backward, s);
 }
 
-ssm_status launched(hipError_t e, const char* fn) {
-  if (e != hipSuccess) return fail(SSM_E_LAUNCH, "%s: launch failed: %s", fn, hipGetErrorString(e));
-  return ok();
-}
-
 }  // namespace
 
 extern "C" {
@@ -288,7 +308,7 @@ const char* ssm_status_string(int32_t status) {
   return "unknown status";
 }
 
-const char* ssm_last_error(void) { return g_last_error.c_str(); }
+const char* ssm_last_error(void) { return ssm::last_error(); }
 
 ssm_status ssm_buffer_append(const ssm_dims* d, const void* k_t, const void* v_t,
                              const float* decay_t, const float* beta_t, void* k_buf, void* v_buf,

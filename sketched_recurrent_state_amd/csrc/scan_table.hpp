@@ -27,6 +27,17 @@ struct ScanPlan {
     count = (int)(e - b < CT ? e - b : CT);
     return true;
   }
+  // Chunk c's sequence, that sequence's first token and length, and the chunk's place in it; false
+  // where cell() is.
+  __host__ __device__ __forceinline__ bool locate(int c, int& s, int& first, int& len, int& pos) const {
+    int tok, count;
+    if (!cell(c, tok, count)) return false;
+    s = p[2 * (seqs + 1) + c];
+    first = start(s);
+    len = start(s + 1) - first;
+    pos = tok - first;
+    return true;
+  }
   // Sequence s's first token, length and first chunk; false where the table is not a plan's.
   __host__ __device__ __forceinline__ bool sequence(int s, int& tok, int& len, int& first) const {
     const int b = start(s), e = start(s + 1);
