@@ -67,9 +67,13 @@ hipError_t launch_conv_step(const ssm_conv_dims& d, ConvArgs& a, hipStream_t str
 // selective recurrence
 // ---------------------------------------------------------------------------
 struct SelectiveWork {
+  // for every group of chunks, of the sequences that go on behind it:
+  float* local;    // [groups][channels][d_state]  the state it leaves, from zero (or the sequence's start)
+  float* sums;     // [groups][channels]           the sum of its deltas
+  float* back;     // backward: [groups][channels][d_state]  the gradient that leaves it at its start
   float* states;   // backward: the state before every 16 tokens of a sequence but its first
   float* dbc;      // [tokens][tiles][2][d_state]   dB and dC of a wave's channels
-  float* partial;  // [walkers][channels][d_state + 2]  dA, dD, ddt_bias of a walker's sequences
+  float* partial;  // [groups][channels][d_state + 2]  dA, dD, ddt_bias of a group's tokens
   size_t bytes;
 };
 
@@ -78,7 +82,8 @@ struct SelectiveArgs {
   Rows x, dt, z, B, C, out, dout;
   Rows dx, ddt, dz, dB, dC;
   const float *A, *D, *dt_bias;
-  int channels, groups, softplus, num_slots, walkers;
+  int channels, groups, softplus, num_slots;
+  int time_groups, group_chunks;  // groups of the plan's chunks, and chunks of one
   const int32_t* slot;
   const float *state_in, *dstate;
   float *state, *dstate_in;

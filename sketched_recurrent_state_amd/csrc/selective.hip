@@ -6,30 +6,32 @@ namespace ssm {
 namespace {
 
 // One block of a sequence: raw inputs of the lane's token.
-template <typename T, int S, int NS, bool OUT>
+template <typename T, int S, int NS, bool C, bool Z, bool DY>
 struct SelBlock {
   using SH = SelShape<S, NS>;
-  Packed<T, SH::EC> x, dt, z;
+  Packed<T, SH::EC> x, dt, z, dy;
   Packed<T, SH::EN> b, c;
-  __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, int64_t tok, bool on) {
+  __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0) {
+    const bool on = t0 + w.t < cell.count;
+    const int64_t tok = (int64_t)cell.first + cell.pos + t0 + w.t;
     const int c0 = w.c0 + w.q * SH::EC, n0 = w.group * SH::N + w.q * SH::EN;
     load_or_zero(x, a.x.row<T>(tok) + c0, on);
     load_or_zero(dt, a.dt.row<T>(tok) + c0, on);
     load_or_zero(b, a.B.row<T>(tok) + n0, on);
-    if constexpr (OUT) {
-      load_or_zero(z, a.z.p ? a.z.row<T>(tok) + c0 : nullptr, on && a.z.p);
-      load_or_zero(c, a.C.row<T>(tok) + n0, on);
-    }
+    if constexpr (Z) load_or_zero(z, a.z.p ? a.z.row<T>(tok) + c0 : nullptr, on && a.z.p);
+    if constexpr (C) load_or_zero(c, a.C.row<T>(tok) + n0, on);
+    if constexpr (DY) load_or_zero(dy, a.dout.row<T>(tok) + c0, on);
   }
 };
 
-// OUT: outputs and final states. Otherwise (the backward pass's first kernel): the state before every
-// block but the sequence's first.
+// The main pass over a group. OUT: outputs and final states. Otherwise (the backward pass's second
+// kernel): the state before every block but the sequence's first.
 template <int S, int NS, typename T, bool OUT>
 __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const SelectiveArgs a) {
   using SH = SelShape<S, NS>;
+  using Block = SelBlock<T, S, NS, OUT, OUT, false>;
   constexpr int N = SH::N, CH = SH::CH, EC = SH::EC, EN = SH::EN;
-  __shared__ __align__(16) float2 sv[WAVES][TB][CH];
+  __shared__ __align__(16) float2 sv[WAVES][TB][CH];  // delta, delta x
   __shared__ __align__(16) float sb[WAVES][TB][N], sc[WAVES][OUT ? TB : 1][N];
   __shared__ float sy[WAVES][OUT ? TB : 1][CH];
   const int wave = threadIdx.x >> 6, tiles = a.channels / CH;
@@ -37,8 +39,9 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
   const int tile = blockIdx.x % tile_blocks * WAVES + wave;
   if (tile >= tiles) return;
   const SelTile w = sel_tile<S>(a, tile);
+  const SelGroup grp = sel_group(a, blockIdx.x / tile_blocks);
   const int my = w.c0 + w.ch, n0 = w.sg * NS;
-  float A[NS], bias[EC], skip[EC];
+  float A[NS], bias[EC], skip[EC], h[NS];
   Vec<float, NS>::load(a.A + (size_t)my * N + n0, A);
 #pragma unroll
   for (int i = 0; i < NS; ++i) A[i] *= kLog2e;
@@ -47,27 +50,40 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
     bias[i] = a.dt_bias ? a.dt_bias[w.c0 + w.q * EC + i] : 0.f;
     skip[i] = a.D ? a.D[w.c0 + w.q * EC + i] : 0.f;
   }
-  for (int s = blockIdx.x / tile_blocks; s < a.plan.seqs; s += a.walkers) {
-    SelSeq q;
-    if (!sel_sequence(a, s, q)) continue;
-    const size_t at = ((size_t)q.slot * a.channels + my) * N + n0;
-    float h[NS];
-#pragma unroll
-    for (int i = 0; i < NS; ++i) h[i] = 0.f;
-    if (a.state_in) Vec<float, NS>::load(a.state_in + at, h);
-    SelBlock<T, S, NS, OUT> next;
-    next.load(a, w, (int64_t)q.tok + w.t, w.t < q.len);
-    for (int t0 = 0; t0 < q.len; t0 += TB) {
-      const SelBlock<T, S, NS, OUT> now = next;
-      const bool on = t0 + w.t < q.len;
-      next.load(a, w, (int64_t)q.tok + t0 + TB + w.t, t0 + TB + w.t < q.len);
+  if (OUT && a.state != a.state_in)
+    for_empty_sequences(a, grp, [&](int, int slot) {
+      const size_t at = ((size_t)slot * a.channels + my) * N + n0;
+      float v[NS];
+      zero(v);
+      if (a.state_in) Vec<float, NS>::load(a.state_in + at, v);
+      Vec<float, NS>::store(a.state + at, v);
+    });
+  SelCell c, ahead;
+  if (!next_cell(a, grp.e0, grp.e1, c)) return;
+  zero(h);
+  if (!c.starts()) carry_in<N>(a, grp, c, my, n0, A, h);
+  Block next;
+  next.load(a, w, c, 0);
+  for (bool more = true; more; c = ahead) {
+    more = next_cell(a, c.entry + 1, grp.e1, ahead);
+    const size_t at = ((size_t)c.slot * a.channels + my) * N + n0;
+    if (c.starts()) {
+      zero(h);
+      if (a.state_in) Vec<float, NS>::load(a.state_in + at, h);
+    }
+    for (int t0 = 0; t0 < c.count; t0 += TB) {
+      const Block now = next;
+      const bool on = t0 + w.t < c.count;
+      const int64_t tok = (int64_t)c.first + c.pos + t0 + w.t;
+      if (t0 + TB < c.count) next.load(a, w, c, t0 + TB);
+      else if (more) next.load(a, w, ahead, 0);
       if constexpr (!OUT) {
-        if (t0 > 0) {
-          const size_t block = (size_t)(q.tok / TB + t0 / TB - 1);
+        if (c.pos + t0 > 0) {
+          const size_t block = (size_t)(c.first / TB + (c.pos + t0) / TB - 1);
           Vec<float, NS>::store(a.w.states + (block * a.channels + my) * N + n0, h);
         }
       }
-      float x[EC], dt[EC], b[EN], c[EN];
+      float x[EC], dt[EC], b[EN], cc[EN];
       now.x.unpack(x);
       now.dt.unpack(dt);
       now.b.unpack(b);
@@ -79,42 +95,165 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
       }
       Vec<float, EN>::store(&sb[wave][w.t][w.q * EN], b);
       if constexpr (OUT) {
-        now.c.unpack(c);
-        Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], c);
+        now.c.unpack(cc);
+        Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], cc);
       }
       wave_lds_sync();
+      float y[(TB + S - 1) / S];  // lane sg keeps the tokens that are sg modulo S
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         const float2 v = sv[wave][t][w.ch];
-        float bb[NS], cc[NS], y = 0.f;
+        float bb[NS], ct[NS], yt = 0.f;
         Vec<float, NS>::load(&sb[wave][t][n0], bb);
-        if constexpr (OUT) Vec<float, NS>::load(&sc[wave][t][n0], cc);
+        if constexpr (OUT) Vec<float, NS>::load(&sc[wave][t][n0], ct);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           h[i] = fmaf(__builtin_amdgcn_exp2f(v.x * A[i]), h[i], v.y * bb[i]);
-          if constexpr (OUT) y = fmaf(cc[i], h[i], y);
+          if constexpr (OUT) yt = fmaf(ct[i], h[i], yt);
         }
         if constexpr (OUT) {
-          y = state_sum<S>(y);
-          if (w.sg == 0) sy[wave][t][w.ch] = y;
+          yt = state_sum<S>(yt);
+          y[t / S] = t % S == 0 ? yt : w.sg == t % S ? yt : y[t / S];
         }
       }
-      wave_lds_sync();
       if constexpr (OUT) {
+#pragma unroll
+        for (int i = 0; i < TB / S; ++i) sy[wave][i * S + w.sg][w.ch] = y[i];
+        wave_lds_sync();
         if (on) {
-          float z[EC], y[EC];
+          float z[EC], o[EC];
           now.z.unpack(z);
 #pragma unroll
           for (int i = 0; i < EC; ++i) {
-            y[i] = fmaf(skip[i], x[i], sy[wave][w.t][w.q * EC + i]);
-            if (a.z.p) y[i] *= z[i] * sigmoid(z[i]);
+            o[i] = fmaf(skip[i], x[i], sy[wave][w.t][w.q * EC + i]);
+            if (a.z.p) o[i] *= z[i] * sigmoid(z[i]);
           }
-          store_row<T, EC>(a.out.out<T>((int64_t)q.tok + t0 + w.t) + w.c0 + w.q * EC, y);
+          store_row<T, EC>(a.out.out<T>(tok) + w.c0 + w.q * EC, o);
+        }
+      }
+      wave_lds_sync();
+    }
+    if (OUT && c.ends()) Vec<float, NS>::store(a.state + at, h);
+  }
+}
+
+// The local pass. Forward: the state that the group's last sequence leaves, if it goes on behind the
+// group. BWD: also the gradient that the group's first sequence leaves at the group's start, if it began
+// before. A group inside one sequence makes both in one walk.
+template <int S, int NS, typename T, bool BWD>
+__global__ void __launch_bounds__(64 * WAVES) selective_local_kernel(const SelectiveArgs a) {
+  using SH = SelShape<S, NS>;
+  using Block = SelBlock<T, S, NS, BWD, BWD, BWD>;
+  constexpr int N = SH::N, CH = SH::CH, EC = SH::EC, EN = SH::EN;
+  __shared__ __align__(16) float4 sv[WAVES][TB][CH];  // delta, delta x, dL/dy
+  __shared__ __align__(16) float sb[WAVES][TB][N], sc[WAVES][BWD ? TB : 1][N];
+  const int wave = threadIdx.x >> 6, tiles = a.channels / CH;
+  const int tile_blocks = (tiles + WAVES - 1) / WAVES;
+  const int tile = blockIdx.x % tile_blocks * WAVES + wave;
+  if (tile >= tiles) return;
+  const SelTile w = sel_tile<S>(a, tile);
+  const SelGroup grp = sel_group(a, blockIdx.x / tile_blocks);
+  SelCell first, last;
+  if (!next_cell(a, grp.e0, grp.e1, first) || !prev_cell(a, grp.e1 - 1, grp.e0 - 1, last)) return;
+  const bool goes_on = !last.ends();                     // the last sequence, behind the group
+  const bool began = BWD && !first.starts();             // the first sequence, before it
+  if (!goes_on && !began) return;
+  const int my = w.c0 + w.ch, n0 = w.sg * NS;
+  float A[NS], bias[EC];
+  Vec<float, NS>::load(a.A + (size_t)my * N + n0, A);
+#pragma unroll
+  for (int i = 0; i < NS; ++i) A[i] *= kLog2e;
+#pragma unroll
+  for (int i = 0; i < EC; ++i) bias[i] = a.dt_bias ? a.dt_bias[w.c0 + w.q * EC + i] : 0.f;
+
+  // Walks from chunk c to the end of its sequence or of the group. leaves: the gradient is wanted.
+  auto walk = [&](SelCell c, bool leaves) {
+    const int seq = c.seq;
+    float h[NS], g[NS], p[NS], sum = 0.f;
+    zero(h);
+    zero(g);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) p[i] = 1.f;
+    if (c.starts() && a.state_in)
+      Vec<float, NS>::load(a.state_in + ((size_t)c.slot * a.channels + my) * N + n0, h);
+    Block next;
+    next.load(a, w, c, 0);
+    SelCell ahead, end = c;
+    for (bool more = true; more; c = ahead) {
+      end = c;
+      more = next_cell(a, c.entry + 1, grp.e1, ahead) && ahead.seq == seq;
+      for (int t0 = 0; t0 < c.count; t0 += TB) {
+        const Block now = next;
+        const bool on = t0 + w.t < c.count;
+        if (t0 + TB < c.count) next.load(a, w, c, t0 + TB);
+        else if (more) next.load(a, w, ahead, 0);
+        float x[EC], dt[EC], b[EN], cc[EN], z[EC], dy[EC];
+        now.x.unpack(x);
+        now.dt.unpack(dt);
+        now.b.unpack(b);
+        if constexpr (BWD) {
+          now.z.unpack(z);
+          now.dy.unpack(dy);
+          now.c.unpack(cc);
+        }
+#pragma unroll
+        for (int i = 0; i < EC; ++i) {
+          const float raw = dt[i] + bias[i];
+          const float delta = on ? (a.softplus ? softplus(raw) : raw) : 0.f;
+          if constexpr (BWD) {
+            if (a.z.p) dy[i] *= z[i] * sigmoid(z[i]);
+            sv[wave][w.t][w.q * EC + i] = make_float4(delta, delta * x[i], dy[i], 0.f);
+          } else {
+            *reinterpret_cast<float2*>(&sv[wave][w.t][w.q * EC + i]) = make_float2(delta, delta * x[i]);
+          }
+        }
+        Vec<float, EN>::store(&sb[wave][w.t][w.q * EN], b);
+        if constexpr (BWD) Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], cc);
+        wave_lds_sync();
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          const float2 v = *reinterpret_cast<const float2*>(&sv[wave][t][w.ch]);
+          float bb[NS], ct[NS], d = 0.f;
+          Vec<float, NS>::load(&sb[wave][t][n0], bb);
+          if constexpr (BWD) {
+            Vec<float, NS>::load(&sc[wave][t][n0], ct);
+            d = sv[wave][t][w.ch].z;
+          }
+          sum += v.x;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            const float decay = __builtin_amdgcn_exp2f(v.x * A[i]);
+            h[i] = fmaf(decay, h[i], v.y * bb[i]);
+            if constexpr (BWD) {
+              p[i] *= decay;
+              g[i] = fmaf(p[i], ct[i] * d, g[i]);
+            }
+          }
         }
         wave_lds_sync();
       }
     }
-    if constexpr (OUT) Vec<float, NS>::store(a.state + at, h);
+    const size_t at = ((size_t)grp.g * a.channels + my) * N + n0;
+    if (!end.ends()) {
+      Vec<float, NS>::store(a.w.local + at, h);
+      if (w.sg == 0) a.w.sums[(size_t)grp.g * a.channels + my] = sum;
+    }
+    if constexpr (BWD) {
+      if (leaves) {
+        if (end.ends() && a.dstate) {
+          float l[NS];
+          Vec<float, NS>::load(a.dstate + ((size_t)end.slot * a.channels + my) * N + n0, l);
+#pragma unroll
+          for (int i = 0; i < NS; ++i) g[i] = fmaf(p[i], l[i], g[i]);
+        }
+        Vec<float, NS>::store(a.w.back + at, g);
+      }
+    }
+  };
+  if (began) walk(first, true);
+  if (goes_on && !(began && last.seq == first.seq)) {
+    const int e = max(seq_entry(a, last.seq), grp.e0);
+    if (next_cell(a, e, grp.e1, first) && first.seq == last.seq) walk(first, false);
   }
 }
 
@@ -156,30 +295,55 @@ __global__ void __launch_bounds__(256) selective_step_kernel(const SelectiveArgs
   }
 }
 
-int walkers_of(const ssm_selective_dims& d, int tile_blocks) {
-  const int most = 4096 / tile_blocks > 1 ? 4096 / tile_blocks : 1;
-  return d.batch < most ? (d.batch > 0 ? d.batch : 1) : most;
-}
+constexpr int kWaves = 4096;  // that a pass aims at
 
-int tiles_of(const ssm_selective_dims& d) {  // of the mapping of selective_dispatch
-  const int S = d.d_state <= 16 ? 4 : d.d_state / 4;
-  return d.channels * S / 64;
-}
-int tile_blocks_of(const ssm_selective_dims& d) { return (tiles_of(d) + WAVES - 1) / WAVES; }
-
-template <bool OUT>
-hipError_t launch_scan_pass(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream) {
-  const int tb = tile_blocks_of(d);
-  a.walkers = walkers_of(d, tb);
+// Launches a pass over the groups: f(S, NS, type, grid).
+template <typename F>
+hipError_t over_groups(const ssm_selective_dims& d, const SelectiveArgs& a, F&& f) {
+  const unsigned tile_blocks = (unsigned)(selective_tiles(d) + WAVES - 1) / WAVES;
   return selective_dispatch(d, [&](auto S, auto NS, auto T) {
-    hipLaunchKernelGGL((selective_scan_kernel<decltype(S)::value, decltype(NS)::value,
-                                              typename decltype(T)::type, OUT>),
-                       dim3((unsigned)tb * (unsigned)a.walkers), dim3(64 * WAVES), 0, stream, a);
+    f(S, NS, T, dim3(tile_blocks * (unsigned)a.time_groups));
     return hipGetLastError();
   });
 }
 
+template <bool OUT>
+hipError_t launch_scan_pass(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream) {
+  return over_groups(d, a, [&](auto S, auto NS, auto T, dim3 grid) {
+    hipLaunchKernelGGL((selective_scan_kernel<decltype(S)::value, decltype(NS)::value,
+                                              typename decltype(T)::type, OUT>),
+                       grid, dim3(64 * WAVES), 0, stream, a);
+  });
+}
+
 }  // namespace
+
+SelGroups selective_groups(const ssm_selective_dims& d, int cap) {
+  if (cap < 1) return SelGroups{1, 1};
+  const int tiles = selective_tiles(d);
+  int groups = (kWaves + tiles - 1) / tiles;
+  if (groups > cap) groups = cap;
+  int chunks = (cap + groups - 1) / groups;
+  // joining the groups before costs a group about a fortieth of a chunk each
+  while ((long long)chunks * chunks * 25 < cap) ++chunks;
+  return SelGroups{chunks, (cap + chunks - 1) / chunks};
+}
+
+hipError_t launch_selective_local(const ssm_selective_dims& d, SelectiveArgs& a, bool backward,
+                                  hipStream_t stream) {
+  const SelGroups g = selective_groups(d, a.plan.cap);
+  a.time_groups = g.groups;
+  a.group_chunks = g.chunks;
+  if (g.groups == 1) return hipSuccess;
+  return over_groups(d, a, [&](auto S, auto NS, auto T, dim3 grid) {
+    constexpr int s = decltype(S)::value, ns = decltype(NS)::value;
+    using TI = typename decltype(T)::type;
+    if (backward)
+      hipLaunchKernelGGL((selective_local_kernel<s, ns, TI, true>), grid, dim3(64 * WAVES), 0, stream, a);
+    else
+      hipLaunchKernelGGL((selective_local_kernel<s, ns, TI, false>), grid, dim3(64 * WAVES), 0, stream, a);
+  });
+}
 
 hipError_t launch_selective_states(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream) {
   return launch_scan_pass<false>(d, a, stream);
@@ -187,23 +351,31 @@ hipError_t launch_selective_states(const ssm_selective_dims& d, SelectiveArgs& a
 
 SelectiveWork selective_work(const ssm_selective_dims& d, int total, bool backward, void* base) {
   SelectiveWork w{};
-  if (!backward) return w;
-  const int tb = tile_blocks_of(d);
+  const SelGroups g = selective_groups(d, d.batch > 0 ? scan_capacity(total, d.batch) : 0);
+  const size_t states = (size_t)d.channels * d.d_state;
   size_t at = 0;
   auto take = [&](size_t floats) {
     float* p = reinterpret_cast<float*>(static_cast<char*>(base) + at);
-    at += floats * sizeof(float);
+    at += floats * sizeof(float);  // channels are a multiple of 16, so every part is one of 64 bytes
     return p;
   };
-  w.states = take(((size_t)total / TB + 1) * d.channels * d.d_state);
-  w.dbc = take((size_t)total * tiles_of(d) * 2 * d.d_state);
-  w.partial = take((size_t)walkers_of(d, tb) * d.channels * (d.d_state + 2));
+  if (g.groups > 1) {
+    w.local = take(g.groups * states);
+    w.sums = take((size_t)g.groups * d.channels);
+  }
+  if (backward) {
+    if (g.groups > 1) w.back = take(g.groups * states);
+    w.states = take(((size_t)total / TB + 1) * states);
+    w.dbc = take((size_t)total * selective_tiles(d) * 2 * d.d_state);
+    w.partial = take((size_t)g.groups * d.channels * (d.d_state + 2));
+  }
   w.bytes = at;
   return w;
 }
 
 hipError_t launch_selective_forward(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream) {
-  return launch_scan_pass<true>(d, a, stream);
+  const hipError_t e = launch_selective_local(d, a, false, stream);
+  return e == hipSuccess ? launch_scan_pass<true>(d, a, stream) : e;
 }
 
 hipError_t launch_selective_step(const ssm_selective_dims& d, const SelectiveArgs& a,

@@ -1,4 +1,4 @@
-// selective.hpp -- the selective recurrence: shared by the forward, backward and single-token kernels.
+// selective.hpp -- the selective recurrence over packed prompts: what the forward and backward passes share.
 //
 // A wave takes 64 / S channels: S lanes a channel, each with NS = d_state / S of its states. Sixteen
 // tokens ("a block") at a time are read by all lanes (lane = 4 * token + quarter, 16 / S channels
@@ -6,6 +6,15 @@
 // token and channel, and passed through LDS of the wave's own: no workgroup barrier. Per state and
 // token the recurrence is a product, an exp2, a product and two fused ones, so prompts are bound by the
 // vector ALU, not by HBM.
+//
+// Time is divided too: the plan's 64-token chunks go to `groups` of equal size, whatever sequences
+// they belong to, and a wave walks one group. A sequence that crosses groups needs its state
+// at each group's start: a first pass ("local") takes every group's part from a state of zero and
+// notes the sum of delta, and the main pass joins the groups before its own,
+//   h <- exp(A sum delta) h + local,
+// which costs a few exps a group. Likewise backwards, where the gradient that leaves a group at its start
+// is sum_t P_t C_t dy_t with P_t the product of the decays up to t: taken in the same forward
+// walk.
 #pragma once
 
 #include "layer.hpp"
@@ -16,8 +25,20 @@ namespace ssm {
 constexpr int TB = 16;     // tokens of a block
 constexpr int WAVES = 4;   // of a workgroup
 
-// log(1 + e^x) without losing small values; above 20 it is x in fp32.
-__device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1pf(expf(x)); }
+// log(1 + e^x) = max(x, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|x| <= 1: the series to s^15 (s <= 1/3, the
+// next term below 2^-27 of the sum), so small values keep their digits. x = +inf and NaN pass through.
+__device__ __forceinline__ float softplus(float x) {
+  const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(x));
+  const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
+  float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
+  p = fmaf(q, p, 1.f / 11.f);
+  p = fmaf(q, p, 1.f / 9.f);
+  p = fmaf(q, p, 1.f / 7.f);
+  p = fmaf(q, p, 1.f / 5.f);
+  p = fmaf(q, p, 1.f / 3.f);
+  p = fmaf(q, p, 1.f);
+  return fmaf(2.f * s, p, x > 0.f || x != x ? x : 0.f);
+}
 
 template <int S, int NS>
 struct SelShape {
@@ -27,8 +48,8 @@ struct SelShape {
 // Sum over the S lanes of a channel.
 template <int S>
 __device__ __forceinline__ float state_sum(float x) {
-  x += dpp<DPP_QUAD_1032>(x);
-  x += dpp<DPP_QUAD_2301>(x);
+  if constexpr (S >= 2) x += dpp<DPP_QUAD_1032>(x);
+  if constexpr (S >= 4) x += dpp<DPP_QUAD_2301>(x);
   if constexpr (S >= 8) x += dpp<DPP_HALF_MIRROR>(x);
   if constexpr (S >= 16) x += dpp<DPP_ROR8>(x);
   return x;
@@ -43,7 +64,7 @@ __device__ __forceinline__ float channel_sum(float x) {
 
 // The wave's tile of channels, and the lane's place in it.
 struct SelTile {
-  int tile, c0, group;   // first channel
+  int tile, c0, group;   // first channel, and the group of B and C
   int lane, t, q;        // reading: token t of a block, quarter q
   int ch, sg;            // computing: channel ch of the tile, states sg * NS ..
 };
@@ -83,19 +104,113 @@ __device__ __forceinline__ void store_row(T* p, const float* v) {
   }
 }
 
-// A walker's sequences: every walkers-th.
-struct SelSeq {
-  int seq, tok, len, slot;
+// A chunk of the plan that holds tokens.
+struct SelCell {
+  int entry, seq, slot, first, len, pos, count;
+  __device__ __forceinline__ bool starts() const { return pos == 0; }
+  __device__ __forceinline__ bool ends() const { return pos + count == len; }
 };
-__device__ __forceinline__ bool sel_sequence(const SelectiveArgs& a, int s, SelSeq& q) {
-  int first;
-  if (!a.plan.sequence(s, q.tok, q.len, first)) return false;
-  q.seq = s;
-  q.slot = a.slot ? a.slot[s] : s;
-  return q.slot >= 0 && q.slot < a.num_slots;
+__device__ __forceinline__ bool sel_slot(const SelectiveArgs& a, int seq, int& slot) {
+  slot = a.slot ? a.slot[seq] : seq;
+  return slot >= 0 && slot < a.num_slots;
+}
+__device__ __forceinline__ bool sel_cell(const SelectiveArgs& a, int e, SelCell& c) {
+  if (!a.plan.locate(e, c.seq, c.first, c.len, c.pos)) return false;
+  c.entry = e;
+  c.count = min(c.len - c.pos, CT);
+  return sel_slot(a, c.seq, c.slot);
+}
+// The first such chunk in [e, end), or in (end, e] going down.
+__device__ __forceinline__ bool next_cell(const SelectiveArgs& a, int e, int end, SelCell& c) {
+  for (; e < end; ++e)
+    if (sel_cell(a, e, c)) return true;
+  return false;
+}
+__device__ __forceinline__ bool prev_cell(const SelectiveArgs& a, int e, int end, SelCell& c) {
+  for (; e > end; --e)
+    if (sel_cell(a, e, c)) return true;
+  return false;
 }
 
-// The states before every block, for the backward pass; sets a.walkers.
+// A group's entries of the chunk table.
+struct SelGroup {
+  int g, e0, e1;
+};
+__device__ __forceinline__ SelGroup sel_group(const SelectiveArgs& a, int g) {
+  return SelGroup{g, g * a.group_chunks, min((g + 1) * a.group_chunks, a.plan.cap)};
+}
+// The entries of sequence s that a plan gives it, cut to the table.
+__device__ __forceinline__ int seq_entry(const SelectiveArgs& a, int s) {
+  return min(max(a.plan.chunk(s), 0), a.plan.cap);
+}
+
+// f(sequence, slot) for the sequences without tokens among the group's entries' numbers (the table has an
+// entry for every sequence).
+template <typename F>
+__device__ __forceinline__ void for_empty_sequences(const SelectiveArgs& a, const SelGroup& g, F&& f) {
+  const int lane = threadIdx.x & 63;
+  for (int e = g.e0; e < g.e1 && e < a.plan.seqs; e += 64) {
+    int tok, len = 1, first, slot = 0;
+    const int s = e + lane;
+    const bool none = s < g.e1 && s < a.plan.seqs && a.plan.sequence(s, tok, len, first) && len == 0 &&
+                      sel_slot(a, s, slot);
+    for (uint64_t left = __ballot(none); left; left &= left - 1) {
+      const int l = __builtin_ctzll(left);
+      f(e + l, __builtin_amdgcn_readlane(slot, l));
+    }
+  }
+}
+
+template <int NS>
+__device__ __forceinline__ void zero(float (&h)[NS]) {
+#pragma unroll
+  for (int i = 0; i < NS; ++i) h[i] = 0.f;
+}
+
+// The state before the group's first chunk c, which is not its sequence's first: the groups before.
+template <int N, int NS>
+__device__ __forceinline__ void carry_in(const SelectiveArgs& a, const SelGroup& g, const SelCell& c, int my,
+                                         int n0, const float (&A2)[NS], float (&h)[NS]) {
+  zero(h);
+  const int from = seq_entry(a, c.seq) / a.group_chunks;
+  const size_t step = (size_t)a.channels * N;
+  const float* p = a.w.local + ((size_t)from * a.channels + my) * N + n0;
+  const float* d = a.w.sums + (size_t)from * a.channels + my;
+#pragma unroll 4
+  for (int i = from; i < g.g; ++i, p += step, d += a.channels) {
+    float l[NS];
+    Vec<float, NS>::load(p, l);
+    const float sum = i > from ? *d : 0.f;  // nothing yet to decay
+#pragma unroll
+    for (int k = 0; k < NS; ++k) h[k] = fmaf(__builtin_amdgcn_exp2f(A2[k] * sum), h[k], l[k]);
+  }
+}
+// The gradient that enters the group's last chunk c from behind, where its sequence goes on.
+template <int N, int NS>
+__device__ __forceinline__ void carry_back(const SelectiveArgs& a, const SelGroup& g, const SelCell& c, int my,
+                                           int n0, const float (&A2)[NS], float (&h)[NS]) {
+  zero(h);
+  const int last = min(max(seq_entry(a, c.seq + 1) - 1, 0) / a.group_chunks, a.time_groups - 1);
+#pragma unroll 4
+  for (int i = last; i > g.g; --i) {
+    float l[NS];
+    Vec<float, NS>::load(a.w.back + ((size_t)i * a.channels + my) * N + n0, l);
+    const float sum = i < last ? a.w.sums[(size_t)i * a.channels + my] : 0.f;  // nothing yet to decay
+#pragma unroll
+    for (int k = 0; k < NS; ++k) h[k] = fmaf(__builtin_amdgcn_exp2f(A2[k] * sum), h[k], l[k]);
+  }
+}
+
+// Groups of the chunk table for a wave count that fills the GPU.
+struct SelGroups {
+  int chunks, groups;
+};
+SelGroups selective_groups(const ssm_selective_dims& d, int cap);
+
+// The local pass; sets a's groups.
+hipError_t launch_selective_local(const ssm_selective_dims& d, SelectiveArgs& a, bool backward,
+                                  hipStream_t stream);
+// The states before every block, for the backward pass.
 hipError_t launch_selective_states(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream);
 
 // Calls f(S, NS, type) for d.d_state: S lanes a channel, NS states a lane.
@@ -112,6 +227,11 @@ hipError_t selective_dispatch(const ssm_selective_dims& d, F&& f) {
     case 64: return with(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
   }
   return hipErrorInvalidValue;
+}
+
+inline int selective_tiles(const ssm_selective_dims& d) {  // of selective_dispatch's mapping
+  const int S = d.d_state <= 16 ? 4 : d.d_state / 4;
+  return d.channels * S / 64;
 }
 
 }  // namespace ssm

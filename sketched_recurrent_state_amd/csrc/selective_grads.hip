@@ -19,8 +19,11 @@ struct GradBlock {
   using SH = SelShape<S, NS>;
   Packed<T, SH::EC> x, dt, z, dy;
   Packed<T, SH::EN> b, c;
-  float h[NS];
-  __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, int64_t tok, bool on) {
+  float h0[NS];  // the state before the block
+  __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0,
+                                       int my, int n) {
+    const bool on = t0 + w.t < cell.count;
+    const int64_t tok = (int64_t)cell.first + cell.pos + t0 + w.t;
     const int c0 = w.c0 + w.q * SH::EC, n0 = w.group * SH::N + w.q * SH::EN;
     load_or_zero(x, a.x.row<T>(tok) + c0, on);
     load_or_zero(dt, a.dt.row<T>(tok) + c0, on);
@@ -28,6 +31,14 @@ struct GradBlock {
     load_or_zero(z, a.z.p ? a.z.row<T>(tok) + c0 : nullptr, on && a.z.p);
     load_or_zero(b, a.B.row<T>(tok) + n0, on);
     load_or_zero(c, a.C.row<T>(tok) + n0, on);
+    if (cell.pos + t0 > 0) {
+      const size_t block = (size_t)(cell.first / TB + (cell.pos + t0) / TB - 1);
+      Vec<float, NS>::load(a.w.states + (block * a.channels + my) * SH::N + n, h0);
+    } else if (a.state_in) {
+      Vec<float, NS>::load(a.state_in + ((size_t)cell.slot * a.channels + my) * SH::N + n, h0);
+    } else {
+      zero(h0);
+    }
   }
 };
 
@@ -40,42 +51,49 @@ __global__ void __launch_bounds__(64 * WAVES) selective_grads_kernel(const Selec
   __shared__ __align__(16) float4 so[WAVES][TB][CH];  // sum G B, sum G a h A, y
   const int wave = threadIdx.x >> 6, tiles = a.channels / CH;
   const int tile_blocks = (tiles + WAVES - 1) / WAVES;
-  const int tile = blockIdx.x % tile_blocks * WAVES + wave, walker = blockIdx.x / tile_blocks;
+  const int tile = blockIdx.x % tile_blocks * WAVES + wave;
   if (tile >= tiles) return;
   const SelTile w = sel_tile<S>(a, tile);
+  const SelGroup grp = sel_group(a, blockIdx.x / tile_blocks);
   const int my = w.c0 + w.ch, n0 = w.sg * NS;
-  float A[NS], dA[NS], bias[EC], skip[EC], dD[EC], dbias[EC];
+  float A[NS], A2[NS], dA[NS], bias[EC], skip[EC], dD[EC], dbias[EC];
   Vec<float, NS>::load(a.A + (size_t)my * N + n0, A);
+  zero(dA);
+  zero(dD);
+  zero(dbias);
 #pragma unroll
-  for (int i = 0; i < NS; ++i) dA[i] = 0.f;
+  for (int i = 0; i < NS; ++i) A2[i] = kLog2e * A[i];
 #pragma unroll
   for (int i = 0; i < EC; ++i) {
     bias[i] = a.dt_bias ? a.dt_bias[w.c0 + w.q * EC + i] : 0.f;
     skip[i] = a.D ? a.D[w.c0 + w.q * EC + i] : 0.f;
-    dD[i] = dbias[i] = 0.f;
   }
-  for (int s = walker; s < a.plan.seqs; s += a.walkers) {
-    SelSeq q;
-    if (!sel_sequence(a, s, q)) continue;
-    const size_t at = ((size_t)s * a.channels + my) * N + n0;
-    float g[NS];
-#pragma unroll
-    for (int i = 0; i < NS; ++i) g[i] = 0.f;
-    if (a.dstate) Vec<float, NS>::load(a.dstate + at, g);
-    for (int t0 = q.len > 0 ? (q.len - 1) / TB * TB : -1; t0 >= 0; t0 -= TB) {
+  if (a.dstate_in)
+    for_empty_sequences(a, grp, [&](int, int slot) {
+      const size_t at = ((size_t)slot * a.channels + my) * N + n0;
+      float v[NS];
+      zero(v);
+      if (a.dstate) Vec<float, NS>::load(a.dstate + at, v);
+      Vec<float, NS>::store(a.dstate_in + at, v);
+    });
+  SelCell cell, ahead;
+  bool more = prev_cell(a, grp.e1 - 1, grp.e0 - 1, cell);
+  float g[NS];
+  zero(g);
+  if (more && !cell.ends()) carry_back<N>(a, grp, cell, my, n0, A2, g);
+  for (; more; cell = ahead) {
+    more = prev_cell(a, cell.entry - 1, grp.e0 - 1, ahead);
+    const size_t at = ((size_t)cell.slot * a.channels + my) * N + n0;
+    if (cell.ends()) {
+      zero(g);
+      if (a.dstate) Vec<float, NS>::load(a.dstate + at, g);
+    }
+    for (int t0 = (cell.count - 1) / TB * TB; t0 >= 0; t0 -= TB) {
       GradBlock<T, S, NS> now;
-      const bool on = t0 + w.t < q.len;
-      const int64_t tok = (int64_t)q.tok + t0 + w.t;
-      now.load(a, w, tok, on);
-      float h0[NS];
-#pragma unroll
-      for (int i = 0; i < NS; ++i) h0[i] = 0.f;
-      if (t0 > 0) {
-        const size_t block = (size_t)(q.tok / TB + t0 / TB - 1);
-        Vec<float, NS>::load(a.w.states + (block * a.channels + my) * N + n0, h0);
-      } else if (a.state_in) {
-        Vec<float, NS>::load(a.state_in + at, h0);
-      }
+      now.load(a, w, cell, t0, my, n0);
+      const bool on = t0 + w.t < cell.count;
+      const int64_t tok = (int64_t)cell.first + cell.pos + t0 + w.t;
+      const float(&h0)[NS] = now.h0;
       float x[EC], raw[EC], z[EC], dy[EC], dout[EC], b[EN], c[EN];
       now.x.unpack(x);
       now.dt.unpack(raw);
@@ -101,7 +119,7 @@ __global__ void __launch_bounds__(64 * WAVES) selective_grads_kernel(const Selec
         Vec<float, NS>::load(&sb[wave][t][n0], bb);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          d[t][i] = __builtin_amdgcn_exp2f(v.x * (kLog2e * A[i]));
+          d[t][i] = __builtin_amdgcn_exp2f(v.x * A2[i]);
           h[t][i] = fmaf(d[t][i], t ? h[t ? t - 1 : 0][i] : h0[i], v.y * bb[i]);
         }
       }
@@ -166,10 +184,10 @@ __global__ void __launch_bounds__(64 * WAVES) selective_grads_kernel(const Selec
       }
       wave_lds_sync();
     }
-    if (a.dstate_in) Vec<float, NS>::store(a.dstate_in + at, g);
+    if (a.dstate_in && cell.starts()) Vec<float, NS>::store(a.dstate_in + at, g);
   }
-  // this walker's sums over tokens: [d_state][channels] would be strided; [channels][d_state], then D, bias
-  float* sums = a.w.partial + (size_t)walker * a.channels * (N + 2);
+  // this group's sums over tokens: dA, then dD and ddt_bias
+  float* sums = a.w.partial + (size_t)grp.g * a.channels * (N + 2);
   Vec<float, NS>::store(sums + (size_t)my * N + n0, dA);
 #pragma unroll
   for (int i = 0; i < EC; ++i) {
@@ -200,15 +218,15 @@ __global__ void __launch_bounds__(256) selective_sum_tiles_kernel(const Selectiv
   store_row<T, 1>(to, &s);
 }
 
-// dA, dD and ddt_bias: the sums over the walkers.
+// dA, dD and ddt_bias: the sums over the groups of chunks.
 __global__ void __launch_bounds__(256)
-selective_sum_walkers_kernel(const SelectiveArgs a, int N) {
+selective_sum_groups_kernel(const SelectiveArgs a, int N) {
   const int i = blockIdx.x * 256 + threadIdx.x;
   const int cols = a.channels * (N + 2);
   if (i >= cols) return;
   float s = 0.f;
 #pragma unroll 8
-  for (int k = 0; k < a.walkers; ++k) s += a.w.partial[(size_t)k * cols + i];
+  for (int k = 0; k < a.time_groups; ++k) s += a.w.partial[(size_t)k * cols + i];
   const int dA = a.channels * N;
   if (i < dA) a.dA[i] = s;
   else if (i < dA + a.channels) {
@@ -221,13 +239,14 @@ selective_sum_walkers_kernel(const SelectiveArgs a, int N) {
 }  // namespace
 
 hipError_t launch_selective_backward(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream) {
-  hipError_t e = launch_selective_states(d, a, stream);
+  hipError_t e = launch_selective_local(d, a, true, stream);
+  if (e == hipSuccess) e = launch_selective_states(d, a, stream);
   if (e != hipSuccess) return e;
   return selective_dispatch(d, [&](auto S, auto NS, auto T) {
     constexpr int s = decltype(S)::value, ns = decltype(NS)::value;
     using TI = typename decltype(T)::type;
     const int tiles = d.channels * s / 64, tb = (tiles + WAVES - 1) / WAVES;
-    hipLaunchKernelGGL((selective_grads_kernel<s, ns, TI>), dim3((unsigned)tb * (unsigned)a.walkers),
+    hipLaunchKernelGGL((selective_grads_kernel<s, ns, TI>), dim3((unsigned)tb * (unsigned)a.time_groups),
                        dim3(64 * WAVES), 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -238,7 +257,7 @@ hipError_t launch_selective_backward(const ssm_selective_dims& d, SelectiveArgs&
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const int cols = d.channels * (d.d_state + 2);
-    hipLaunchKernelGGL(selective_sum_walkers_kernel, dim3((cols + 255) / 256), dim3(256), 0, stream, a,
+    hipLaunchKernelGGL(selective_sum_groups_kernel, dim3((cols + 255) / 256), dim3(256), 0, stream, a,
                        d.d_state);
     return hipGetLastError();
   });
