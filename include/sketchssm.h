@@ -476,7 +476,7 @@ ssm_status ssm_stream_probe(float* buf, int64_t n_tiles, int32_t shape, void* st
  *
  * Token arrays are rows: row t is `width` elements from data + t * stride elements on, so that
  * an array may be a column range of a larger one (a fused projection, its gradient). A stride is at
- * least the width, a multiple of 8 and below 2^31. Outputs must not overlap inputs or each other;
+ * least the width, a multiple of 8 and below 2^26. Outputs must not overlap inputs or each other;
  * column ranges of one array (the same stride) do not overlap. Weights are fp32.
  * Sums, states and statistics are fp32; results in bf16 are rounded once, to nearest. Results are the
  * same bits from run to run.

@@ -72,7 +72,7 @@ struct SelectiveWork {
   float* sums;     // [groups][channels]           the sum of its deltas
   float* back;     // backward: [groups][channels][d_state]  the gradient that leaves it at its start
   float* states;   // backward: the state before every 16 tokens of a sequence but its first
-  float* dbc;      // [tokens][tiles][2][d_state]   dB and dC of a wave's channels
+  float* dbc;      // [tokens + 1][tiles][2][d_state]  dB and dC of a wave's channels
   float* partial;  // [groups][channels][d_state + 2]  dA, dD, ddt_bias of a group's tokens
   size_t bytes;
 };
@@ -83,6 +83,7 @@ struct SelectiveArgs {
   Rows dx, ddt, dz, dB, dC;
   const float *A, *D, *dt_bias;
   int channels, groups, softplus, num_slots;
+  int gated;  // without a gate z is x
   int time_groups, group_chunks;  // groups of the plan's chunks, and chunks of one
   const int32_t* slot;
   const float *state_in, *dstate;

@@ -42,8 +42,8 @@ ssm_status check_dtype(int t, const char* what, const char* fn) {
 // Rows that hold `rows` > 0 rows of `width`.
 ssm_status check_rows(const ssm_rows& r, size_t width, const char* name, const char* fn) {
   if (r.data == nullptr) return fail(SSM_E_NULL, "%s: %s is NULL", fn, name);
-  if (r.stride < (int64_t)width || r.stride % 8 != 0 || r.stride >= (1LL << 31))
-    return fail(SSM_E_SHAPE, "%s: %s has a stride of %lld, not a multiple of 8 in [%zu, 2^31)", fn,
+  if (r.stride < (int64_t)width || r.stride % 8 != 0 || r.stride >= (1LL << 26))
+    return fail(SSM_E_SHAPE, "%s: %s has a stride of %lld, not a multiple of 8 in [%zu, 2^26)", fn,
                 name, (long long)r.stride, width);
   return SSM_OK;
 }
@@ -214,7 +214,8 @@ ssm::SelectiveArgs selective_args(const ssm_selective_dims& d, const ssm_selecti
   ssm::SelectiveArgs a{};
   a.x = ssm::rows_of(in.x);
   a.dt = ssm::rows_of(in.dt);
-  a.z = ssm::rows_of(in.z);
+  a.gated = in.z.data != nullptr;
+  a.z = ssm::rows_of(a.gated ? in.z : in.x);
   a.B = ssm::rows_of(in.B);
   a.C = ssm::rows_of(in.C);
   a.A = in.A;

@@ -5,25 +5,6 @@ namespace ssm {
 
 namespace {
 
-// One block of a sequence: raw inputs of the lane's token.
-template <typename T, int S, int NS, bool C, bool Z, bool DY>
-struct SelBlock {
-  using SH = SelShape<S, NS>;
-  Packed<T, SH::EC> x, dt, z, dy;
-  Packed<T, SH::EN> b, c;
-  __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0) {
-    const bool on = t0 + w.t < cell.count;
-    const int64_t tok = (int64_t)cell.first + cell.pos + t0 + w.t;
-    const int c0 = w.c0 + w.q * SH::EC, n0 = w.group * SH::N + w.q * SH::EN;
-    load_or_zero(x, a.x.row<T>(tok) + c0, on);
-    load_or_zero(dt, a.dt.row<T>(tok) + c0, on);
-    load_or_zero(b, a.B.row<T>(tok) + n0, on);
-    if constexpr (Z) load_or_zero(z, a.z.p ? a.z.row<T>(tok) + c0 : nullptr, on && a.z.p);
-    if constexpr (C) load_or_zero(c, a.C.row<T>(tok) + n0, on);
-    if constexpr (DY) load_or_zero(dy, a.dout.row<T>(tok) + c0, on);
-  }
-};
-
 // The main pass over a group. OUT: outputs and final states. Otherwise (the backward pass's second
 // kernel): the state before every block but the sequence's first.
 template <int S, int NS, typename T, bool OUT>
@@ -31,25 +12,25 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
   using SH = SelShape<S, NS>;
   using Block = SelBlock<T, S, NS, OUT, OUT, false>;
   constexpr int N = SH::N, CH = SH::CH, EC = SH::EC, EN = SH::EN;
-  __shared__ __align__(16) float2 sv[WAVES][TB][CH];  // delta, delta x
+  __shared__ __align__(16) float2 sv[WAVES][TB][CH + 1];  // delta, delta x; a row of 16 channels more would
+                                                          // start in the same bank again
   __shared__ __align__(16) float sb[WAVES][TB][N], sc[WAVES][OUT ? TB : 1][N];
   __shared__ float sy[WAVES][OUT ? TB : 1][CH];
-  const int wave = threadIdx.x >> 6, tiles = a.channels / CH;
+  __shared__ __align__(16) float sbias[WAVES][CH], sskip[WAVES][CH];
+  const int wave = scalar(threadIdx.x >> 6), tiles = a.channels / CH;
   const int tile_blocks = (tiles + WAVES - 1) / WAVES;
   const int tile = blockIdx.x % tile_blocks * WAVES + wave;
   if (tile >= tiles) return;
   const SelTile w = sel_tile<S>(a, tile);
   const SelGroup grp = sel_group(a, blockIdx.x / tile_blocks);
   const int my = w.c0 + w.ch, n0 = w.sg * NS;
-  float A[NS], bias[EC], skip[EC], h[NS];
+  float A[NS], h[NS];
   Vec<float, NS>::load(a.A + (size_t)my * N + n0, A);
 #pragma unroll
   for (int i = 0; i < NS; ++i) A[i] *= kLog2e;
-#pragma unroll
-  for (int i = 0; i < EC; ++i) {
-    bias[i] = a.dt_bias ? a.dt_bias[w.c0 + w.q * EC + i] : 0.f;
-    skip[i] = a.D ? a.D[w.c0 + w.q * EC + i] : 0.f;
-  }
+  stage_channels(sbias[wave], a.dt_bias, w);
+  stage_channels(sskip[wave], a.D, w);
+  wave_lds_sync();
   if (OUT && a.state != a.state_in)
     for_empty_sequences(a, grp, [&](int, int slot) {
       const size_t at = ((size_t)slot * a.channels + my) * N + n0;
@@ -66,7 +47,7 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
   next.load(a, w, c, 0);
   for (bool more = true; more; c = ahead) {
     more = next_cell(a, c.entry + 1, grp.e1, ahead);
-    const size_t at = ((size_t)c.slot * a.channels + my) * N + n0;
+    const size_t at = (size_t)c.slot * a.channels * N + (uint32_t)(my * N + n0);
     if (c.starts()) {
       zero(h);
       if (a.state_in) Vec<float, NS>::load(a.state_in + at, h);
@@ -74,25 +55,25 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
     for (int t0 = 0; t0 < c.count; t0 += TB) {
       const Block now = next;
       const bool on = t0 + w.t < c.count;
-      const int64_t tok = (int64_t)c.first + c.pos + t0 + w.t;
+      const int64_t tok0 = (int64_t)c.first + c.pos + t0;
       if (t0 + TB < c.count) next.load(a, w, c, t0 + TB);
       else if (more) next.load(a, w, ahead, 0);
       if constexpr (!OUT) {
         if (c.pos + t0 > 0) {
           const size_t block = (size_t)(c.first / TB + (c.pos + t0) / TB - 1);
-          Vec<float, NS>::store(a.w.states + (block * a.channels + my) * N + n0, h);
+          Vec<float, NS>::store(a.w.states + block * a.channels * N + (uint32_t)(my * N + n0), h);
         }
       }
-      float x[EC], dt[EC], b[EN], cc[EN];
+      float x[EC], dt[EC], delta[EC], bias[EC], b[EN], cc[EN];
       now.x.unpack(x);
       now.dt.unpack(dt);
       now.b.unpack(b);
+      Vec<float, EC>::load(&sbias[wave][w.q * EC], bias);
 #pragma unroll
-      for (int i = 0; i < EC; ++i) {
-        const float raw = dt[i] + bias[i];
-        const float delta = on ? (a.softplus ? softplus(raw) : raw) : 0.f;
-        sv[wave][w.t][w.q * EC + i] = make_float2(delta, delta * x[i]);
-      }
+      for (int i = 0; i < EC; ++i) dt[i] += bias[i];
+      steps(a, dt, t0 + TB <= c.count, on, delta);
+#pragma unroll
+      for (int i = 0; i < EC; ++i) sv[wave][w.t][w.q * EC + i] = make_float2(delta[i], delta[i] * x[i]);
       Vec<float, EN>::store(&sb[wave][w.t][w.q * EN], b);
       if constexpr (OUT) {
         now.c.unpack(cc);
@@ -121,14 +102,13 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
         for (int i = 0; i < TB / S; ++i) sy[wave][i * S + w.sg][w.ch] = y[i];
         wave_lds_sync();
         if (on) {
-          float z[EC], o[EC];
+          float z[EC], o[EC], skip[EC];
           now.z.unpack(z);
+          Vec<float, EC>::load(&sskip[wave][w.q * EC], skip);
 #pragma unroll
-          for (int i = 0; i < EC; ++i) {
-            o[i] = fmaf(skip[i], x[i], sy[wave][w.t][w.q * EC + i]);
-            if (a.z.p) o[i] *= z[i] * sigmoid(z[i]);
-          }
-          store_row<T, EC>(a.out.out<T>(tok) + w.c0 + w.q * EC, o);
+          for (int i = 0; i < EC; ++i) o[i] = fmaf(skip[i], x[i], sy[wave][w.t][w.q * EC + i]);
+          apply_gate(a, z, o);
+          store_row<T, EC>(row_at<T>(a.out, tok0, w.t, w.c0 + w.q * EC), o);
         }
       }
       wave_lds_sync();
@@ -145,9 +125,11 @@ __global__ void __launch_bounds__(64 * WAVES) selective_local_kernel(const Selec
   using SH = SelShape<S, NS>;
   using Block = SelBlock<T, S, NS, BWD, BWD, BWD>;
   constexpr int N = SH::N, CH = SH::CH, EC = SH::EC, EN = SH::EN;
-  __shared__ __align__(16) float4 sv[WAVES][TB][CH];  // delta, delta x, dL/dy
+  using V = std::conditional_t<BWD, float4, float2>;
+  __shared__ __align__(16) V sv[WAVES][TB][CH + 1];  // delta, delta x, and backwards dL/dy
   __shared__ __align__(16) float sb[WAVES][TB][N], sc[WAVES][BWD ? TB : 1][N];
-  const int wave = threadIdx.x >> 6, tiles = a.channels / CH;
+  __shared__ __align__(16) float sbias[WAVES][CH];
+  const int wave = scalar(threadIdx.x >> 6), tiles = a.channels / CH;
   const int tile_blocks = (tiles + WAVES - 1) / WAVES;
   const int tile = blockIdx.x % tile_blocks * WAVES + wave;
   if (tile >= tiles) return;
@@ -159,12 +141,12 @@ __global__ void __launch_bounds__(64 * WAVES) selective_local_kernel(const Selec
   const bool began = BWD && !first.starts();             // the first sequence, before it
   if (!goes_on && !began) return;
   const int my = w.c0 + w.ch, n0 = w.sg * NS;
-  float A[NS], bias[EC];
+  float A[NS];
   Vec<float, NS>::load(a.A + (size_t)my * N + n0, A);
 #pragma unroll
   for (int i = 0; i < NS; ++i) A[i] *= kLog2e;
-#pragma unroll
-  for (int i = 0; i < EC; ++i) bias[i] = a.dt_bias ? a.dt_bias[w.c0 + w.q * EC + i] : 0.f;
+  stage_channels(sbias[wave], a.dt_bias, w);
+  wave_lds_sync();
 
   // Walks from chunk c to the end of its sequence or of the group. leaves: the gradient is wanted.
   auto walk = [&](SelCell c, bool leaves) {
@@ -175,7 +157,7 @@ __global__ void __launch_bounds__(64 * WAVES) selective_local_kernel(const Selec
 #pragma unroll
     for (int i = 0; i < NS; ++i) p[i] = 1.f;
     if (c.starts() && a.state_in)
-      Vec<float, NS>::load(a.state_in + ((size_t)c.slot * a.channels + my) * N + n0, h);
+      Vec<float, NS>::load(a.state_in + (size_t)c.slot * a.channels * N + (uint32_t)(my * N + n0), h);
     Block next;
     next.load(a, w, c, 0);
     SelCell ahead, end = c;
@@ -187,7 +169,7 @@ __global__ void __launch_bounds__(64 * WAVES) selective_local_kernel(const Selec
         const bool on = t0 + w.t < c.count;
         if (t0 + TB < c.count) next.load(a, w, c, t0 + TB);
         else if (more) next.load(a, w, ahead, 0);
-        float x[EC], dt[EC], b[EN], cc[EN], z[EC], dy[EC];
+        float x[EC], dt[EC], delta[EC], bias[EC], b[EN], cc[EN], z[EC], dy[EC];
         now.x.unpack(x);
         now.dt.unpack(dt);
         now.b.unpack(b);
@@ -196,28 +178,29 @@ __global__ void __launch_bounds__(64 * WAVES) selective_local_kernel(const Selec
           now.dy.unpack(dy);
           now.c.unpack(cc);
         }
+        Vec<float, EC>::load(&sbias[wave][w.q * EC], bias);
+#pragma unroll
+        for (int i = 0; i < EC; ++i) dt[i] += bias[i];
+        steps(a, dt, t0 + TB <= c.count, on, delta);
+        if constexpr (BWD) apply_gate(a, z, dy);
 #pragma unroll
         for (int i = 0; i < EC; ++i) {
-          const float raw = dt[i] + bias[i];
-          const float delta = on ? (a.softplus ? softplus(raw) : raw) : 0.f;
-          if constexpr (BWD) {
-            if (a.z.p) dy[i] *= z[i] * sigmoid(z[i]);
-            sv[wave][w.t][w.q * EC + i] = make_float4(delta, delta * x[i], dy[i], 0.f);
-          } else {
-            *reinterpret_cast<float2*>(&sv[wave][w.t][w.q * EC + i]) = make_float2(delta, delta * x[i]);
-          }
+          if constexpr (BWD)
+            sv[wave][w.t][w.q * EC + i] = make_float4(delta[i], delta[i] * x[i], dy[i], 0.f);
+          else
+            sv[wave][w.t][w.q * EC + i] = make_float2(delta[i], delta[i] * x[i]);
         }
         Vec<float, EN>::store(&sb[wave][w.t][w.q * EN], b);
         if constexpr (BWD) Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], cc);
         wave_lds_sync();
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
-          const float2 v = *reinterpret_cast<const float2*>(&sv[wave][t][w.ch]);
+          const V v = sv[wave][t][w.ch];
           float bb[NS], ct[NS], d = 0.f;
           Vec<float, NS>::load(&sb[wave][t][n0], bb);
           if constexpr (BWD) {
             Vec<float, NS>::load(&sc[wave][t][n0], ct);
-            d = sv[wave][t][w.ch].z;
+            d = v.z;
           }
           sum += v.x;
 #pragma unroll
@@ -277,7 +260,7 @@ __global__ void __launch_bounds__(256) selective_step_kernel(const SelectiveArgs
   Vec<T, NS>::load(a.C.row<T>(row) + g * N + sg * NS, cc);
   Vec<T, 1>::load(a.x.row<T>(row) + c, &x);
   Vec<T, 1>::load(a.dt.row<T>(row) + c, &dt);
-  if (a.z.p) Vec<T, 1>::load(a.z.row<T>(row) + c, &z);
+  if (a.gated) Vec<T, 1>::load(a.z.row<T>(row) + c, &z);
   const float raw = dt + (a.dt_bias ? a.dt_bias[c] : 0.f);
   const float delta = a.softplus ? softplus(raw) : raw;
   float y = 0.f;
@@ -290,12 +273,10 @@ __global__ void __launch_bounds__(256) selective_step_kernel(const SelectiveArgs
   y = state_sum<S>(y);
   if (sg == 0) {
     if (a.D) y = fmaf(a.D[c], x, y);
-    if (a.z.p) y *= z * sigmoid(z);
+    if (a.gated) y *= z * sigmoid(z);
     store_row<T, 1>(a.out.out<T>(row) + c, &y);
   }
 }
-
-constexpr int kWaves = 4096;  // that a pass aims at
 
 // Launches a pass over the groups: f(S, NS, type, grid).
 template <typename F>
@@ -318,20 +299,38 @@ hipError_t launch_scan_pass(const ssm_selective_dims& d, SelectiveArgs& a, hipSt
 
 }  // namespace
 
-SelGroups selective_groups(const ssm_selective_dims& d, int cap) {
+// A pass takes as long as the SIMD that gets the most waves (all are alike but for the last group's): that
+// many times a group's chunks, and what a group costs beside them (its start, and a hundredth of
+// a chunk for every group that is joined). Registers let 5 waves of the forward pass and 3 of the gradients
+// stay on a SIMD; the rest waits for a place. Fewer than four leave it waiting for LDS and exps part of
+// the time: kAlone, estimated from the time of one wave a SIMD, 1.8 times that of its instructions.
+SelGroups selective_groups(const ssm_selective_dims& d, int cap, bool backward) {
   if (cap < 1) return SelGroups{1, 1};
-  const int tiles = selective_tiles(d);
-  int groups = (kWaves + tiles - 1) / tiles;
-  if (groups > cap) groups = cap;
-  int chunks = (cap + groups - 1) / groups;
-  // joining the groups before costs a group about a fortieth of a chunk each
-  while ((long long)chunks * chunks * 25 < cap) ++chunks;
-  return SelGroups{chunks, (cap + chunks - 1) / chunks};
+  constexpr int kSimds = 1024;
+  constexpr float kAlone[] = {0.f, 1.8f, 2.5f, 3.24f};  // the time of 1, 2, 3 waves
+  const int most = backward ? 3 : 5;
+  const auto time_of = [&](long long waves) { return waves < 4 ? kAlone[waves] : (float)waves; };
+  const long long tiles = selective_tiles(d);
+  SelGroups best{cap, 1};
+  float least = 0.f;
+  for (int groups = 1; groups <= cap && groups <= 4096; ++groups) {
+    const int chunks = (cap + groups - 1) / groups, used = (cap + chunks - 1) / chunks;
+    if (used < groups) continue;  // the same chunks with fewer groups
+    const long long waves = (tiles * groups + kSimds - 1) / kSimds;
+    const float cost = ((float)(waves / most) * time_of(most) + time_of(waves % most)) *
+                       (chunks + 0.5f + groups / 100.f);
+    if (groups == 1 || cost < least) {
+      least = cost;
+      best = SelGroups{chunks, groups};
+    }
+    if (waves > 10) break;
+  }
+  return best;
 }
 
 hipError_t launch_selective_local(const ssm_selective_dims& d, SelectiveArgs& a, bool backward,
                                   hipStream_t stream) {
-  const SelGroups g = selective_groups(d, a.plan.cap);
+  const SelGroups g = selective_groups(d, a.plan.cap, backward);
   a.time_groups = g.groups;
   a.group_chunks = g.chunks;
   if (g.groups == 1) return hipSuccess;
@@ -351,7 +350,7 @@ hipError_t launch_selective_states(const ssm_selective_dims& d, SelectiveArgs& a
 
 SelectiveWork selective_work(const ssm_selective_dims& d, int total, bool backward, void* base) {
   SelectiveWork w{};
-  const SelGroups g = selective_groups(d, d.batch > 0 ? scan_capacity(total, d.batch) : 0);
+  const SelGroups g = selective_groups(d, d.batch > 0 ? scan_capacity(total, d.batch) : 0, backward);
   const size_t states = (size_t)d.channels * d.d_state;
   size_t at = 0;
   auto take = [&](size_t floats) {
@@ -366,7 +365,7 @@ SelectiveWork selective_work(const ssm_selective_dims& d, int total, bool backwa
   if (backward) {
     if (g.groups > 1) w.back = take(g.groups * states);
     w.states = take(((size_t)total / TB + 1) * states);
-    w.dbc = take((size_t)total * selective_tiles(d) * 2 * d.d_state);
+    w.dbc = take(((size_t)total + 1) * selective_tiles(d) * 2 * d.d_state);
     w.partial = take((size_t)g.groups * d.channels * (d.d_state + 2));
   }
   w.bytes = at;

@@ -25,19 +25,17 @@ namespace ssm {
 constexpr int TB = 16;     // tokens of a block
 constexpr int WAVES = 4;   // of a workgroup
 
-// log(1 + e^x) = max(x, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|x| <= 1: the series to s^15 (s <= 1/3, the
-// next term below 2^-27 of the sum), so small values keep their digits. x = +inf and NaN pass through.
+// log(1 + e^x) = max(x, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|x| <= 1, so small values keep their digits.
+// atanh(s) / s as a polynomial in q = s^2 <= 1/9 whose largest relative error is the least (2^-28). x = +inf
+// and NaN pass through.
 __device__ __forceinline__ float softplus(float x) {
   const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(x));
   const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
-  float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
-  p = fmaf(q, p, 1.f / 11.f);
-  p = fmaf(q, p, 1.f / 9.f);
-  p = fmaf(q, p, 1.f / 7.f);
-  p = fmaf(q, p, 1.f / 5.f);
-  p = fmaf(q, p, 1.f / 3.f);
+  float p = fmaf(q, 0.140891671f, 0.139803007f);
+  p = fmaf(q, p, 0.200124547f);
+  p = fmaf(q, p, 0.333331585f);
   p = fmaf(q, p, 1.f);
-  return fmaf(2.f * s, p, x > 0.f || x != x ? x : 0.f);
+  return fmaf(2.f * s, p, fmaxf(x, 0.f));
 }
 
 template <int S, int NS>
@@ -82,12 +80,22 @@ __device__ __forceinline__ SelTile sel_tile(const SelectiveArgs& a, int tile) {
   return w;
 }
 
-// E consecutive elements, zero where the row holds no token.
+// One value for the wave, in a scalar register (the plan is read by vector loads).
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Element `col` of row `row` (both the lane's) behind row tok0 (the wave's): a scalar base and an offset of
+// 32 bits (strides are below 2^26), so that an array's place takes one vector register, not two.
+template <typename T>
+__device__ __forceinline__ T* row_at(const Rows& m, int64_t tok0, int row, int col) {
+  char* base = static_cast<char*>(const_cast<void*>(m.p)) + tok0 * m.stride * (int64_t)sizeof(T);
+  const uint32_t off = (uint32_t)row * (uint32_t)(m.stride * sizeof(T)) + (uint32_t)col * (uint32_t)sizeof(T);
+  return reinterpret_cast<T*>(base + off);
+}
+
 template <typename T, int E>
-__device__ __forceinline__ void load_or_zero(Packed<T, E>& r, const T* p, bool on) {
+__device__ __forceinline__ void mask_out(Packed<T, E>& r, uint32_t mask) {
 #pragma unroll
-  for (int i = 0; i < Packed<T, E>::NW; ++i) r.w[i] = 0u;
-  if (on) r.load(p);
+  for (int i = 0; i < Packed<T, E>::NW; ++i) r.w[i] &= mask;
 }
 
 template <typename T, int E>
@@ -115,10 +123,16 @@ __device__ __forceinline__ bool sel_slot(const SelectiveArgs& a, int seq, int& s
   return slot >= 0 && slot < a.num_slots;
 }
 __device__ __forceinline__ bool sel_cell(const SelectiveArgs& a, int e, SelCell& c) {
-  if (!a.plan.locate(e, c.seq, c.first, c.len, c.pos)) return false;
+  c = SelCell{};
+  int ok = a.plan.locate(e, c.seq, c.first, c.len, c.pos) && sel_slot(a, c.seq, c.slot);
   c.entry = e;
+  c.seq = scalar(c.seq);
+  c.slot = scalar(c.slot);
+  c.first = scalar(c.first);
+  c.len = scalar(c.len);
+  c.pos = scalar(c.pos);
   c.count = min(c.len - c.pos, CT);
-  return sel_slot(a, c.seq, c.slot);
+  return scalar(ok);
 }
 // The first such chunk in [e, end), or in (end, e] going down.
 __device__ __forceinline__ bool next_cell(const SelectiveArgs& a, int e, int end, SelCell& c) {
@@ -167,6 +181,66 @@ __device__ __forceinline__ void zero(float (&h)[NS]) {
   for (int i = 0; i < NS; ++i) h[i] = 0.f;
 }
 
+// One block of a sequence: raw inputs of the lane's token, zero where there is none (the block's last row is
+// read all the same and masked out: a branch around every load costs more).
+template <typename T, int S, int NS, bool C, bool Z, bool DY>
+struct SelBlock {
+  using SH = SelShape<S, NS>;
+  Packed<T, SH::EC> x, dt, z, dy;
+  Packed<T, SH::EN> b, c;
+  __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0) {
+    const int64_t tok0 = (int64_t)cell.first + cell.pos + t0;
+    const int left = cell.count - t0, row = min(w.t, left - 1);
+    const int c0 = w.c0 + w.q * SH::EC, n0 = w.group * SH::N + w.q * SH::EN;
+    x.load(row_at<T>(a.x, tok0, row, c0));
+    dt.load(row_at<T>(a.dt, tok0, row, c0));
+    b.load(row_at<T>(a.B, tok0, row, n0));
+    if constexpr (Z) z.load(row_at<T>(a.z, tok0, row, c0));  // x where there is no gate
+    if constexpr (C) c.load(row_at<T>(a.C, tok0, row, n0));
+    if constexpr (DY) dy.load(row_at<T>(a.dout, tok0, row, c0));
+    if (left < TB) {
+      const uint32_t mask = w.t < left ? 0xFFFFFFFFu : 0u;
+      mask_out(x, mask);
+      mask_out(dt, mask);
+      mask_out(b, mask);
+      if constexpr (Z) mask_out(z, mask);
+      if constexpr (C) mask_out(c, mask);
+      if constexpr (DY) mask_out(dy, mask);
+    }
+  }
+};
+
+// Steps and gates of a lane's channels. One branch of the wave for all of them: a branch for each value
+// costs more than the value.
+template <int E>
+__device__ __forceinline__ void steps(const SelectiveArgs& a, const float (&raw)[E], bool whole, bool on,
+                                      float (&delta)[E]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) delta[i] = raw[i];
+  if (a.softplus) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) delta[i] = softplus(raw[i]);
+  }
+  if (!whole) {  // rows without a token leave the state as it is
+#pragma unroll
+    for (int i = 0; i < E; ++i) delta[i] = on ? delta[i] : 0.f;
+  }
+}
+template <int E>
+__device__ __forceinline__ void apply_gate(const SelectiveArgs& a, const float (&z)[E], float (&v)[E]) {
+  if (a.gated) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] *= z[i] * sigmoid(z[i]);
+  }
+}
+
+// A channel parameter of the wave's tile in LDS, zero where there is none: read by every block, and registers
+// are short.
+template <int CH>
+__device__ __forceinline__ void stage_channels(float (&to)[CH], const float* from, const SelTile& w) {
+  if (w.lane < CH) to[w.lane] = from ? from[w.c0 + w.lane] : 0.f;
+}
+
 // The state before the group's first chunk c, which is not its sequence's first: the groups before.
 template <int N, int NS>
 __device__ __forceinline__ void carry_in(const SelectiveArgs& a, const SelGroup& g, const SelCell& c, int my,
@@ -201,11 +275,11 @@ __device__ __forceinline__ void carry_back(const SelectiveArgs& a, const SelGrou
   }
 }
 
-// Groups of the chunk table for a wave count that fills the GPU.
+// Groups of the chunk table: chunks of a group, and their number.
 struct SelGroups {
   int chunks, groups;
 };
-SelGroups selective_groups(const ssm_selective_dims& d, int cap);
+SelGroups selective_groups(const ssm_selective_dims& d, int cap, bool backward);
 
 // The local pass; sets a's groups.
 hipError_t launch_selective_local(const ssm_selective_dims& d, SelectiveArgs& a, bool backward,

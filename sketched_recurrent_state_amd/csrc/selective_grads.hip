@@ -15,59 +15,87 @@ namespace ssm {
 namespace {
 
 template <typename T, int S, int NS>
-struct GradBlock {
+struct GradBlock : SelBlock<T, S, NS, true, true, true> {
   using SH = SelShape<S, NS>;
-  Packed<T, SH::EC> x, dt, z, dy;
-  Packed<T, SH::EN> b, c;
   float h0[NS];  // the state before the block
   __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0,
                                        int my, int n) {
-    const bool on = t0 + w.t < cell.count;
-    const int64_t tok = (int64_t)cell.first + cell.pos + t0 + w.t;
-    const int c0 = w.c0 + w.q * SH::EC, n0 = w.group * SH::N + w.q * SH::EN;
-    load_or_zero(x, a.x.row<T>(tok) + c0, on);
-    load_or_zero(dt, a.dt.row<T>(tok) + c0, on);
-    load_or_zero(dy, a.dout.row<T>(tok) + c0, on);
-    load_or_zero(z, a.z.p ? a.z.row<T>(tok) + c0 : nullptr, on && a.z.p);
-    load_or_zero(b, a.B.row<T>(tok) + n0, on);
-    load_or_zero(c, a.C.row<T>(tok) + n0, on);
+    SelBlock<T, S, NS, true, true, true>::load(a, w, cell, t0);
+    const uint32_t at = (uint32_t)(my * SH::N + n);
     if (cell.pos + t0 > 0) {
       const size_t block = (size_t)(cell.first / TB + (cell.pos + t0) / TB - 1);
-      Vec<float, NS>::load(a.w.states + (block * a.channels + my) * SH::N + n, h0);
+      Vec<float, NS>::load(a.w.states + block * a.channels * SH::N + at, h0);
     } else if (a.state_in) {
-      Vec<float, NS>::load(a.state_in + ((size_t)cell.slot * a.channels + my) * SH::N + n, h0);
+      Vec<float, NS>::load(a.state_in + (size_t)cell.slot * a.channels * SH::N + at, h0);
     } else {
       zero(h0);
     }
   }
 };
 
+// Sums of v[0 .. V) over the lanes that share lane % S, by halving: every step adds two lanes' values
+// and gives each half of the lanes half of the values. Afterwards v[0 .. kHalved) of a lane are
+// v[halved_at ..) of all lanes. V = 2 NS values take 16 instructions instead of 48 (S = 4).
+template <int S, int V>
+__device__ __forceinline__ void channel_halve(float (&v)[V], int lane) {
+  constexpr int V1 = V / 2, V2 = V / 4, V3 = V / 8;
+#pragma unroll
+  for (int i = 0; i < V1; ++i) halve32(v[i], v[i + V1]);
+#pragma unroll
+  for (int i = 0; i < V2; ++i) halve16(v[i], v[i + V2]);
+  if constexpr (S <= 8) {
+    if constexpr (V3 > 0) {
+#pragma unroll
+      for (int i = 0; i < V3; ++i) v[i] = halve8(v[i], v[i + V3], lane & 8);
+    } else {
+      v[0] += dpp<DPP_ROR8>(v[0]);
+    }
+  }
+  if constexpr (S <= 4) v[0] += dpp<DPP_ROR4>(v[0]);
+}
+template <int S, int V>
+__device__ __forceinline__ int halved_at(int lane) {
+  return (lane & 32 ? V / 2 : 0) + (lane & 16 ? V / 4 : 0) + (S <= 8 && (lane & 8) ? V / 8 : 0);
+}
+template <int S, int V>
+constexpr int kHalved = S == 16 ? V / 4 : V >= 8 ? V / 8 : 1;  // values a lane is left with
+
+__device__ __forceinline__ void store3(float4* p, const float (&v)[3]) {
+  *reinterpret_cast<float3*>(p) = make_float3(v[0], v[1], v[2]);
+}
+
+constexpr int HB = TB / 2;  // tokens whose states are in registers at once
+
+// A block's states are computed from the one before it: for its later half (through the first, whose
+// states are not kept), then for the first. 16 tokens' states and decays would take 128 registers and
+// leave one wave a SIMD.
 template <int S, int NS, typename T>
-__global__ void __launch_bounds__(64 * WAVES) selective_grads_kernel(const SelectiveArgs a) {
+__global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const SelectiveArgs a) {
   using SH = SelShape<S, NS>;
-  constexpr int N = SH::N, CH = SH::CH, EC = SH::EC, EN = SH::EN;
-  __shared__ __align__(16) float4 sv[WAVES][TB][CH];  // delta, delta x, dL/dy, -
+  constexpr int N = SH::N, CH = SH::CH, EC = SH::EC, EN = SH::EN, KEEP = (HB + S - 1) / S;
+  // rows of CH + 1: one of 16 channels would start in the same bank as the last
+  __shared__ __align__(16) float4 sv[WAVES][TB][CH + 1];  // delta, delta x, dL/dy, x
+  __shared__ __align__(16) float4 so[WAVES][TB][CH + 1];  // sum G B, sum G a h A / ln 2, y, d delta / d dt
   __shared__ __align__(16) float sb[WAVES][TB][N], sc[WAVES][TB][N];
-  __shared__ __align__(16) float4 so[WAVES][TB][CH];  // sum G B, sum G a h A, y
-  const int wave = threadIdx.x >> 6, tiles = a.channels / CH;
+  __shared__ __align__(16) float sz[WAVES][TB][CH];       // dL/dout times the gate's derivative
+  __shared__ __align__(16) float sbias[WAVES][CH], sskip[WAVES][CH];
+  const int wave = scalar(threadIdx.x >> 6), tiles = a.channels / CH;
   const int tile_blocks = (tiles + WAVES - 1) / WAVES;
   const int tile = blockIdx.x % tile_blocks * WAVES + wave;
   if (tile >= tiles) return;
   const SelTile w = sel_tile<S>(a, tile);
   const SelGroup grp = sel_group(a, blockIdx.x / tile_blocks);
   const int my = w.c0 + w.ch, n0 = w.sg * NS;
-  float A[NS], A2[NS], dA[NS], bias[EC], skip[EC], dD[EC], dbias[EC];
-  Vec<float, NS>::load(a.A + (size_t)my * N + n0, A);
+  float A2[NS], dA[NS], dD[EC], dbias[EC];
+  Vec<float, NS>::load(a.A + (size_t)my * N + n0, A2);
   zero(dA);
   zero(dD);
   zero(dbias);
 #pragma unroll
-  for (int i = 0; i < NS; ++i) A2[i] = kLog2e * A[i];
-#pragma unroll
-  for (int i = 0; i < EC; ++i) {
-    bias[i] = a.dt_bias ? a.dt_bias[w.c0 + w.q * EC + i] : 0.f;
-    skip[i] = a.D ? a.D[w.c0 + w.q * EC + i] : 0.f;
-  }
+  for (int i = 0; i < NS; ++i) A2[i] *= kLog2e;
+  stage_channels(sbias[wave], a.dt_bias, w);
+  stage_channels(sskip[wave], a.D, w);
+  wave_lds_sync();
   if (a.dstate_in)
     for_empty_sequences(a, grp, [&](int, int slot) {
       const size_t at = ((size_t)slot * a.channels + my) * N + n0;
@@ -76,111 +104,166 @@ __global__ void __launch_bounds__(64 * WAVES) selective_grads_kernel(const Selec
       if (a.dstate) Vec<float, NS>::load(a.dstate + at, v);
       Vec<float, NS>::store(a.dstate_in + at, v);
     });
+  // the lane's place among dB and dC of a token and tile: its values are dB of its NS states, then dC
+  const int kept = halved_at<S, 2 * NS>(w.lane);
+  const uint32_t dbc_at = (uint32_t)((kept < NS ? 0 : N - NS) + n0 + kept);
   SelCell cell, ahead;
   bool more = prev_cell(a, grp.e1 - 1, grp.e0 - 1, cell);
   float g[NS];
   zero(g);
-  if (more && !cell.ends()) carry_back<N>(a, grp, cell, my, n0, A2, g);
+  GradBlock<T, S, NS> next;
+  if (more) {
+    if (!cell.ends()) carry_back<N>(a, grp, cell, my, n0, A2, g);
+    next.load(a, w, cell, (cell.count - 1) / TB * TB, my, n0);
+  }
   for (; more; cell = ahead) {
     more = prev_cell(a, cell.entry - 1, grp.e0 - 1, ahead);
-    const size_t at = ((size_t)cell.slot * a.channels + my) * N + n0;
+    const size_t at = (size_t)cell.slot * a.channels * N + (uint32_t)(my * N + n0);
     if (cell.ends()) {
       zero(g);
       if (a.dstate) Vec<float, NS>::load(a.dstate + at, g);
     }
     for (int t0 = (cell.count - 1) / TB * TB; t0 >= 0; t0 -= TB) {
-      GradBlock<T, S, NS> now;
-      now.load(a, w, cell, t0, my, n0);
+      const GradBlock<T, S, NS> now = next;
+      if (t0 > 0) next.load(a, w, cell, t0 - TB, my, n0);
+      else if (more) next.load(a, w, ahead, (ahead.count - 1) / TB * TB, my, n0);
       const bool on = t0 + w.t < cell.count;
-      const int64_t tok = (int64_t)cell.first + cell.pos + t0 + w.t;
-      const float(&h0)[NS] = now.h0;
-      float x[EC], raw[EC], z[EC], dy[EC], dout[EC], b[EN], c[EN];
-      now.x.unpack(x);
-      now.dt.unpack(raw);
-      now.z.unpack(z);
-      now.dy.unpack(dout);
-      now.b.unpack(b);
-      now.c.unpack(c);
+      const int64_t tok0 = (int64_t)cell.first + cell.pos + t0;
+      {
+        float x[EC], raw[EC], delta[EC], bias[EC], z[EC], dy[EC], b[EN], c[EN];
+        now.x.unpack(x);
+        now.dt.unpack(raw);
+        now.z.unpack(z);
+        now.dy.unpack(dy);
+        now.b.unpack(b);
+        now.c.unpack(c);
+        Vec<float, EC>::load(&sbias[wave][w.q * EC], bias);
 #pragma unroll
-      for (int i = 0; i < EC; ++i) {
-        raw[i] += bias[i];
-        const float delta = on ? (a.softplus ? softplus(raw[i]) : raw[i]) : 0.f;
-        dy[i] = a.z.p ? dout[i] * (z[i] * sigmoid(z[i])) : dout[i];
-        sv[wave][w.t][w.q * EC + i] = make_float4(delta, delta * x[i], dy[i], 0.f);
-      }
-      Vec<float, EN>::store(&sb[wave][w.t][w.q * EN], b);
-      Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], c);
-      wave_lds_sync();
-      float h[TB][NS], d[TB][NS];  // states after, decays
+        for (int i = 0; i < EC; ++i) raw[i] += bias[i];
+        steps(a, raw, t0 + TB <= cell.count, on, delta);
+        if (a.gated) {
+          float dz[EC];
 #pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        const float4 v = sv[wave][t][w.ch];
-        float bb[NS];
-        Vec<float, NS>::load(&sb[wave][t][n0], bb);
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          d[t][i] = __builtin_amdgcn_exp2f(v.x * A2[i]);
-          h[t][i] = fmaf(d[t][i], t ? h[t ? t - 1 : 0][i] : h0[i], v.y * bb[i]);
+          for (int i = 0; i < EC; ++i) {
+            const float s = sigmoid(z[i]);
+            dz[i] = dy[i] * (s * fmaf(z[i], 1.f - s, 1.f));
+            dy[i] *= z[i] * s;
+          }
+          Vec<float, EC>::store(&sz[wave][w.t][w.q * EC], dz);
         }
-      }
-#pragma unroll
-      for (int t = TB - 1; t >= 0; --t) {
-        const float4 v = sv[wave][t][w.ch];
-        float bb[NS], cc[NS], dB[NS], dC[NS];
-        Vec<float, NS>::load(&sb[wave][t][n0], bb);
-        Vec<float, NS>::load(&sc[wave][t][n0], cc);
-        float e = 0.f, f = 0.f, y = 0.f;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          g[i] = fmaf(cc[i], v.z, g[i]);
-          dC[i] = v.z * h[t][i];
-          dB[i] = v.y * g[i];
-          y = fmaf(cc[i], h[t][i], y);
-          e = fmaf(bb[i], g[i], e);
-          const float p = g[i] * (d[t][i] * (t ? h[t ? t - 1 : 0][i] : h0[i]));
-          dA[i] = fmaf(v.x, p, dA[i]);
-          f = fmaf(A[i], p, f);
-          g[i] *= d[t][i];
-        }
-        e = state_sum<S>(e);
-        f = state_sum<S>(f);
-        y = state_sum<S>(y);
-        if (w.sg == 0) so[wave][t][w.ch] = make_float4(e, f, y, 0.f);
-        // every lane has read this token's B and C: the sums over channels take their place
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          dB[i] = channel_sum<S>(dB[i]);
-          dC[i] = channel_sum<S>(dC[i]);
-        }
-        wave_lds_sync();
-        if (w.ch == 0) {
-          Vec<float, NS>::store(&sb[wave][t][n0], dB);
-          Vec<float, NS>::store(&sc[wave][t][n0], dC);
-        }
-      }
-      wave_lds_sync();
-      if (on) {
-        float dx[EC], ddt[EC], dz[EC];
 #pragma unroll
         for (int i = 0; i < EC; ++i) {
-          const float4 o = so[wave][w.t][w.q * EC + i];
-          const float delta = a.softplus ? softplus(raw[i]) : raw[i];
-          dx[i] = fmaf(delta, o.x, skip[i] * dy[i]);
-          ddt[i] = fmaf(x[i], o.x, o.y) * (a.softplus ? sigmoid(raw[i]) : 1.f);
-          dbias[i] += ddt[i];
-          dD[i] = fmaf(dy[i], x[i], dD[i]);
-          const float s = sigmoid(z[i]);
-          dz[i] = dout[i] * fmaf(skip[i], x[i], o.z) * (s * fmaf(z[i], 1.f - s, 1.f));
+          sv[wave][w.t][w.q * EC + i] = make_float4(delta[i], delta[i] * x[i], dy[i], x[i]);
+          so[wave][w.t][w.q * EC + i].w = a.softplus ? sigmoid(raw[i]) : 1.f;
         }
+        Vec<float, EN>::store(&sb[wave][w.t][w.q * EN], b);
+        Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], c);
+      }
+      wave_lds_sync();
+      float h[TB / HB][NS];  // the states before each part
+#pragma unroll
+      for (int i = 0; i < NS; ++i) h[0][i] = now.h0[i];
+#pragma unroll
+      for (int part = 1; part < TB / HB; ++part) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) h[part][i] = h[part - 1][i];
+#pragma unroll
+        for (int t = (part - 1) * HB; t < part * HB; ++t) {
+          const float2 v = *reinterpret_cast<const float2*>(&sv[wave][t][w.ch]);
+          float bb[NS];
+          Vec<float, NS>::load(&sb[wave][t][n0], bb);
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+            h[part][i] = fmaf(__builtin_amdgcn_exp2f(v.x * A2[i]), h[part][i], v.y * bb[i]);
+        }
+      }
+#pragma unroll
+      for (int part = TB / HB - 1; part >= 0; --part) {
+        float keep[KEEP][3];  // lane sg keeps the tokens that are sg modulo S
+        float hs[HB + 1][NS], d[HB][NS];  // states before each token and after the last, decays
+#pragma unroll
+        for (int i = 0; i < NS; ++i) hs[0][i] = h[part][i];
+#pragma unroll
+        for (int t = 0; t < HB; ++t) {
+          const float2 v = *reinterpret_cast<const float2*>(&sv[wave][part * HB + t][w.ch]);
+          float bb[NS];
+          Vec<float, NS>::load(&sb[wave][part * HB + t][n0], bb);
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            d[t][i] = __builtin_amdgcn_exp2f(v.x * A2[i]);
+            hs[t + 1][i] = fmaf(d[t][i], hs[t][i], v.y * bb[i]);
+          }
+        }
+#pragma unroll
+        for (int t = HB - 1; t >= 0; --t) {
+          const int tb = part * HB + t;
+          const float4 v = sv[wave][tb][w.ch];
+          float bb[NS], cc[NS], sums[2 * NS];
+          Vec<float, NS>::load(&sb[wave][tb][n0], bb);
+          Vec<float, NS>::load(&sc[wave][tb][n0], cc);
+          float e = 0.f, f = 0.f, y = 0.f;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            g[i] = fmaf(cc[i], v.z, g[i]);
+            sums[i] = v.y * g[i];
+            sums[NS + i] = v.z * hs[t + 1][i];
+            y = fmaf(cc[i], hs[t + 1][i], y);
+            e = fmaf(bb[i], g[i], e);
+            g[i] *= d[t][i];
+            const float p = g[i] * hs[t][i];
+            dA[i] = fmaf(v.x, p, dA[i]);
+            f = fmaf(A2[i], p, f);
+          }
+          // dA is not used before the walk's end, so the compiler would add to it behind the whole block and keep
+          // its 16 tokens' products in registers until then (241 instead of 164)
+#pragma unroll
+          for (int i = 0; i < NS; ++i) asm volatile("" : "+v"(dA[i]));
+          e = state_sum<S>(e);
+          f = state_sum<S>(f);
+          y = state_sum<S>(y);
+          float(&k)[3] = keep[t / S];
+          const bool mine = w.sg == t % S;
+          const bool first = t == HB - 1 || t % S == S - 1;  // of the tokens that share the registers
+          k[0] = first || mine ? e : k[0];
+          k[1] = first || mine ? f : k[1];
+          k[2] = first || mine ? y : k[2];
+          // each sum is stored as it is made, by every lane that has it; rows without a token (whose sums are
+          // zero) go to a row behind the last
+          channel_halve<S>(sums, w.lane);
+          const int64_t row = t0 + tb < cell.count ? tok0 + tb : (int64_t)a.plan.total;
+          float* to = a.w.dbc + (row * tiles + tile) * 2 * N;
+#pragma unroll
+          for (int i = 0; i < kHalved<S, 2 * NS>; ++i) to[dbc_at + i] = sums[i];
+        }
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i)
+          if (S <= HB || w.sg < HB)
+            store3(&so[wave][part * HB + i * S + w.sg][w.ch], keep[i]);
+        wave_lds_sync();
+      }
+      if (on) {
+        float dx[EC], ddt[EC], skip[EC];
+        Vec<float, EC>::load(&sskip[wave][w.q * EC], skip);
         const int c0 = w.c0 + w.q * EC;
-        store_row<T, EC>(a.dx.out<T>(tok) + c0, dx);
-        store_row<T, EC>(a.ddt.out<T>(tok) + c0, ddt);
-        if (a.z.p) store_row<T, EC>(a.dz.out<T>(tok) + c0, dz);
-        float* to = a.w.dbc + ((size_t)tok * tiles + tile) * 2 * N + w.q * EN;
-        Vec<float, EN>::load(&sb[wave][w.t][w.q * EN], b);
-        Vec<float, EN>::load(&sc[wave][w.t][w.q * EN], c);
-        Vec<float, EN>::store(to, b);
-        Vec<float, EN>::store(to + N, c);
+        float ypre[EC];
+#pragma unroll
+        for (int i = 0; i < EC; ++i) {
+          const float4 v = sv[wave][w.t][w.q * EC + i], o = so[wave][w.t][w.q * EC + i];
+          dx[i] = fmaf(v.x, o.x, skip[i] * v.z);
+          ddt[i] = fmaf(v.w, o.x, kLn2 * o.y) * o.w;
+          dbias[i] += ddt[i];
+          dD[i] = fmaf(v.z, v.w, dD[i]);
+          ypre[i] = fmaf(skip[i], v.w, o.z);
+        }
+        if (a.gated) {
+          float dz[EC];
+          Vec<float, EC>::load(&sz[wave][w.t][w.q * EC], dz);
+#pragma unroll
+          for (int i = 0; i < EC; ++i) dz[i] *= ypre[i];
+          store_row<T, EC>(row_at<T>(a.dz, tok0, w.t, c0), dz);
+        }
+        store_row<T, EC>(row_at<T>(a.dx, tok0, w.t, c0), dx);
+        store_row<T, EC>(row_at<T>(a.ddt, tok0, w.t, c0), ddt);
       }
       wave_lds_sync();
     }
