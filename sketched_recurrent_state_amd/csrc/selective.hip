@@ -299,38 +299,25 @@ hipError_t launch_scan_pass(const ssm_selective_dims& d, SelectiveArgs& a, hipSt
 
 }  // namespace
 
-// A pass takes as long as the SIMD that gets the most waves (all are alike but for the last group's): that
-// many times a group's chunks, and what a group costs beside them (its start, and a hundredth of
-// a chunk for every group that is joined). Registers let 5 waves of the forward pass and 3 of the gradients
-// stay on a SIMD; the rest waits for a place. Fewer than four leave it waiting for LDS and exps part of
-// the time: kAlone, estimated from the time of one wave a SIMD, 1.8 times that of its instructions.
-SelGroups selective_groups(const ssm_selective_dims& d, int cap, bool backward) {
+// Ten waves a SIMD of the whole GPU in all (5 of the forward pass's and 3 of the gradients' are resident at
+// a time): with fewer, longer groups the last ones leave SIMDs without work. A prompt of 8192 tokens
+// x 5120 channels, by chunks of a group: 3: 342 us, 4: 330, 6: 352, 8: 349, 11: 391, 16: 448;
+// the gradients of 2 x 2048 tokens: 2: 487 us, 4: 491, 6: 579, 8: 582, 11: 617. Joining the groups before costs a
+// group about a fiftieth of a chunk each, so long prompts of few channels get longer groups.
+constexpr int kWaves = 10240;
+SelGroups selective_groups(const ssm_selective_dims& d, int cap) {
   if (cap < 1) return SelGroups{1, 1};
-  constexpr int kSimds = 1024;
-  constexpr float kAlone[] = {0.f, 1.8f, 2.5f, 3.24f};  // the time of 1, 2, 3 waves
-  const int most = backward ? 3 : 5;
-  const auto time_of = [&](long long waves) { return waves < 4 ? kAlone[waves] : (float)waves; };
-  const long long tiles = selective_tiles(d);
-  SelGroups best{cap, 1};
-  float least = 0.f;
-  for (int groups = 1; groups <= cap && groups <= 4096; ++groups) {
-    const int chunks = (cap + groups - 1) / groups, used = (cap + chunks - 1) / chunks;
-    if (used < groups) continue;  // the same chunks with fewer groups
-    const long long waves = (tiles * groups + kSimds - 1) / kSimds;
-    const float cost = ((float)(waves / most) * time_of(most) + time_of(waves % most)) *
-                       (chunks + 0.5f + groups / 100.f);
-    if (groups == 1 || cost < least) {
-      least = cost;
-      best = SelGroups{chunks, groups};
-    }
-    if (waves > 10) break;
-  }
-  return best;
+  const int tiles = selective_tiles(d);
+  int groups = (kWaves + tiles - 1) / tiles;
+  if (groups > cap) groups = cap;
+  int chunks = (cap + groups - 1) / groups;
+  while ((long long)chunks * chunks * 50 < cap) ++chunks;
+  return SelGroups{chunks, (cap + chunks - 1) / chunks};
 }
 
 hipError_t launch_selective_local(const ssm_selective_dims& d, SelectiveArgs& a, bool backward,
                                   hipStream_t stream) {
-  const SelGroups g = selective_groups(d, a.plan.cap, backward);
+  const SelGroups g = selective_groups(d, a.plan.cap);
   a.time_groups = g.groups;
   a.group_chunks = g.chunks;
   if (g.groups == 1) return hipSuccess;
@@ -350,7 +337,7 @@ hipError_t launch_selective_states(const ssm_selective_dims& d, SelectiveArgs& a
 
 SelectiveWork selective_work(const ssm_selective_dims& d, int total, bool backward, void* base) {
   SelectiveWork w{};
-  const SelGroups g = selective_groups(d, d.batch > 0 ? scan_capacity(total, d.batch) : 0, backward);
+  const SelGroups g = selective_groups(d, d.batch > 0 ? scan_capacity(total, d.batch) : 0);
   const size_t states = (size_t)d.channels * d.d_state;
   size_t at = 0;
   auto take = [&](size_t floats) {

@@ -279,7 +279,7 @@ __device__ __forceinline__ void carry_back(const SelectiveArgs& a, const SelGrou
 struct SelGroups {
   int chunks, groups;
 };
-SelGroups selective_groups(const ssm_selective_dims& d, int cap, bool backward);
+SelGroups selective_groups(const ssm_selective_dims& d, int cap);
 
 // The local pass; sets a's groups.
 hipError_t launch_selective_local(const ssm_selective_dims& d, SelectiveArgs& a, bool backward,
