@@ -1,10 +1,11 @@
 // conv.hip -- the short causal convolution of a layer's inputs, its activation and the l2 norm of
 // queries and keys, forward, backward and for single tokens (formulas in include/sketchssm.h).
 //
-// One pass over the tokens: every lane holds 8 channels (16 bytes of bf16), its taps and the last
-// K - 1 inputs in registers and walks a run of tokens, so that an input is read once (and K - 1
-// more at the start of a run) and nothing goes through LDS. Bound by HBM. A norm's run of channels
-// is 2 to 16 neighbouring lanes: its sums are DPP steps.
+// One pass over the tokens: every lane holds E channels, its taps and the last K - 1 inputs in registers
+// and walks a run of tokens, so that an input is read once (and K - 1 more at the start of a run)
+// and nothing goes through LDS. Bound by HBM. A norm's run of channels is 2 to 32 neighbouring lanes: its
+// sums are DPP steps. E = 8 forward (16 bytes of bf16 a load) and 4 backward, whose sums for the weights
+// would otherwise take 256 registers and leave one wave a SIMD.
 #include "layer.hpp"
 #include "launch.hpp"
 
@@ -14,11 +15,14 @@ namespace {
 
 constexpr int NT = 256;  // threads of a workgroup: four waves, each on runs of its own
 
+constexpr int EF = 8, EB = 4;  // channels of a lane, forward and backward
+
 // This lane's part, tile and run.
 struct ConvLane {
-  int part, run, c;  // c: first of the lane's 8 channels in the part
+  int part, run, c;  // c: first of the lane's channels in the part
   bool active;
 };
+template <int E>
 __device__ __forceinline__ ConvLane conv_lane(const ConvArgs& a) {
   int p = 0;
 #pragma unroll
@@ -30,34 +34,35 @@ __device__ __forceinline__ ConvLane conv_lane(const ConvArgs& a) {
   ConvLane l;
   l.part = p;
   l.run = (b / P.tiles * (NT >> 6) + (threadIdx.x >> 6)) * (64 >> log) + (lane >> log);
-  l.c = ((tile << log) + (lane & ((1 << log) - 1))) * 8;
+  l.c = ((tile << log) + (lane & ((1 << log) - 1))) * E;
   l.active = l.c < P.channels;
   return l;
 }
 
-// Sum over an aligned run of 2, 4, 8 or 16 lanes (all of them active).
+// Sum over an aligned run of 2, 4, .. 32 lanes (all of them active).
 __device__ __forceinline__ float run_sum(float x, int lanes) {
   x += dpp<DPP_QUAD_1032>(x);
   if (lanes >= 4) x += dpp<DPP_QUAD_2301>(x);
   if (lanes >= 8) x += dpp<DPP_HALF_MIRROR>(x);
   if (lanes >= 16) x += dpp<DPP_ROR8>(x);
+  if (lanes >= 32) x = xsum16(x);
   return x;
 }
 
-template <int K>
+template <int K, int E>
 struct Taps {
-  float w[8 * K], b[8];
+  float w[E * K], b[E];
   __device__ __forceinline__ void load(const ConvArgs& a, int c) {
-    Vec<float, 8 * K>::load(a.weight + (size_t)c * K, w);
+    Vec<float, E * K>::load(a.weight + (size_t)c * K, w);
     if (a.bias) {
-      Vec<float, 8>::load(a.bias + c, b);
+      Vec<float, E>::load(a.bias + c, b);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = 0.f;
+      for (int i = 0; i < E; ++i) b[i] = 0.f;
     }
   }
   // u of the token whose inputs are x[K - 1], the ones before it x[0 .. K - 2]
-  __device__ __forceinline__ float at(const float (*x)[8], int i) const {
+  __device__ __forceinline__ float at(const float (*x)[E], int i) const {
     float u = b[i];
 #pragma unroll
     for (int j = 0; j < K; ++j) u = fmaf(w[i * K + j], x[j][i], u);
@@ -65,22 +70,33 @@ struct Taps {
   }
 };
 
-// y of a token from its window of inputs
-template <int K>
-__device__ __forceinline__ void conv_token(const ConvArgs& a, const ConvPart& P, const Taps<K>& taps,
-                                           const float (*x)[8], float (&y)[8]) {
+template <typename T, int E>
+__device__ __forceinline__ void store_channels(T* p, const float (&v)[E]) {
+  if constexpr (E == 8) store8(p, v);
+  else store4(p, make_float4(v[0], v[1], v[2], v[3]));
+}
+template <int E>
+__device__ __forceinline__ void clear(float (&v)[E]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < E; ++i) v[i] = 0.f;
+}
+
+// y of a token from its window of inputs
+template <int K, int E>
+__device__ __forceinline__ void conv_token(const ConvArgs& a, const ConvPart& P, const Taps<K, E>& taps,
+                                           const float (*x)[E], float (&y)[E]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
     const float u = taps.at(x, i);
     y[i] = a.silu ? u * sigmoid(u) : u;
   }
   if (P.norm_lanes) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(y[i], y[i], s);
+    for (int i = 0; i < E; ++i) s = fmaf(y[i], y[i], s);
     const float r = P.scale * __builtin_amdgcn_rsqf(run_sum(s, P.norm_lanes) + a.eps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] *= r;
+    for (int i = 0; i < E; ++i) y[i] *= r;
   }
 }
 
@@ -113,28 +129,28 @@ __device__ __forceinline__ bool empty_sequence(const ConvArgs& a, int r, int& sl
 }
 
 // The K - 1 inputs before the run, oldest first: tokens of the sequence, or its kept state.
-template <int K, typename T>
+template <int K, int E, typename T>
 __device__ __forceinline__ void history(const ConvArgs& a, const ConvPart& P, const Run& run, int c,
-                                        float (*x)[8]) {
+                                        float (*x)[E]) {
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
     const int p = run.pos - (K - 1) + j;
     if (p >= 0) {
-      Vec<T, 8>::load(P.x.row<T>(run.first + p) + c, x[j]);
+      Vec<T, E>::load(P.x.row<T>(run.first + p) + c, x[j]);
     } else if (a.state_in) {
-      Vec<T, 8>::load(static_cast<const T*>(a.state_in) +
+      Vec<T, E>::load(static_cast<const T*>(a.state_in) +
                           ((size_t)run.slot * (K - 1) + (K - 1 + p)) * a.C + P.offset + c,
                       x[j]);
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
+      clear(x[j]);
     }
   }
 }
 
 template <int K, typename T>
 __global__ void __launch_bounds__(NT) conv_forward_kernel(const ConvArgs a) {
-  const ConvLane l = conv_lane(a);
+  constexpr int E = EF;
+  const ConvLane l = conv_lane<E>(a);
   if (!l.active) return;
   const ConvPart& P = a.part[l.part];
   const int c = l.c;
@@ -144,43 +160,44 @@ __global__ void __launch_bounds__(NT) conv_forward_kernel(const ConvArgs a) {
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       const size_t at = ((size_t)slot * (K - 1) + j) * a.C + P.offset + c;
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (a.state_in) Vec<T, 8>::load(static_cast<const T*>(a.state_in) + at, v);
-      store8(static_cast<T*>(a.state) + at, v);
+      float v[E];
+      clear(v);
+      if (a.state_in) Vec<T, E>::load(static_cast<const T*>(a.state_in) + at, v);
+      store_channels(static_cast<T*>(a.state) + at, v);
     }
   }
   Run run;
   if (!conv_run(a, l.run, run)) return;
-  Taps<K> taps;
+  Taps<K, E> taps;
   taps.load(a, P.offset + c);
-  float x[K - 1 + U][8];
-  history<K, T>(a, P, run, c, x);
+  float x[K - 1 + U][E];
+  history<K, E, T>(a, P, run, c, x);
   if (run.pos == 0 && a.state) {
     // the last K - 1 of the kept inputs and the sequence's; read before they are written, since
     // both may be the same memory: only this lane touches them
     const int len = run.len;
-    float end[K - 1][8];
+    float end[K - 1][E];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       const int p = len - (K - 1) + j;
       if (p >= 0) {
-        Vec<T, 8>::load(P.x.row<T>(run.first + p) + c, end[j]);
+        Vec<T, E>::load(P.x.row<T>(run.first + p) + c, end[j]);
       } else {
 #pragma unroll
         for (int h = 0; h < K - 1; ++h)
           if (K - 1 + p == h)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) end[j][i] = x[h][i];
+            for (int i = 0; i < E; ++i) end[j][i] = x[h][i];
       }
     }
 #pragma unroll
     for (int j = 0; j < K - 1; ++j)
-      store8(static_cast<T*>(a.state) + ((size_t)run.slot * (K - 1) + j) * a.C + P.offset + c, end[j]);
+      store_channels(static_cast<T*>(a.state) + ((size_t)run.slot * (K - 1) + j) * a.C + P.offset + c, end[j]);
   }
   const T* in = P.x.row<T>(run.first + run.pos) + c;
   T* out = P.y.out<T>(run.first + run.pos) + c;
   for (int t = 0; t < run.count; t += U) {
-    Packed<T, 8> raw[U];
+    Packed<T, E> raw[U];
 #pragma unroll
     for (int i = 0; i < U; ++i)
       if (t + i < run.count) raw[i].load(in + (int64_t)(t + i) * P.x.stride);
@@ -188,15 +205,15 @@ __global__ void __launch_bounds__(NT) conv_forward_kernel(const ConvArgs a) {
     for (int i = 0; i < U; ++i) {
       if (t + i < run.count) {
         raw[i].unpack(x[K - 1 + i]);
-        float y[8];
-        conv_token<K>(a, P, taps, x + i, y);
-        store8(out + (int64_t)(t + i) * P.y.stride, y);
+        float y[E];
+        conv_token(a, P, taps, x + i, y);
+        store_channels(out + (int64_t)(t + i) * P.y.stride, y);
       }
     }
 #pragma unroll
     for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = x[U + j][i];
+      for (int i = 0; i < E; ++i) x[j][i] = x[U + j][i];
   }
 }
 
@@ -205,118 +222,123 @@ __global__ void __launch_bounds__(NT) conv_forward_kernel(const ConvArgs a) {
 // makes the gradient of the kept inputs on the way.
 template <int K, typename T>
 __global__ void __launch_bounds__(NT) conv_backward_kernel(const ConvArgs a) {
-  const ConvLane l = conv_lane(a);
+  constexpr int E = EB, U = 4;
+  const ConvLane l = conv_lane<E>(a);
   if (!l.active || l.run >= a.rows) return;
   const ConvPart& P = a.part[l.part];
   const int c = l.c;
-  constexpr int U = 4;
-  Taps<K> taps;
+  Taps<K, E> taps;
   taps.load(a, P.offset + c);
-  float dw[8 * K], db[8];
-#pragma unroll
-  for (int i = 0; i < 8 * K; ++i) dw[i] = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) db[i] = 0.f;
+  float dw[E * K], db[E];
+  clear(dw);
+  clear(db);
   for (int r = l.run; r < a.runs; r += a.rows) {
     int slot;
     if (a.dstate_in && empty_sequence(a, r, slot)) {
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) {
         const size_t at = ((size_t)slot * (K - 1) + j) * a.C + P.offset + c;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (a.dstate) Vec<T, 8>::load(static_cast<const T*>(a.dstate) + at, v);
-        store8(static_cast<T*>(a.dstate_in) + at, v);
+        float v[E];
+        clear(v);
+        if (a.dstate) Vec<T, E>::load(static_cast<const T*>(a.dstate) + at, v);
+        store_channels(static_cast<T*>(a.dstate_in) + at, v);
       }
     }
     Run run;
     if (!conv_run(a, r, run)) continue;
-    float x[K - 1 + U][8], g[K - 1 + U][8];  // g[K - 1 + i]: of token t + i
-    history<K, T>(a, P, run, c, x);
+    float x[K - 1 + U][E], g[K - 1 + U][E];  // [K - 1 + i]: of token t + i
+    history<K, E, T>(a, P, run, c, x);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[j][i] = 0.f;
+    for (int j = 0; j < K - 1; ++j) clear(g[j]);
     const int left = run.len - run.pos;           // tokens up to the sequence's end
-    const int steps = run.count + K - 1;
+    const int steps = run.count + K - 1, with_g = min(steps, left);
     const int64_t t0 = (int64_t)run.first + run.pos;
-    for (int t = 0; t < steps; t += U) {
-      Packed<T, 8> rx[U], ry[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (t + i < steps && t + i < left) {
-          rx[i].load(P.x.row<T>(t0 + t + i) + c);
-          ry[i].load(P.dy.row<T>(t0 + t + i) + c);
-        }
+    Packed<T, E> rx[U], ry[U];
+    const auto fetch = [&](int t) {  // rows behind the last are read again, and not used
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        float(&gt)[8] = g[K - 1 + i];
-        if (t + i < steps && t + i < left) {
-          float dy[8], act[8], slope[8];
-          rx[i].unpack(x[K - 1 + i]);
-          ry[i].unpack(dy);
+        const int64_t at = t0 + min(t + i, with_g - 1);
+        rx[i].load(P.x.row<T>(at) + c);
+        ry[i].load(P.dy.row<T>(at) + c);
+      }
+    };
+    fetch(0);
+    for (int t = 0; t < steps; t += U) {
+      float dys[U][E];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float u = taps.at(x + i, e);
-            const float s = a.silu ? sigmoid(u) : 1.f;
+      for (int i = 0; i < U; ++i) {
+        rx[i].unpack(x[K - 1 + i]);
+        ry[i].unpack(dys[i]);
+      }
+      if (t + U < steps) fetch(t + U);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        float(&gt)[E] = g[K - 1 + i];
+        float(&dy)[E] = dys[i];
+        float act[E], slope[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float u = taps.at(x + i, e);
+          act[e] = u;
+          slope[e] = 1.f;
+          if (a.silu) {
+            const float s = sigmoid(u);
             act[e] = u * s;
-            slope[e] = a.silu ? s * fmaf(u, 1.f - s, 1.f) : 1.f;
+            slope[e] = s * fmaf(u, 1.f - s, 1.f);
           }
-          if (P.norm_lanes) {
-            float s = 0.f, d = 0.f;
+        }
+        if (P.norm_lanes) {
+          float s = 0.f, d = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              s = fmaf(act[e], act[e], s);
-              d = fmaf(act[e], dy[e], d);
-            }
-            const float r1 = __builtin_amdgcn_rsqf(run_sum(s, P.norm_lanes) + a.eps);
-            d = run_sum(d, P.norm_lanes) * r1 * r1;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dy[e] = P.scale * r1 * (dy[e] - act[e] * d);
+          for (int e = 0; e < E; ++e) {
+            s = fmaf(act[e], act[e], s);
+            d = fmaf(act[e], dy[e], d);
           }
+          const float r1 = __builtin_amdgcn_rsqf(run_sum(s, P.norm_lanes) + a.eps);
+          d = run_sum(d, P.norm_lanes) * r1 * r1;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) gt[e] = dy[e] * slope[e];
-          if (t + i < run.count) {
+          for (int e = 0; e < E; ++e) dy[e] = P.scale * r1 * (dy[e] - act[e] * d);
+        }
+        const bool here = t + i < with_g;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              db[e] += gt[e];
+        for (int e = 0; e < E; ++e) gt[e] = here ? dy[e] * slope[e] : 0.f;
+        if (t + i < run.count) {
 #pragma unroll
-              for (int j = 0; j < K; ++j) dw[e * K + j] = fmaf(gt[e], x[i + j][e], dw[e * K + j]);
-            }
+          for (int e = 0; e < E; ++e) {
+            db[e] += gt[e];
+#pragma unroll
+            for (int j = 0; j < K; ++j) dw[e * K + j] = fmaf(gt[e], x[i + j][e], dw[e * K + j]);
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) gt[e] = 0.f;
         }
         // dx of the token K - 1 back
         const int s = t + i - (K - 1), p = run.pos + s;
         if (t + i < steps && (s >= 0 || (run.pos == 0 && a.dstate_in))) {
-          float dx[8];
+          float dx[E];
           const int end = p - (run.len - (K - 1));  // its row in the final state, if any
           if (a.dstate && end >= 0 && end < K - 1) {
-            Vec<T, 8>::load(static_cast<const T*>(a.dstate) +
+            Vec<T, E>::load(static_cast<const T*>(a.dstate) +
                                 ((size_t)run.slot * (K - 1) + end) * a.C + P.offset + c,
                             dx);
           } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dx[e] = 0.f;
+            clear(dx);
           }
 #pragma unroll
           for (int j = 0; j < K; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dx[e] = fmaf(taps.w[e * K + j], g[K - 1 + i - j][e], dx[e]);
+            for (int e = 0; e < E; ++e) dx[e] = fmaf(taps.w[e * K + j], g[K - 1 + i - j][e], dx[e]);
           if (s >= 0) {
-            store8(P.dx.out<T>(t0 + s) + c, dx);
+            store_channels(P.dx.out<T>(t0 + s) + c, dx);
           } else {
-            store8(static_cast<T*>(a.dstate_in) + ((size_t)run.slot * (K - 1) + t + i) * a.C +
-                       P.offset + c,
-                   dx);
+            store_channels(static_cast<T*>(a.dstate_in) + ((size_t)run.slot * (K - 1) + t + i) * a.C +
+                               P.offset + c,
+                           dx);
           }
         }
       }
 #pragma unroll
       for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < E; ++e) {
           x[j][e] = x[U + j][e];
           g[j][e] = g[U + j][e];
         }
@@ -325,12 +347,12 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(const ConvArgs a) {
   float* row = a.partial + (size_t)l.run * (K + 1) * a.C + P.offset + c;
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    float v[8];
+    float v[E];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = dw[e * K + j];
-    store8(row + (size_t)j * a.C, v);
+    for (int e = 0; e < E; ++e) v[e] = dw[e * K + j];
+    store_channels(row + (size_t)j * a.C, v);
   }
-  store8(row + (size_t)K * a.C, db);
+  store_channels(row + (size_t)K * a.C, db);
 }
 
 // The sums over the rows of partial sums, in a fixed order: 64 columns by 16 runs of rows a workgroup.
@@ -358,22 +380,23 @@ conv_sum_kernel(const float* __restrict__ partial, int rows, int K, int C, float
 
 template <int K, typename T>
 __global__ void __launch_bounds__(NT) conv_step_kernel(const ConvArgs a) {
-  const ConvLane l = conv_lane(a);
+  constexpr int E = EF;
+  const ConvLane l = conv_lane<E>(a);
   int slot;
   if (!l.active || l.run >= a.runs || !slot_of(a, l.run, slot)) return;
   const ConvPart& P = a.part[l.part];
   T* state = static_cast<T*>(a.state) + (size_t)slot * (K - 1) * a.C + P.offset + l.c;
-  Packed<T, 8> raw[K];
+  Packed<T, E> raw[K];
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) raw[j].load(state + (size_t)j * a.C);
   raw[K - 1].load(P.x.row<T>(l.run) + l.c);
-  Taps<K> taps;
+  Taps<K, E> taps;
   taps.load(a, P.offset + l.c);
-  float x[K][8], y[8];
+  float x[K][E], y[E];
 #pragma unroll
   for (int j = 0; j < K; ++j) raw[j].unpack(x[j]);
-  conv_token<K>(a, P, taps, x, y);
-  store8(P.y.out<T>(l.run) + l.c, y);
+  conv_token(a, P, taps, x, y);
+  store_channels(P.y.out<T>(l.run) + l.c, y);
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) raw[j + 1].store(state + (size_t)j * a.C);
 }
@@ -393,17 +416,18 @@ hipError_t conv_dispatch(const ssm_conv_dims& d, F&& f) {
   return hipErrorInvalidValue;
 }
 
-// Tiles of the parts; returns the grid for `runs` runs of a tile.
+// Tiles of the parts, with E channels a lane; returns the grid for `runs` runs of a tile.
+template <int E>
 unsigned conv_grid(ConvArgs& a, int runs) {
   unsigned blocks = 0;
   for (int p = 0; p < a.parts; ++p) {
     ConvPart& P = a.part[p];
     int log = 1;
-    while (log < 6 && (8 << log) < P.channels) ++log;
-    // a norm's run stays inside a tile
-    while ((1 << log) < P.norm_lanes) ++log;
+    while (log < 6 && (E << log) < P.channels) ++log;
+    P.norm_lanes = P.norm / E;
+    while ((1 << log) < P.norm_lanes) ++log;  // a norm's run stays inside a tile
     P.log_lanes = log;
-    P.tiles = (P.channels + (8 << log) - 1) / (8 << log);
+    P.tiles = (P.channels + (E << log) - 1) / (E << log);
     P.first_block = (int)blocks;
     const int at_once = (NT >> 6) * (64 >> log);
     blocks += (unsigned)P.tiles * (unsigned)((runs + at_once - 1) / at_once);
@@ -413,9 +437,10 @@ unsigned conv_grid(ConvArgs& a, int runs) {
 
 constexpr int kWaves = 2048;  // of the whole GPU, below which runs are made shorter
 
-int run_log(int cap, int C) {
+// log2 of the tokens of a run, for waves of `wide` channels
+int run_log(int cap, int C, int wide) {
   int log = 6;
-  while (log > 3 && ((long long)cap << (6 - log)) * ((C + 511) / 512) < kWaves) --log;
+  while (log > 3 && ((long long)cap << (6 - log)) * ((C + wide - 1) / wide) < kWaves) --log;
   return log;
 }
 
@@ -432,14 +457,14 @@ int channels_of(const ssm_conv_dims& d) {
 
 size_t conv_workspace(const ssm_conv_dims& d, int total) {
   const int C = channels_of(d), cap = scan_capacity(total, d.batch);
-  const int log = run_log(cap, C);
+  const int log = run_log(cap, C, 64 * EB);
   return (size_t)partial_rows(cap << (6 - log)) * (d.taps + 1) * C * sizeof(float);
 }
 
 hipError_t launch_conv_forward(const ssm_conv_dims& d, ConvArgs& a, hipStream_t stream) {
-  a.log_run = run_log(a.plan.cap, a.C);
+  a.log_run = run_log(a.plan.cap, a.C, 64 * EF);
   a.runs = a.plan.cap << (6 - a.log_run);
-  const unsigned grid = conv_grid(a, a.runs);
+  const unsigned grid = conv_grid<EF>(a, a.runs);
   return conv_dispatch(d, [&](auto K, auto T) {
     hipLaunchKernelGGL((conv_forward_kernel<decltype(K)::value, typename decltype(T)::type>),
                        dim3(grid), dim3(NT), 0, stream, a);
@@ -448,10 +473,10 @@ hipError_t launch_conv_forward(const ssm_conv_dims& d, ConvArgs& a, hipStream_t 
 }
 
 hipError_t launch_conv_backward(const ssm_conv_dims& d, ConvArgs& a, hipStream_t stream) {
-  a.log_run = run_log(a.plan.cap, a.C);
+  a.log_run = run_log(a.plan.cap, a.C, 64 * EB);
   a.runs = a.plan.cap << (6 - a.log_run);
   a.rows = partial_rows(a.runs);
-  const unsigned grid = conv_grid(a, a.rows);
+  const unsigned grid = conv_grid<EB>(a, a.rows);
   return conv_dispatch(d, [&](auto K, auto T) {
     constexpr int k = decltype(K)::value;
     if (a.rows > 0) {  // no sequences: the sums of nothing are still written
@@ -469,7 +494,7 @@ hipError_t launch_conv_backward(const ssm_conv_dims& d, ConvArgs& a, hipStream_t
 
 hipError_t launch_conv_step(const ssm_conv_dims& d, ConvArgs& a, hipStream_t stream) {
   a.runs = d.batch;
-  const unsigned grid = conv_grid(a, a.runs);
+  const unsigned grid = conv_grid<EF>(a, a.runs);
   return conv_dispatch(d, [&](auto K, auto T) {
     hipLaunchKernelGGL((conv_step_kernel<decltype(K)::value, typename decltype(T)::type>),
                        dim3(grid), dim3(NT), 0, stream, a);

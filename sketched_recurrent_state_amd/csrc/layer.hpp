@@ -32,13 +32,14 @@ inline Rows rows_of(const ssm_rows& r) { return Rows{r.data, r.stride}; }
 // ---------------------------------------------------------------------------
 // convolution
 // ---------------------------------------------------------------------------
-// A part's channels over lanes: 8 channels a lane, 2^log_lanes lanes a tile (64, fewer where the
-// part is narrower), the wave's other lanes on other runs of tokens.
+// A part's channels over lanes: 2^log_lanes lanes a tile (64, fewer where the part is narrower), the
+// wave's other lanes on other runs of tokens. The last three and norm_lanes are set by the launch.
 struct ConvPart {
   Rows x, y, dy, dx;
   int channels, offset;  // its channels, and those of the parts before
-  int norm_lanes;        // lanes of a norm's run, 0: no norm
+  int norm;              // channels of a norm's run, 0: no norm
   float scale;
+  int norm_lanes;        // its lanes
   int log_lanes, tiles, first_block;
 };
 

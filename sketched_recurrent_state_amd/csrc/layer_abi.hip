@@ -139,7 +139,7 @@ ssm::ConvArgs conv_args(const ssm_conv_dims& d, int C, const ssm_rows* x, const 
     ssm::ConvPart& P = a.part[p];
     P.channels = d.channels[p];
     P.offset = offset;
-    P.norm_lanes = d.norm[p] / 8;
+    P.norm = d.norm[p];
     P.scale = d.norm[p] ? d.scale[p] : 1.f;
     if (x) P.x = ssm::rows_of(x[p]);
     if (y) P.y = ssm::rows_of(y[p]);

@@ -1,9 +1,9 @@
 // norm.hip -- the norm of a layer's outputs in groups of channels with a gate, forward and backward
 // (formulas in include/sketchssm.h).
 //
-// One pass: a group's values stay in registers between its statistics and its result. A group of
-// up to 512 channels is an aligned run of lanes of one wave (8 channels a lane), a wider one a
-// workgroup. Bound by HBM.
+// One pass: a lane holds 8 channels of a group, which stay in registers between the group's statistics
+// and its result. A group of up to 512 channels is an aligned run of lanes of one wave, a wider one a
+// workgroup of as many waves as it needs. Bound by HBM.
 #include "layer.hpp"
 #include "launch.hpp"
 
@@ -11,36 +11,46 @@ namespace ssm {
 
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 256;     // threads of a workgroup of narrow groups
 constexpr int SMALL = 512;  // the widest group of one wave
-constexpr long long kMostBlocks = 1 << 23;  // keeps a grid below 2^32 threads; then a workgroup takes several
+constexpr int MOST = 1024;  // threads of a workgroup of one wide group (8192 channels)
+constexpr long long kMostBlocks = 1 << 22;  // keeps a grid below 2^32 threads; then a workgroup takes several
 
-// Lanes of a group of the first kind.
+// Lanes of a group: a power of two of them in a wave, or (0) a workgroup.
 inline int group_lanes(int width) {
+  if (width > SMALL) return 0;
   int l = 2;
   while (8 * l < width) l *= 2;
   return l;
 }
+inline int threads_of(int width) { return width > SMALL ? (width + SMALL - 1) / SMALL * 64 : NT; }
 
 // Sum over the lanes of a group (L >= 2 aligned lanes of a wave), or over the workgroup (L = 0;
-// all threads call it).
-template <int L>
-__device__ __forceinline__ float group_sum(float x, float* sw) {
-  x += dpp<DPP_QUAD_1032>(x);
-  if constexpr (L == 0 || L >= 4) x += dpp<DPP_QUAD_2301>(x);
-  if constexpr (L == 0 || L >= 8) x += dpp<DPP_HALF_MIRROR>(x);
-  if constexpr (L == 0 || L >= 16) x += dpp<DPP_ROR8>(x);
-  if constexpr (L == 0 || L >= 32) x = xsum16(x);
-  if constexpr (L == 0 || L >= 64) x = xsum32(x);
+// all threads call it). N values at once.
+template <int L, int N>
+__device__ __forceinline__ void group_sum(float (&x)[N], float (*sw)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] += dpp<DPP_QUAD_1032>(x[i]);
+    if constexpr (L == 0 || L >= 4) x[i] += dpp<DPP_QUAD_2301>(x[i]);
+    if constexpr (L == 0 || L >= 8) x[i] += dpp<DPP_HALF_MIRROR>(x[i]);
+    if constexpr (L == 0 || L >= 16) x[i] += dpp<DPP_ROR8>(x[i]);
+    if constexpr (L == 0 || L >= 32) x[i] = xsum16(x[i]);
+    if constexpr (L == 0 || L >= 64) x[i] = xsum32(x[i]);
+  }
   if constexpr (L == 0) {
     __syncthreads();  // the last call's reads are done
-    if ((threadIdx.x & 63) == 0) sw[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = sw[0];
+    if ((threadIdx.x & 63) == 0)
 #pragma unroll
-    for (int i = 1; i < NT / 64; ++i) x += sw[i];
+      for (int i = 0; i < N; ++i) sw[threadIdx.x >> 6][i] = x[i];
+    __syncthreads();
+    const int waves = blockDim.x >> 6;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = sw[0][i];
+    for (int w = 1; w < waves; ++w)
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] += sw[w][i];
   }
-  return x;
 }
 
 __device__ __forceinline__ float gate_of(float z, bool sig) {
@@ -54,211 +64,191 @@ __device__ __forceinline__ float gate_of(float z, bool sig, float& slope) {
   return sig ? s : z * s;
 }
 
-// A lane's channels of a group: V runs of 8. The first is at 8 * lane, the next a workgroup's
-// channels further.
-template <int V>
-struct Cols {
-  int c[V];
-  bool on[V];
-  __device__ __forceinline__ Cols(int lane, int width) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      c[v] = 8 * (lane + v * NT);
-      on[v] = c[v] < width;
-      if (!on[v]) c[v] = 0;
-    }
-  }
-};
-
-// Mean (0 where not centred) and 1 / sqrt(var + eps) of a group's u, 0 in lanes without channels.
-template <int L, int V>
-__device__ __forceinline__ void group_stats(const NormArgs& a, const Cols<V>& k, const float (&u)[V][8],
-                                            float* sw, float& mean, float& r) {
+// Mean (0 where not centred) and 1 / sqrt(var + eps) of a group's u, which is 0 in lanes without channels.
+template <int L>
+__device__ __forceinline__ void group_stats(const NormArgs& a, bool on, const float (&u)[8], float (*sw)[1],
+                                            float& mean, float& r) {
   const float inv = 1.f / (float)a.width;
   mean = 0.f;
   if (a.centred) {
-    float s = 0.f;
+    float s[1] = {0.f};
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += u[v][i];
-    mean = group_sum<L>(s, sw) * inv;
+    for (int i = 0; i < 8; ++i) s[0] += u[i];
+    group_sum<L>(s, sw);
+    mean = s[0] * inv;
   }
-  float s = 0.f;
+  float s[1] = {0.f};
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (k.on[v])
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(u[v][i] - mean, u[v][i] - mean, s);
-  r = __builtin_amdgcn_rsqf(fmaf(group_sum<L>(s, sw), inv, a.eps));
+  for (int i = 0; i < 8; ++i) s[0] = fmaf(u[i] - mean, u[i] - mean, s[0]);
+  s[0] = on ? s[0] : 0.f;
+  group_sum<L>(s, sw);
+  r = __builtin_amdgcn_rsqf(fmaf(s[0], inv, a.eps));
 }
 
-template <int V>
-__device__ __forceinline__ void load_weights(const float* p, const Cols<V>& k, size_t at, float otherwise,
-                                             float (&w)[V][8]) {
+__device__ __forceinline__ void load_weights(const float* p, size_t at, float otherwise, float (&w)[8]) {
+  if (p) {
+    Vec<float, 8>::load(p + at, w);
+  } else {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if (p) {
-      Vec<float, 8>::load(p + at + k.c[v], w[v]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[v][i] = otherwise;
-    }
+    for (int i = 0; i < 8; ++i) w[i] = otherwise;
   }
 }
 
-// Loads x (and z): 0 in lanes without channels.
-template <typename T, int V>
-__device__ __forceinline__ void load_cols(const T* p, const Cols<V>& k, float (&x)[V][8]) {
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    Packed<T, 8> raw = {};
-    if (k.on[v]) raw.load(p + k.c[v]);
-    raw.unpack(x[v]);
+// A lane's place: its group's number in the workgroup and its first channel.
+template <int L>
+struct Place {
+  static constexpr int PER = L == 0 ? 1 : NT / (L == 0 ? 1 : L);  // groups of a workgroup
+  int group, c;
+  bool on;  // lanes past the group's width read its first channels, and do not count
+  __device__ __forceinline__ Place(int width) {
+    const int lane = L == 0 ? threadIdx.x : threadIdx.x % (L == 0 ? 1 : L);
+    group = L == 0 ? 0 : threadIdx.x / (L == 0 ? 1 : L);
+    on = 8 * lane < width;
+    c = on ? 8 * lane : 0;
   }
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack_on(const Packed<T, 8>& raw, bool on, float (&x)[8]) {
+  raw.unpack(x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = on ? x[i] : 0.f;
 }
 
-template <int L, int V, typename TX, typename T>
-__global__ void __launch_bounds__(NT) norm_kernel(const NormArgs a) {
-  __shared__ float sw[NT / 64];
-  constexpr int PER = L == 0 ? 1 : NT / (L == 0 ? 1 : L);  // groups of a workgroup
-  const int lane = L == 0 ? threadIdx.x : threadIdx.x % (L == 0 ? 1 : L);
-  const Cols<V> k(lane, a.width);
-  long long item = (long long)blockIdx.x * PER + (L == 0 ? 0 : threadIdx.x / (L == 0 ? 1 : L));
-  for (; item < (long long)a.rows * a.groups; item += (long long)gridDim.x * PER) {
+template <int L, int GATE, typename TX, typename T>
+__global__ void __launch_bounds__(L == 0 ? MOST : NT) norm_kernel(const NormArgs a) {
+  __shared__ float sw[MOST / 64][1];
+  const Place<L> k(a.width);
+  long long item = (long long)blockIdx.x * k.PER + k.group;
+  for (; item < (long long)a.rows * a.groups; item += (long long)gridDim.x * k.PER) {
     const int row = (int)(item / a.groups), g = (int)(item % a.groups);
-    const size_t at = (size_t)g * a.width, wat = a.shared ? 0 : at;
-    float x[V][8], gate[V][8], w[V][8], b[V][8];
-    load_cols<TX, V>(a.x.row<TX>(row) + at, k, x);
-    if (a.gate != SSM_GATE_NONE) {
-      load_cols<T, V>(a.z.row<T>(row) + at, k, gate);
+    const size_t at = (size_t)g * a.width + k.c, wat = a.shared ? k.c : at;
+    Packed<TX, 8> rx;
+    Packed<T, 8> rz;
+    rx.load(a.x.row<TX>(row) + at);
+    if constexpr (GATE != SSM_GATE_NONE) rz.load(a.z.row<T>(row) + at);
+    float x[8], gate[8], w[8], b[8], o[8];
+    load_weights(a.weight, wat, 1.f, w);
+    load_weights(a.bias, wat, 0.f, b);
+    unpack_on(rx, k.on, x);
+    if constexpr (GATE != SSM_GATE_NONE) {
+      unpack_on(rz, k.on, gate);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) gate[v][i] = gate_of(gate[v][i], a.sigmoid);
+      for (int i = 0; i < 8; ++i) gate[i] = gate_of(gate[i], a.sigmoid);
     }
-    load_weights<V>(a.weight, k, wat, 1.f, w);
-    load_weights<V>(a.bias, k, wat, 0.f, b);
-    if (a.gate == SSM_GATE_BEFORE) {
+    if constexpr (GATE == SSM_GATE_BEFORE) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[v][i] *= gate[v][i];
+      for (int i = 0; i < 8; ++i) x[i] *= gate[i];
     }
     float mean, r;
-    group_stats<L, V>(a, k, x, sw, mean, r);
+    group_stats<L>(a, k.on, x, sw, mean, r);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (!k.on[v]) continue;
-      float o[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[i] = fmaf((x[v][i] - mean) * r, w[v][i], b[v][i]);
-        if (a.gate == SSM_GATE_AFTER) o[i] *= gate[v][i];
-      }
-      store8(a.out.out<T>(row) + at + k.c[v], o);
+    for (int i = 0; i < 8; ++i) {
+      o[i] = fmaf((x[i] - mean) * r, w[i], b[i]);
+      if constexpr (GATE == SSM_GATE_AFTER) o[i] *= gate[i];
     }
+    if (k.on) store8(a.out.out<T>(row) + at, o);
   }
 }
 
 // Backward: a lane keeps its channels (of one group, or of every group where weights are shared) over
-// the rows that its workgroup takes, with their sums for the weights in registers.
-template <int L, int V, typename TX, typename T>
-__global__ void __launch_bounds__(NT) norm_backward_kernel(const NormArgs a) {
-  __shared__ float sw[NT / 64];
-  constexpr int PER = L == 0 ? 1 : NT / (L == 0 ? 1 : L);
-  const int lane = L == 0 ? threadIdx.x : threadIdx.x % (L == 0 ? 1 : L);
-  const int place = L == 0 ? 0 : threadIdx.x / (L == 0 ? 1 : L);
-  const Cols<V> k(lane, a.width);
+// the rows that its workgroup takes, with their sums for the weights in registers. The next row is read
+// while this one's sums go through the lanes.
+template <int L, int GATE, typename TX, typename T>
+__global__ void __launch_bounds__(L == 0 ? MOST : NT) norm_backward_kernel(const NormArgs a) {
+  __shared__ float sw[MOST / 64][1], sw2[MOST / 64][2];
+  const Place<L> k(a.width);
+  constexpr int PER = Place<L>::PER;
   // items: (row, group) where weights are shared, else the rows of one group
-  const int wgroups = a.shared ? 1 : a.groups;
-  const int tile = blockIdx.x, g0 = a.shared ? 0 : tile * PER + place;
+  const int g0 = a.shared ? 0 : (int)blockIdx.x * PER + k.group;
   const long long items = a.shared ? (long long)a.rows * a.groups : (g0 < a.groups ? a.rows : 0);
-  const int first = a.shared ? (int)blockIdx.y * PER + place : blockIdx.y;
+  const int first = a.shared ? (int)blockIdx.y * PER + k.group : blockIdx.y;
   const int stride = a.shared ? a.parts * PER : a.parts;
-  const size_t wat = a.shared ? 0 : (size_t)(g0 < a.groups ? g0 : 0) * a.width;
-  float w[V][8], b[V][8], dw[V][8], db[V][8];
-  load_weights<V>(a.weight, k, wat, 1.f, w);
-  load_weights<V>(a.bias, k, wat, 0.f, b);
+  const size_t wat = (size_t)(a.shared || g0 >= a.groups ? 0 : g0) * a.width + k.c;
+  float w[8], b[8], dw[8], db[8];
+  load_weights(a.weight, wat, 1.f, w);
+  if constexpr (GATE == SSM_GATE_AFTER) load_weights(a.bias, wat, 0.f, b);
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[v][i] = db[v][i] = 0.f;
+  for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.f;
   const float inv = 1.f / (float)a.width;
+  Packed<TX, 8> rx;
+  Packed<T, 8> rz, rd;
+  const auto place = [&](long long item, int& row, size_t& at) {
+    row = a.shared ? (int)(item / a.groups) : (int)item;
+    at = a.shared ? (size_t)(item % a.groups) * a.width + k.c : wat;
+  };
+  const auto fetch = [&](long long item) {
+    int row;
+    size_t at;
+    place(item, row, at);
+    rx.load(a.x.row<TX>(row) + at);
+    rd.load(a.dout.row<T>(row) + at);
+    if constexpr (GATE != SSM_GATE_NONE) rz.load(a.z.row<T>(row) + at);
+  };
+  if (first < items) fetch(first);
   for (long long item = first; item < items; item += stride) {
-    const int row = a.shared ? (int)(item / a.groups) : (int)item;
-    const size_t at = a.shared ? (size_t)(item % a.groups) * a.width : wat;
-    float x[V][8], u[V][8], gate[V][8], slope[V][8], d[V][8];
-    load_cols<TX, V>(a.x.row<TX>(row) + at, k, x);
-    load_cols<T, V>(a.dout.row<T>(row) + at, k, d);
-    if (a.gate != SSM_GATE_NONE) {
-      load_cols<T, V>(a.z.row<T>(row) + at, k, gate);
+    int row;
+    size_t at;
+    place(item, row, at);
+    float x[8], u[8], gate[8], slope[8], d[8], dz[8];
+    unpack_on(rx, k.on, x);
+    unpack_on(rd, k.on, d);
+    if constexpr (GATE != SSM_GATE_NONE) {
+      unpack_on(rz, k.on, gate);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) gate[v][i] = gate_of(gate[v][i], a.sigmoid, slope[v][i]);
+      for (int i = 0; i < 8; ++i) gate[i] = gate_of(gate[i], a.sigmoid, slope[i]);
     }
+    if (item + stride < items) fetch(item + stride);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        u[v][i] = a.gate == SSM_GATE_BEFORE ? x[v][i] * gate[v][i] : x[v][i];
+    for (int i = 0; i < 8; ++i) u[i] = GATE == SSM_GATE_BEFORE ? x[i] * gate[i] : x[i];
     float mean, r;
-    group_stats<L, V>(a, k, u, sw, mean, r);
-    float dz[V][8], sn = 0.f, s1 = 0.f;
+    group_stats<L>(a, k.on, u, sw, mean, r);
+    float s[2] = {0.f, 0.f};
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float n = (u[v][i] - mean) * r;
-        float o = d[v][i];
-        if (a.gate == SSM_GATE_AFTER) {
-          dz[v][i] = o * fmaf(n, w[v][i], b[v][i]) * slope[v][i];
-          o *= gate[v][i];
-        }
-        u[v][i] = n;
-        if (k.on[v]) {
-          dw[v][i] = fmaf(o, n, dw[v][i]);
-          db[v][i] += o;
-        }
-        d[v][i] = o * w[v][i];
-        if (k.on[v]) {
-          sn = fmaf(d[v][i], n, sn);
-          s1 += d[v][i];
-        }
+    for (int i = 0; i < 8; ++i) {
+      const float n = (u[i] - mean) * r;
+      float o = d[i];
+      if constexpr (GATE == SSM_GATE_AFTER) {
+        dz[i] = o * fmaf(n, w[i], b[i]) * slope[i];
+        o *= gate[i];
       }
-    sn = group_sum<L>(sn, sw) * inv;
-    s1 = a.centred ? group_sum<L>(s1, sw) * inv : 0.f;
+      u[i] = n;
+      dw[i] = fmaf(o, n, dw[i]);  // d is 0 in lanes without channels
+      db[i] += o;
+      d[i] = o * w[i];
+      s[0] = fmaf(d[i], n, s[0]);
+      s[1] += d[i];
+    }
+    group_sum<L>(s, sw2);
+    const float sn = s[0] * inv, s1 = a.centred ? s[1] * inv : 0.f;
+    float dx[8];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (!k.on[v]) continue;
-      float dx[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float du = r * (d[v][i] - u[v][i] * sn - s1);
-        if (a.gate == SSM_GATE_BEFORE) {
-          dz[v][i] = du * x[v][i] * slope[v][i];
-          dx[i] = du * gate[v][i];
-        } else {
-          dx[i] = du;
-        }
+    for (int i = 0; i < 8; ++i) {
+      const float du = r * (d[i] - u[i] * sn - s1);
+      if constexpr (GATE == SSM_GATE_BEFORE) {
+        dz[i] = du * x[i] * slope[i];
+        dx[i] = du * gate[i];
+      } else {
+        dx[i] = du;
       }
-      store8(a.dx.out<TX>(row) + at + k.c[v], dx);
-      if (a.gate != SSM_GATE_NONE) store8(a.dz.out<T>(row) + at + k.c[v], dz[v]);
+    }
+    if (k.on) {
+      store8(a.dx.out<TX>(row) + at, dx);
+      if constexpr (GATE != SSM_GATE_NONE) store8(a.dz.out<T>(row) + at, dz);
     }
   }
   // the workgroup's sums: those of its other places join the first's where weights are shared
-  const size_t cols = (size_t)wgroups * a.width;
+  const size_t cols = (size_t)(a.shared ? 1 : a.groups) * a.width;
   float* out = a.partial + (size_t)blockIdx.y * 2 * cols;
   if constexpr (L != 0) {
     if (a.shared) {
       __shared__ float sums[2][SMALL];
       for (int p = 0; p < PER; ++p) {
-        if (place == p && k.on[0])
+        if (k.group == p && k.on)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            sums[0][k.c[0] + i] = dw[0][i] + (p ? sums[0][k.c[0] + i] : 0.f);
-            sums[1][k.c[0] + i] = db[0][i] + (p ? sums[1][k.c[0] + i] : 0.f);
+            sums[0][k.c + i] = dw[i] + (p ? sums[0][k.c + i] : 0.f);
+            sums[1][k.c + i] = db[i] + (p ? sums[1][k.c + i] : 0.f);
           }
         __syncthreads();
       }
@@ -269,15 +259,12 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(const NormArgs a) {
       return;
     }
   }
-  if (!a.shared && g0 >= a.groups) return;
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (k.on[v]) {
-      store8(out + wat + k.c[v], dw[v]);
-      store8(out + cols + wat + k.c[v], db[v]);
-    }
+  if (!k.on || g0 >= a.groups) return;
+  store8(out + wat, dw);
+  store8(out + cols + wat, db);
 }
 
+// The sums over the rows of partial sums, in a fixed order.
 constexpr int RY = 16;
 __global__ void __launch_bounds__(64 * RY)
 norm_sum_kernel(const float* __restrict__ partial, int rows, int cols, float* __restrict__ dweight,
@@ -299,35 +286,34 @@ norm_sum_kernel(const float* __restrict__ partial, int rows, int cols, float* __
   else dbias[col - cols] = s;
 }
 
-// Calls f(L, V, x type, in type): lanes of a group (0: a workgroup) and runs of 8 channels a lane.
+// Calls f(lanes of a group (0: a workgroup), gate, x type, in type).
 template <typename F>
 hipError_t norm_dispatch(const ssm_norm_dims& d, F&& f) {
-  auto types = [&](auto L, auto V) -> hipError_t {
+  auto types = [&](auto L, auto G) -> hipError_t {
     if (d.x_dtype == SSM_IN_BF16) {
-      if (d.in_dtype == SSM_IN_BF16) return f(L, V, type_tag<uint16_t>{}, type_tag<uint16_t>{});
-      return f(L, V, type_tag<uint16_t>{}, type_tag<float>{});
+      if (d.in_dtype == SSM_IN_BF16) return f(L, G, type_tag<uint16_t>{}, type_tag<uint16_t>{});
+      return f(L, G, type_tag<uint16_t>{}, type_tag<float>{});
     }
-    if (d.in_dtype == SSM_IN_BF16) return f(L, V, type_tag<float>{}, type_tag<uint16_t>{});
-    return f(L, V, type_tag<float>{}, type_tag<float>{});
+    if (d.in_dtype == SSM_IN_BF16) return f(L, G, type_tag<float>{}, type_tag<uint16_t>{});
+    return f(L, G, type_tag<float>{}, type_tag<float>{});
   };
-#define SSM_CASE(l, v) return types(std::integral_constant<int, l>{}, std::integral_constant<int, v>{})
-  if (d.width <= SMALL) {
-    switch (group_lanes(d.width)) {
-      case 2: SSM_CASE(2, 1);
-      case 4: SSM_CASE(4, 1);
-      case 8: SSM_CASE(8, 1);
-      case 16: SSM_CASE(16, 1);
-      case 32: SSM_CASE(32, 1);
-      case 64: SSM_CASE(64, 1);
+  auto gates = [&](auto L) -> hipError_t {
+    switch (d.gate) {
+      case SSM_GATE_NONE: return types(L, std::integral_constant<int, SSM_GATE_NONE>{});
+      case SSM_GATE_AFTER: return types(L, std::integral_constant<int, SSM_GATE_AFTER>{});
+      case SSM_GATE_BEFORE: return types(L, std::integral_constant<int, SSM_GATE_BEFORE>{});
     }
+    return hipErrorInvalidValue;
+  };
+  switch (group_lanes(d.width)) {
+    case 0: return gates(std::integral_constant<int, 0>{});
+    case 2: return gates(std::integral_constant<int, 2>{});
+    case 4: return gates(std::integral_constant<int, 4>{});
+    case 8: return gates(std::integral_constant<int, 8>{});
+    case 16: return gates(std::integral_constant<int, 16>{});
+    case 32: return gates(std::integral_constant<int, 32>{});
+    case 64: return gates(std::integral_constant<int, 64>{});
   }
-  switch ((d.width + 8 * NT - 1) / (8 * NT)) {
-    case 1: SSM_CASE(0, 1);
-    case 2: SSM_CASE(0, 2);
-    case 3: SSM_CASE(0, 3);
-    case 4: SSM_CASE(0, 4);
-  }
-#undef SSM_CASE
   return hipErrorInvalidValue;
 }
 
@@ -336,7 +322,7 @@ struct BackwardGrid {
   int tiles, parts;
 };
 BackwardGrid backward_grid(const ssm_norm_dims& d, int rows) {
-  const int per = d.width <= SMALL ? NT / group_lanes(d.width) : 1;
+  const int lanes = group_lanes(d.width), per = lanes ? NT / lanes : 1;
   BackwardGrid b;
   b.tiles = d.shared ? 1 : (d.groups + per - 1) / per;
   const long long items = d.shared ? ((long long)rows * d.groups + per - 1) / per : rows;
@@ -353,12 +339,13 @@ size_t norm_workspace(const ssm_norm_dims& d, int rows) {
 }
 
 hipError_t launch_norm(const ssm_norm_dims& d, const NormArgs& a, hipStream_t stream) {
-  return norm_dispatch(d, [&](auto L, auto V, auto TX, auto T) {
-    constexpr int l = decltype(L)::value, per = l == 0 ? 1 : NT / (l == 0 ? 1 : l);
+  return norm_dispatch(d, [&](auto L, auto G, auto TX, auto T) {
+    constexpr int l = decltype(L)::value, per = Place<l>::PER;
     const long long blocks = ((long long)a.rows * a.groups + per - 1) / per;
-    hipLaunchKernelGGL((norm_kernel<l, decltype(V)::value, typename decltype(TX)::type,
+    hipLaunchKernelGGL((norm_kernel<l, decltype(G)::value, typename decltype(TX)::type,
                                     typename decltype(T)::type>),
-                       dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3(NT), 0, stream, a);
+                       dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)),
+                       dim3(threads_of(d.width)), 0, stream, a);
     return hipGetLastError();
   });
 }
@@ -366,10 +353,10 @@ hipError_t launch_norm(const ssm_norm_dims& d, const NormArgs& a, hipStream_t st
 hipError_t launch_norm_backward(const ssm_norm_dims& d, NormArgs& a, hipStream_t stream) {
   const BackwardGrid b = backward_grid(d, a.rows);
   a.parts = b.parts;
-  return norm_dispatch(d, [&](auto L, auto V, auto TX, auto T) {
-    hipLaunchKernelGGL((norm_backward_kernel<decltype(L)::value, decltype(V)::value,
+  return norm_dispatch(d, [&](auto L, auto G, auto TX, auto T) {
+    hipLaunchKernelGGL((norm_backward_kernel<decltype(L)::value, decltype(G)::value,
                                              typename decltype(TX)::type, typename decltype(T)::type>),
-                       dim3((unsigned)b.tiles, (unsigned)b.parts), dim3(NT), 0, stream, a);
+                       dim3((unsigned)b.tiles, (unsigned)b.parts), dim3(threads_of(d.width)), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int cols = (a.shared ? 1 : a.groups) * a.width;
