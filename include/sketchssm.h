@@ -479,7 +479,8 @@ ssm_status ssm_stream_probe(float* buf, int64_t n_tiles, int32_t shape, void* st
  * least the width, a multiple of 8 and below 2^26. Outputs must not overlap inputs or each other;
  * column ranges of one array (the same stride) do not overlap. Weights are fp32.
  * Sums, states and statistics are fp32; results in bf16 are rounded once, to nearest. Results are the
- * same bits from run to run.
+ * same bits from run to run. A plan that ssm_scan_plan did not write gives wrong results, but nothing outside
+ * the arrays is touched, whatever it holds.
  */
 typedef struct {
   void* data;

@@ -138,26 +138,6 @@ class NormDims(ctypes.Structure):
                    int(shared), int(centred), eps)
 
 
-class _Rows(ctypes.Structure):
-    """ssm_rows"""
-
-    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
-
-
-class _SelectiveInputs(ctypes.Structure):
-    """ssm_selective_inputs"""
-
-    _fields_ = ([(n, _Rows) for n in ("x", "dt", "z", "B", "C")]
-                + [(n, ctypes.c_void_p) for n in ("A", "D", "dt_bias")])
-
-
-class _SelectiveGrads(ctypes.Structure):
-    """ssm_selective_grads"""
-
-    _fields_ = ([(n, _Rows) for n in ("dx", "ddt", "dz", "dB", "dC")]
-                + [(n, ctypes.c_void_p) for n in ("dA", "dD", "ddt_bias")])
-
-
 def _load():
     # The tensors handed to the library come from PyTorch's HIP runtime, and the
     # process must hold exactly one HIP runtime: load torch first so that the
@@ -213,8 +193,8 @@ def _load():
     lib.ssm_window_plan.restype = i32
     lib.ssm_window_plan.argtypes = [dp] + [vp] * 6
     cp, sp, np_ = (ctypes.POINTER(t) for t in (ConvDims, SelectiveDims, NormDims))
-    rp, lp = ctypes.POINTER(_Rows), ctypes.POINTER(i64)
-    ins, outs = ctypes.POINTER(_SelectiveInputs), ctypes.POINTER(_SelectiveGrads)
+    rp = ins = outs = vp  # arrays of rows, as addresses and strides (_flat)
+    lp = ctypes.POINTER(i64)
     lib.ssm_conv_sizes.argtypes = [cp, i32, lp]
     lib.ssm_conv_forward.argtypes = [cp, i32, vp, i32, vp, vp, rp, vp, vp, vp, rp, vp]
     lib.ssm_conv_backward.argtypes = [cp, i32, vp, vp, rp, vp, vp, rp, vp, rp, vp, vp, vp, vp, i64, vp]
@@ -654,26 +634,32 @@ _F32_T, _I32_T = (_torch.float32,), (_torch.int32,)
 _IN_T = {IN_BF16: (_torch.bfloat16,), IN_F32: (_torch.float32,)}
 
 
+# the address of a device's current stream, without a Stream object around it
+_stream_of_device = getattr(_torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: _torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on_device(args, stream, call) -> None:
     """call(stream address) on the device that the tensors among args share: their device
     becomes the current one for the call, and its current stream is the default."""
-    dev = None
+    index = None
     for a in args:
         if a is None or isinstance(a, int):
             continue
-        if dev is None:
-            dev = a.device
-        elif a.device != dev:
-            raise ValueError(f"tensors on different devices: {dev}, {a.device}")
-    if dev is None:
+        i = a.get_device()
+        if index is None:
+            index = i
+        elif i != index:
+            raise ValueError(f"tensors on different devices: {index}, {i}")
+    if index is None:
         return call(_stream(stream))  # raw addresses
     if stream is None:
-        stream = _torch.cuda.current_stream(dev)
-    if not isinstance(stream, int):
+        stream = _stream_of_device(index)
+    elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if dev.index == _torch.cuda.current_device():
+    if index == _torch.cuda.current_device():
         return call(stream)
-    with _torch.cuda.device(dev):
+    with _torch.cuda.device(index):
         call(stream)
 
 
@@ -808,21 +794,24 @@ def window_plan(d: Dims, lengths, tau, parity, update_rows, n_update, stream=Non
 # ----------------------------------------------------------------------------
 # around the recurrence: short convolution, selective recurrence, output norm
 # ----------------------------------------------------------------------------
-def _row_addr(x, name: str, types, rows: int, width: int) -> _Rows:
-    """Rows of `width` elements: a contiguous tensor, one whose first dimension alone is strided (a
-    column range of a larger one), an address of contiguous rows, or None."""
+def _row_addr(x, name: str, types, rows: int, width: int) -> tuple:
+    """Address and stride of rows of `width` elements: a contiguous tensor, one whose first dimension alone is
+    strided (a column range of a larger one), an address of contiguous rows, or None."""
     if x is None:
-        return _Rows(None, width)
+        return 0, width
     if isinstance(x, int):
-        return _Rows(x, width)
+        return x, width
+    if x.is_cuda and (types is None or x.dtype in types) and x.numel() == rows * width:
+        if x.is_contiguous():
+            return x.data_ptr(), width
+        if x.dim() == 2 and x.stride(1) == 1 and x.shape[0] == rows:
+            return x.data_ptr(), x.stride(0) if rows > 1 else width
     if not x.is_cuda:
         raise ValueError(f"{name}: expected a device tensor")
     if types is not None and x.dtype not in types:
         raise TypeError(f"{name}: dtype {x.dtype} not in {types}")
     if x.numel() != rows * width:
         raise ValueError(f"{name}: {x.numel()} elements, the dimensions need {rows} x {width}")
-    if x.is_contiguous():
-        return _Rows(x.data_ptr(), width)
     inner = 1
     for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
         if size != 1 and stride != inner:
@@ -830,7 +819,12 @@ def _row_addr(x, name: str, types, rows: int, width: int) -> _Rows:
         inner *= size
     if x.shape[0] != rows:
         raise ValueError(f"{name}: expected {rows} rows of {width}, got {tuple(x.shape)}")
-    return _Rows(x.data_ptr(), x.stride(0) if rows > 1 else width)
+    return x.data_ptr(), x.stride(0) if rows > 1 else width
+
+
+# Addresses and strides one after another have the layout of ssm_rows and of the structs made of it; an array
+# of integers is built in a fraction of the time of the structs.
+_ROWS1, _ROWS4, _INS, _OUTS = (ctypes.c_int64 * n for n in (2, 2 * CONV_PARTS, 13, 13))
 
 
 def _bytes_of(call, *args) -> int:
@@ -846,8 +840,10 @@ def _conv_parts(d: ConvDims, xs, name: str, types, rows: int):
     xs = list(xs) if isinstance(xs, (list, tuple)) else [xs]
     if len(xs) != d.parts:
         raise ValueError(f"{name}: {len(xs)} parts, the dimensions have {d.parts}")
-    return (_Rows * CONV_PARTS)(*[_row_addr(x, f"{name}[{p}]", types, rows, d.channels[p])
-                                  for p, x in enumerate(xs)]), xs
+    flat = []
+    for p, x in enumerate(xs):
+        flat += _row_addr(x, name, types, rows, d.channels[p])
+    return _ROWS4(*flat), xs
 
 
 def _conv_width(d: ConvDims) -> int:
@@ -920,11 +916,11 @@ def conv_step(d: ConvDims, x, weight, bias, state, y, *, slot=None, num_slots: O
 
 def _selective_in(d: SelectiveDims, rows: int, x, dt, A, B, C, D, z, dt_bias):
     tin, ch, bc = _IN_T.get(d.in_dtype), d.channels, d.groups * d.d_state
-    return _SelectiveInputs(
-        _row_addr(x, "x", tin, rows, ch), _row_addr(dt, "dt", tin, rows, ch),
-        _row_addr(z, "z", tin, rows, ch), _row_addr(B, "B", tin, rows, bc),
-        _row_addr(C, "C", tin, rows, bc), _addr(A, "A", _F32_T, ch * d.d_state),
-        _addr(D, "D", _F32_T, ch), _addr(dt_bias, "dt_bias", _F32_T, ch))
+    return _INS(
+        *_row_addr(x, "x", tin, rows, ch), *_row_addr(dt, "dt", tin, rows, ch),
+        *_row_addr(z, "z", tin, rows, ch), *_row_addr(B, "B", tin, rows, bc),
+        *_row_addr(C, "C", tin, rows, bc), _addr(A, "A", _F32_T, ch * d.d_state) or 0,
+        _addr(D, "D", _F32_T, ch) or 0, _addr(dt_bias, "dt_bias", _F32_T, ch) or 0)
 
 
 def selective_sizes(d: SelectiveDims, total_tokens: int) -> tuple:
@@ -946,14 +942,14 @@ def selective_forward(d: SelectiveDims, total_tokens: int, plan, x, dt, A, B, C,
     ns = d.batch if num_slots is None else _count(num_slots, "num_slots")
     states = ns * d.channels * d.d_state
     ins = _selective_in(d, total, x, dt, A, B, C, D, z, dt_bias)
-    o = _row_addr(out, "out", _IN_T.get(d.in_dtype), total, d.channels)
+    o = _ROWS1(*_row_addr(out, "out", _IN_T.get(d.in_dtype), total, d.channels))
     a = (_addr(plan, "plan", _I32_T, _plan_ints(total, d.batch)), ns,
          _addr(slot, "slot", _I32_T, d.batch), _addr(state_in, "state_in", _F32_T, states))
     end = _addr(state, "state", _F32_T, states)
     args = (plan, x, dt, A, B, C, D, z, dt_bias, state, out, state_in, slot)
     ws, have = _workspace(workspace, lambda: selective_sizes(d, total)[0], args, stream)
     _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_selective_forward(
-        ctypes.byref(d), total, *a, ctypes.byref(ins), end, ctypes.byref(o), ws.data_ptr(), have, s)))
+        ctypes.byref(d), total, *a, ins, end, o, ws.data_ptr(), have, s)))
 
 
 def selective_backward(d: SelectiveDims, total_tokens: int, plan, x, dt, A, B, C, dout, dx, ddt, dA, dB,
@@ -967,12 +963,12 @@ def selective_backward(d: SelectiveDims, total_tokens: int, plan, x, dt, A, B, C
     tin, ch, bc = _IN_T.get(d.in_dtype), d.channels, d.groups * d.d_state
     states = d.batch * ch * d.d_state
     ins = _selective_in(d, total, x, dt, A, B, C, D, z, dt_bias)
-    g = _row_addr(dout, "dout", tin, total, ch)
-    outs = _SelectiveGrads(
-        _row_addr(dx, "dx", tin, total, ch), _row_addr(ddt, "ddt", tin, total, ch),
-        _row_addr(dz, "dz", tin, total, ch), _row_addr(dB, "dB", tin, total, bc),
-        _row_addr(dC, "dC", tin, total, bc), _addr(dA, "dA", _F32_T, ch * d.d_state),
-        _addr(dD, "dD", _F32_T, ch), _addr(ddt_bias, "ddt_bias", _F32_T, ch))
+    g = _ROWS1(*_row_addr(dout, "dout", tin, total, ch))
+    outs = _OUTS(
+        *_row_addr(dx, "dx", tin, total, ch), *_row_addr(ddt, "ddt", tin, total, ch),
+        *_row_addr(dz, "dz", tin, total, ch), *_row_addr(dB, "dB", tin, total, bc),
+        *_row_addr(dC, "dC", tin, total, bc), _addr(dA, "dA", _F32_T, ch * d.d_state) or 0,
+        _addr(dD, "dD", _F32_T, ch) or 0, _addr(ddt_bias, "ddt_bias", _F32_T, ch) or 0)
     a = (_addr(plan, "plan", _I32_T, _plan_ints(total, d.batch)),
          _addr(state_in, "state_in", _F32_T, states))
     end, start = _addr(dstate, "dstate", _F32_T, states), _addr(dstate_in, "dstate_in", _F32_T, states)
@@ -980,7 +976,7 @@ def selective_backward(d: SelectiveDims, total_tokens: int, plan, x, dt, A, B, C
             dstate, dstate_in)
     ws, have = _workspace(workspace, lambda: selective_sizes(d, total)[1], args, stream)
     _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_selective_backward(
-        ctypes.byref(d), total, *a, ctypes.byref(ins), ctypes.byref(g), end, ctypes.byref(outs), start,
+        ctypes.byref(d), total, *a, ins, g, end, outs, start,
         ws.data_ptr(), have, s)))
 
 
@@ -989,19 +985,19 @@ def selective_step(d: SelectiveDims, x, dt, A, B, C, state, out, *, D=None, z=No
     """ssm_selective_step: one token of each of d.batch rows; the state is updated in place."""
     ns = d.batch if num_slots is None else _count(num_slots, "num_slots")
     ins = _selective_in(d, d.batch, x, dt, A, B, C, D, z, dt_bias)
-    o = _row_addr(out, "out", _IN_T.get(d.in_dtype), d.batch, d.channels)
+    o = _ROWS1(*_row_addr(out, "out", _IN_T.get(d.in_dtype), d.batch, d.channels))
     a = (ns, _addr(slot, "slot", _I32_T, d.batch))
     s0 = _addr(state, "state", _F32_T, ns * d.channels * d.d_state)
     _on_device((x, dt, A, B, C, state, out, D, z, dt_bias, slot), stream,
-               lambda s: _check(_lib.ssm_selective_step(ctypes.byref(d), *a, ctypes.byref(ins), s0,
-                                                        ctypes.byref(o), s)))
+               lambda s: _check(_lib.ssm_selective_step(ctypes.byref(d), *a, ins, s0,
+                                                        o, s)))
 
 
 def _norm_in(d: NormDims, rows: int, x, z, weight, bias):
     wide = d.groups * d.width
     own = d.width if d.shared else wide
-    return (_row_addr(x, "x", _IN_T.get(d.x_dtype), rows, wide),
-            _row_addr(z, "z", _IN_T.get(d.in_dtype), rows, wide),
+    return (_ROWS1(*_row_addr(x, "x", _IN_T.get(d.x_dtype), rows, wide)),
+            _ROWS1(*_row_addr(z, "z", _IN_T.get(d.in_dtype), rows, wide)),
             _addr(weight, "weight", _F32_T, own), _addr(bias, "bias", _F32_T, own))
 
 
@@ -1016,9 +1012,9 @@ def gated_norm(d: NormDims, rows: int, x, z, weight, bias, out, stream=None) -> 
     or [width] where shared."""
     rows = _count(rows, "rows")
     xr, zr, w, b = _norm_in(d, rows, x, z, weight, bias)
-    o = _row_addr(out, "out", _IN_T.get(d.in_dtype), rows, d.groups * d.width)
+    o = _ROWS1(*_row_addr(out, "out", _IN_T.get(d.in_dtype), rows, d.groups * d.width))
     _on_device((x, z, weight, bias, out), stream, lambda s: _check(_lib.ssm_gated_norm(
-        ctypes.byref(d), rows, ctypes.byref(xr), ctypes.byref(zr), w, b, ctypes.byref(o), s)))
+        ctypes.byref(d), rows, xr, zr, w, b, o, s)))
 
 
 def gated_norm_backward(d: NormDims, rows: int, x, z, weight, bias, dout, dx, dz, dweight, dbias=None, *,
@@ -1029,12 +1025,12 @@ def gated_norm_backward(d: NormDims, rows: int, x, z, weight, bias, dout, dx, dz
     xr, zr, w, b = _norm_in(d, rows, x, z, weight, bias)
     wide, tin = d.groups * d.width, _IN_T.get(d.in_dtype)
     own = d.width if d.shared else wide
-    g, dxr, dzr = (_row_addr(dout, "dout", tin, rows, wide),
-                   _row_addr(dx, "dx", _IN_T.get(d.x_dtype), rows, wide),
-                   _row_addr(dz, "dz", tin, rows, wide))
+    g, dxr, dzr = (_ROWS1(*_row_addr(dout, "dout", tin, rows, wide)),
+                   _ROWS1(*_row_addr(dx, "dx", _IN_T.get(d.x_dtype), rows, wide)),
+                   _ROWS1(*_row_addr(dz, "dz", tin, rows, wide)))
     dw, db = _addr(dweight, "dweight", _F32_T, own), _addr(dbias, "dbias", _F32_T, own)
     args = (x, z, weight, bias, dout, dx, dz, dweight, dbias)
     ws, have = _workspace(workspace, lambda: gated_norm_sizes(d, rows), args, stream)
     _on_device(args + (ws,), stream, lambda s: _check(_lib.ssm_gated_norm_backward(
-        ctypes.byref(d), rows, ctypes.byref(xr), ctypes.byref(zr), w, b, ctypes.byref(g),
-        ctypes.byref(dxr), ctypes.byref(dzr), dw, db, ws.data_ptr(), have, s)))
+        ctypes.byref(d), rows, xr, zr, w, b, g,
+        dxr, dzr, dw, db, ws.data_ptr(), have, s)))

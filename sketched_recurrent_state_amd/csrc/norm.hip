@@ -14,7 +14,7 @@ namespace {
 constexpr int NT = 256;     // threads of a workgroup of narrow groups
 constexpr int SMALL = 512;  // the widest group of one wave
 constexpr int MOST = 1024;  // threads of a workgroup of one wide group (8192 channels)
-constexpr long long kMostBlocks = 1 << 22;  // keeps a grid below 2^32 threads; then a workgroup takes several
+constexpr long long kMostBlocks = 1 << 21;  // keeps a grid below 2^32 threads; then a workgroup takes several
 
 // Lanes of a group: a power of two of them in a wave, or (0) a workgroup.
 inline int group_lanes(int width) {

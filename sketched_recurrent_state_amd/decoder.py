@@ -1,4 +1,5 @@
-"""Window cadence of the SketchSSM decode path for one linear-attention layer.
+"""Window cadence of the SketchSSM decode path for one linear-attention layer, and what a layer
+has around its recurrence.
 
 ``WindowedDecoder`` owns the device buffers of one layer (the state, the
 sketch, the W-token window buffer) and sequences the library calls:
@@ -13,6 +14,10 @@ Abstract: full-state updates once per window with a sketch refresh, sketch
 reads in between; agihunt.info summary, "Error control": the sketch's error
 never reaches the state). Memory comes from PyTorch; all arithmetic is in the
 library's kernels.
+
+``ShortConv`` keeps the last inputs of a layer's short convolution, ``GatedNorm`` the weights of its
+output norm; both decoders take them, and then take projections and return normalised outputs.
+``SelectiveDecoder`` holds the state of a selective layer (a decay per channel and state).
 """
 from __future__ import annotations
 
@@ -21,14 +26,19 @@ from typing import Optional
 
 import torch
 
-from . import (Dims, IN_BF16, KDA, MAMBA2, SKETCH_BF16, buffer_append, full_read_decode_step,
-               rank_offsets, recurrent_decode_step, scan_forward, scan_plan, scan_sizes,
-               sketch_decode_step, sketch_decode_step_ls, sketch_decode_step_ranked,
-               window_update_refresh, window_update_refresh_ls,
+from . import (ConvDims, Dims, IN_BF16, IN_F32, KDA, MAMBA2, NormDims, SKETCH_BF16, SelectiveDims,
+               buffer_append, conv_forward, conv_step, full_read_decode_step, gated_norm,
+               rank_offsets, recurrent_decode_step, scan_forward, scan_plan,
+               selective_forward, selective_step, sketch_decode_step, sketch_decode_step_ls,
+               sketch_decode_step_ranked, window_update_refresh, window_update_refresh_ls,
                window_update_refresh_ranked)
 
 
-def _checked_lengths(d: Dims, lengths, q):
+def _in_type(in_dtype: int) -> torch.dtype:
+    return torch.bfloat16 if in_dtype == IN_BF16 else torch.float32
+
+
+def _checked_lengths(d, lengths, q):
     """Prompt lengths as Python integers that sum to q's tokens, or the device tensor, which is
     not read back."""
     if isinstance(lengths, torch.Tensor) and lengths.is_cuda:
@@ -46,20 +56,108 @@ def _checked_lengths(d: Dims, lengths, q):
     return lengths
 
 
-def _prefill(d: Dims, state: torch.Tensor, lengths, q, k, v, decay, beta) -> torch.Tensor:
-    """A packed batch of d.batch prompts (checked lengths; token arrays [sum][H][..]) through the
-    recurrence, from `state` and into it; returns y [sum][H][d_v]."""
-    total = q.shape[0]
-    # lengths that are not read back may sum to less: the rows behind them are not written
-    on_device = isinstance(lengths, torch.Tensor)
-    new = torch.zeros if on_device else torch.empty
-    if on_device and lengths.dtype != torch.int32:
+def _plan(lengths, total: int, device) -> torch.Tensor:
+    """The plan of a packed batch (checked lengths). Lengths on the device may sum to less than total."""
+    if isinstance(lengths, torch.Tensor) and lengths.dtype != torch.int32:
         lengths = lengths.long().clamp(0, total)  # so that the cast cannot wrap
-    lengths = torch.as_tensor(lengths, dtype=torch.int32, device=state.device)
-    plan = torch.empty(scan_sizes(d, total)[0], dtype=torch.int32, device=state.device)
+    lengths = torch.as_tensor(lengths, dtype=torch.int32, device=device)
+    n = lengths.numel()
+    plan = torch.empty(2 * (n + 1) + total // 64 + n, dtype=torch.int32, device=device)
     scan_plan(lengths, total, plan)
-    y = new((total, d.heads, d.d_v), device=state.device, dtype=torch.float32)
+    return plan
+
+
+def _new_rows(lengths):
+    """How outputs are made: rows behind the last prompt, if there can be any, are not written, and zero."""
+    return torch.zeros if isinstance(lengths, torch.Tensor) else torch.empty
+
+
+class ShortConv:
+    """The short convolution of a layer's inputs (dims.parts of them) for dims.batch sequences.
+
+    weight: fp32 [C, taps], bias: fp32 [C] or None, C the parts' channels one after another
+    state:  the last taps - 1 inputs [batch, taps - 1, C] in dims.in_dtype (zeros if None), used in place
+    """
+
+    def __init__(self, dims: ConvDims, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                 state: Optional[torch.Tensor] = None):
+        self.d, self.weight, self.bias = dims, weight, bias
+        self.widths = list(dims.channels[:dims.parts])
+        if state is None:
+            state = torch.zeros((dims.batch, dims.taps - 1, sum(self.widths)), device=weight.device,
+                                dtype=_in_type(dims.in_dtype))
+        self.state = state
+
+    def _out(self, make, rows: int):
+        return [make((rows, w), device=self.state.device, dtype=self.state.dtype) for w in self.widths]
+
+    def step(self, *xs) -> list:
+        """One token of every sequence: the parts' rows [batch][channels], in and out."""
+        y = self._out(torch.empty, self.d.batch)
+        conv_step(self.d, xs, self.weight, self.bias, self.state, y)
+        return y
+
+    def prefill(self, lengths, *xs) -> list:
+        """A packed batch of prompts (lengths as in WindowedDecoder.prefill; the parts' rows
+        [sum of lengths][channels]): the parts' outputs, and the state continued."""
+        lengths = _checked_lengths(self.d, lengths, xs[0])
+        with torch.cuda.device_of(self.state):
+            return self._prefill(_plan(lengths, xs[0].shape[0], self.state.device), _new_rows(lengths), xs)
+
+    def _prefill(self, plan, make, xs) -> list:
+        total = xs[0].shape[0]
+        y = self._out(make, total)
+        conv_forward(self.d, total, plan, xs, self.weight, self.bias, y, self.state, state_in=self.state)
+        return y
+
+
+class GatedNorm:
+    """The norm of a layer's outputs in groups of channels, gated: weight (and bias) fp32
+    [groups][width], or [width] with dims.shared."""
+
+    def __init__(self, dims: NormDims, weight: torch.Tensor, bias: Optional[torch.Tensor] = None):
+        self.d, self.weight, self.bias = dims, weight, bias
+
+    def __call__(self, x: torch.Tensor, gate: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """x [rows][groups][width], gate rows of as many channels: a new tensor of x's shape."""
+        out = torch.empty(x.shape, device=x.device, dtype=_in_type(self.d.in_dtype))
+        gated_norm(self.d, x.shape[0], x, gate, self.weight, self.bias, out)
+        return out
+
+
+def _around(d: Dims, conv: Optional[ShortConv], norm: Optional[GatedNorm]) -> None:
+    """Whether a decoder's convolution and norm fit its layer."""
+    if conv is not None:
+        want = [d.heads * d.d_k, d.heads * d.d_k, d.heads * d.d_v]
+        if conv.widths != want or conv.d.batch != d.batch or conv.d.in_dtype != d.in_dtype:
+            raise ValueError(f"{conv.d} does not make the queries, keys and values of {d}")
+    if norm is not None:
+        if (norm.d.groups, norm.d.width, norm.d.x_dtype) != (d.heads, d.d_v, IN_F32):
+            raise ValueError(f"{norm.d} does not take the outputs of {d}")
+
+
+def _heads(d: Dims, parts):
+    """Convolved parts as queries, keys and values by head."""
+    q, k, v = parts
+    rows = q.shape[0]
+    return q.view(rows, d.heads, d.d_k), k.view(rows, d.heads, d.d_k), v.view(rows, d.heads, d.d_v)
+
+
+def _prefill(d: Dims, state: torch.Tensor, lengths, q, k, v, decay, beta, conv=None, norm=None,
+             gate=None) -> torch.Tensor:
+    """A packed batch of d.batch prompts (checked lengths; token arrays [sum][H][..]) through the
+    layer, from `state` and into it; returns its outputs [sum][H][d_v]."""
+    total, make = q.shape[0], _new_rows(lengths)
+    plan = _plan(lengths, total, state.device)
+    if conv is not None:
+        q, k, v = _heads(d, conv._prefill(plan, torch.empty, (q, k, v)))
+    y = make((total, d.heads, d.d_v), device=state.device, dtype=torch.float32)
     scan_forward(d, total, plan, q, k, v, decay, beta, state, y, state_in=state)
+    if norm is not None:
+        y = norm(y, gate)
+        if make is torch.zeros:  # the norm of a row of zeros need not be zero
+            behind = torch.arange(total, device=state.device) >= plan[d.batch]
+            y.masked_fill_(behind[:, None, None], 0.0)
     return y
 
 
@@ -77,12 +175,16 @@ class WindowedDecoder:
     coefficients: "projection" (c = B q~) or "least_squares" (c minimising the error of the
             window-start read; then `sketch` holds orthonormal sketch rows and `read_map`
             [N, H, r, d_k] the per-unit map q~ -> c; uniform rank and fp32 sketch only)
+    conv, norm: the layer's short convolution and output norm, or None. With a convolution q, k, v are the
+            projections that go into it (rows of H d_k, H d_k and H d_v channels; they may be column ranges of
+            one tensor); with a norm the outputs are normalised and gated by `gate`, in its in_dtype.
     The sketch is kept in dims.sketch_dtype (fp32, or bf16 rounded to nearest).
     """
 
     def __init__(self, dims: Dims, state: torch.Tensor, basis: Optional[torch.Tensor] = None, *,
                  read: str = "sketch", fused: bool = True, ranks=None,
-                 coefficients: str = "projection"):
+                 coefficients: str = "projection", conv: Optional[ShortConv] = None,
+                 norm: Optional[GatedNorm] = None):
         if read not in ("sketch", "full", "both"):
             raise ValueError(read)
         if coefficients not in ("projection", "least_squares"):
@@ -92,6 +194,10 @@ class WindowedDecoder:
             raise ValueError("least-squares coefficients use a uniform rank")
         if read != "full" and basis is None:
             raise ValueError("a sketch read needs a basis")
+        if norm is not None and read == "both":
+            raise ValueError("two reads are compared before the norm")
+        _around(dims, conv, norm)
+        self.conv, self.norm = conv, norm
         self.d = dims
         self.read = read
         self.fused = fused
@@ -152,7 +258,7 @@ class WindowedDecoder:
         self.tau = 0
 
     # -- prompts -----------------------------------------------------------------
-    def prefill(self, lengths, q, k, v, decay, beta=None) -> torch.Tensor:
+    def prefill(self, lengths, q, k, v, decay, beta=None, *, gate=None) -> torch.Tensor:
         """Take a packed batch of prompts (integer lengths [N], zero for a sequence with no new
         tokens; token arrays [sum of lengths][H][..]) into the state and refresh the sketch; returns
         the outputs [sum of lengths][H][d_v]. Tokens still in the window are written first. Lengths on
@@ -162,15 +268,18 @@ class WindowedDecoder:
         with torch.cuda.device_of(self.state):  # the flush and the refresh on the scan's stream
             if self.tau:
                 self.flush()
-            y = _prefill(self.d, self.state, lengths, q, k, v, decay, beta)
+            y = _prefill(self.d, self.state, lengths, q, k, v, decay, beta, self.conv, self.norm, gate)
             self.refresh()
         return y
 
     # -- one decode step -----------------------------------------------------------
-    def step(self, q, k, v, decay, beta=None, *, y=None, y_full=None):
-        """Read the output for the current token; returns y (or (y, y_full) for read="both")."""
+    def step(self, q, k, v, decay, beta=None, *, gate=None, y=None, y_full=None):
+        """Read the output for the current token; returns y (or (y, y_full) for read="both"), or with a
+        norm what the norm makes of it."""
         d = self.d
         tau = self.tau + 1
+        if self.conv is not None:
+            q, k, v = _heads(d, self.conv.step(q, k, v))
         N, H, dv = d.batch, d.heads, d.d_v
         if y is None and self.read != "full":
             y = torch.empty((N, H, dv), device=q.device, dtype=torch.float32)
@@ -193,27 +302,66 @@ class WindowedDecoder:
             self.tau = 0
         if self.read == "both":
             return y, y_full
-        return y if self.read == "sketch" else y_full
+        y = y if self.read == "sketch" else y_full
+        return y if self.norm is None else self.norm(y, gate)
 
 
 class RecurrentDecoder:
     """The per-token recurrent decode (the baseline SketchSSM is compared against):
-    every step writes the token into the full state and reads y = S^T q from it."""
+    every step writes the token into the full state and reads y = S^T q from it.
+    conv, norm: as in WindowedDecoder."""
 
-    def __init__(self, dims: Dims, state: torch.Tensor):
-        self.d = dims
-        self.state = state
+    def __init__(self, dims: Dims, state: torch.Tensor, *, conv: Optional[ShortConv] = None,
+                 norm: Optional[GatedNorm] = None):
+        _around(dims, conv, norm)
+        self.d, self.state, self.conv, self.norm = dims, state, conv, norm
 
-    def step(self, q, k, v, decay, beta=None, *, y=None):
+    def step(self, q, k, v, decay, beta=None, *, gate=None, y=None):
         d = self.d
+        if self.conv is not None:
+            q, k, v = _heads(d, self.conv.step(q, k, v))
         if y is None:
             y = torch.empty((d.batch, d.heads, d.d_v), device=q.device, dtype=torch.float32)
         recurrent_decode_step(d, self.state, q, k, v, decay, beta, y)
-        return y
+        return y if self.norm is None else self.norm(y, gate)
 
-    def prefill(self, lengths, q, k, v, decay, beta=None) -> torch.Tensor:
+    def prefill(self, lengths, q, k, v, decay, beta=None, *, gate=None) -> torch.Tensor:
         """Take a packed batch of prompts into the state; returns their outputs (lengths and
         outputs as in WindowedDecoder.prefill)."""
         lengths = _checked_lengths(self.d, lengths, q)
         with torch.cuda.device_of(self.state):
-            return _prefill(self.d, self.state, lengths, q, k, v, decay, beta)
+            return _prefill(self.d, self.state, lengths, q, k, v, decay, beta, self.conv, self.norm, gate)
+
+
+class SelectiveDecoder:
+    """One selective layer's recurrence for dims.batch sequences.
+
+    state:  fp32 [batch, channels, d_state], used in place
+    A:      fp32 [channels, d_state] (negative), D and dt_bias fp32 [channels] or None
+    """
+
+    def __init__(self, dims: SelectiveDims, state: torch.Tensor, A: torch.Tensor, *,
+                 D: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None):
+        self.d, self.state, self.A = dims, state, A
+        self.more = {"D": D, "dt_bias": dt_bias}
+
+    def step(self, x, dt, B, C, z=None, *, out=None) -> torch.Tensor:
+        """One token of every sequence: x, dt, z [batch][channels], B, C [batch][groups][d_state];
+        returns out [batch][channels]."""
+        d = self.d
+        if out is None:
+            out = torch.empty((d.batch, d.channels), device=x.device, dtype=_in_type(d.in_dtype))
+        selective_step(d, x, dt, self.A, B, C, self.state, out, z=z, **self.more)
+        return out
+
+    def prefill(self, lengths, x, dt, B, C, z=None) -> torch.Tensor:
+        """Take a packed batch of prompts (rows [sum of lengths][..]) into the state; returns their outputs
+        (lengths and outputs as in WindowedDecoder.prefill)."""
+        d, total = self.d, x.shape[0]
+        lengths = _checked_lengths(d, lengths, x)
+        with torch.cuda.device_of(self.state):
+            plan = _plan(lengths, total, self.state.device)
+            out = _new_rows(lengths)((total, d.channels), device=self.state.device, dtype=_in_type(d.in_dtype))
+            selective_forward(d, total, plan, x, dt, self.A, B, C, self.state, out, z=z, state_in=self.state,
+                              **self.more)
+        return out

@@ -8,6 +8,26 @@ import pytest
 import sketched_recurrent_state_amd as ssm
 from tests import layer_reference as ref
 
+class Rows(ctypes.Structure):
+    """ssm_rows"""
+
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
+class SelectiveInputs(ctypes.Structure):
+    """ssm_selective_inputs"""
+
+    _fields_ = ([(n, Rows) for n in ("x", "dt", "z", "B", "C")]
+                + [(n, ctypes.c_void_p) for n in ("A", "D", "dt_bias")])
+
+
+class SelectiveGrads(ctypes.Structure):
+    """ssm_selective_grads"""
+
+    _fields_ = ([(n, Rows) for n in ("dx", "ddt", "dz", "dB", "dC")]
+                + [(n, ctypes.c_void_p) for n in ("dA", "dD", "ddt_bias")])
+
+
 A = 1 << 32  # a 16-byte aligned fake device address (never dereferenced)
 GAP = 1 << 28
 
@@ -17,11 +37,11 @@ def at(i):
 
 
 def rows(i, stride):
-    return ssm._Rows(at(i), stride)
+    return Rows(at(i), stride)
 
 
 def parts(first, strides):
-    return (ssm._Rows * 4)(*[rows(first + p, s) for p, s in enumerate(strides)])
+    return (Rows * 4)(*[rows(first + p, s) for p, s in enumerate(strides)])
 
 
 def call(name, *args):
@@ -129,7 +149,7 @@ def test_conv_forward_refusals():
     assert st == 5
     st, msg = conv_forward(d, state=at(2) + 64)
     assert st == 5 and "state" in msg
-    one = (ssm._Rows * 4)(*[ssm._Rows(at(10), 256)] * 3)
+    one = (Rows * 4)(*[Rows(at(10), 256)] * 3)
     assert conv_forward(d, y=one)[0] == 5
 
 
@@ -138,7 +158,7 @@ def test_interleaved_rows():
     d = conv_dims()
 
     def ranges(base, starts, stride=320):
-        return (ssm._Rows * 4)(*[ssm._Rows(base + 2 * s, stride) for s in starts])
+        return (Rows * 4)(*[Rows(base + 2 * s, stride) for s in starts])
 
     for starts, pair in [((0, 56, 128), (0, 1)), ((0, 64, 120), (1, 2)), ((64, 0, 56), (0, 2)),
                          ((128, 192, 72), (0, 2)), ((0, 128, 184), (1, 2)), ((0, 256, 160), (1, 2)),
@@ -206,14 +226,14 @@ def sel_in(**kw):
     a = dict(x=rows(1, 128), dt=rows(2, 128), z=rows(3, 128), B=rows(4, 32), C=rows(5, 32), A=at(6), D=at(7),
              dt_bias=at(8))
     a.update(kw)
-    return ssm._SelectiveInputs(*a.values())
+    return SelectiveInputs(*a.values())
 
 
 def sel_grads(**kw):
     a = dict(dx=rows(21, 128), ddt=rows(22, 128), dz=rows(23, 128), dB=rows(24, 32), dC=rows(25, 32), dA=at(26),
              dD=at(27), ddt_bias=at(28))
     a.update(kw)
-    return ssm._SelectiveGrads(*a.values())
+    return SelectiveGrads(*a.values())
 
 
 def sel_forward(d, total=100, **kw):
@@ -258,7 +278,7 @@ def test_selective_dims():
 
 def test_selective_refusals():
     d = sel_dims()
-    none = ssm._Rows(None, 128)
+    none = Rows(None, 128)
     for name in ("x", "dt", "B", "C"):
         for f in (sel_forward, sel_backward, sel_step):
             st, msg = f(d, ins=sel_in(**{name: none}))
