@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
     for (int t0 = 0; t0 < c.count; t0 += TB) {
       const Block now = next;
       const bool on = t0 + w.t < c.count;
-      const int64_t tok0 = (int64_t)c.first + c.pos + t0;
+      const int tok0 = c.first + c.pos + t0;
       if (t0 + TB < c.count) next.load(a, w, c, t0 + TB);
       else if (more) next.load(a, w, ahead, 0);
       if constexpr (!OUT) {

@@ -84,12 +84,13 @@ __device__ __forceinline__ SelTile sel_tile(const SelectiveArgs& a, int tile) {
 __device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // Element `col` of row `row` (both the lane's) behind row tok0 (the wave's): a scalar base and an offset of
-// 32 bits (strides are below 2^26), so that an array's place takes one vector register, not two.
+// 32 bits (strides are below 2^26), so that an array's place takes one vector register, not two, and the
+// base one product of 32 bits by 32.
 template <typename T>
-__device__ __forceinline__ T* row_at(const Rows& m, int64_t tok0, int row, int col) {
-  char* base = static_cast<char*>(const_cast<void*>(m.p)) + tok0 * m.stride * (int64_t)sizeof(T);
-  const uint32_t off = (uint32_t)row * (uint32_t)(m.stride * sizeof(T)) + (uint32_t)col * (uint32_t)sizeof(T);
-  return reinterpret_cast<T*>(base + off);
+__device__ __forceinline__ T* row_at(const Rows& m, int tok0, int row, int col) {
+  const uint32_t pitch = (uint32_t)m.stride * (uint32_t)sizeof(T);
+  char* base = static_cast<char*>(const_cast<void*>(m.p)) + (uint64_t)(uint32_t)tok0 * pitch;
+  return reinterpret_cast<T*>(base + (uint32_t)((uint32_t)row * pitch + (uint32_t)col * (uint32_t)sizeof(T)));
 }
 
 template <typename T, int E>
@@ -189,7 +190,7 @@ struct SelBlock {
   Packed<T, SH::EC> x, dt, z, dy;
   Packed<T, SH::EN> b, c;
   __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0) {
-    const int64_t tok0 = (int64_t)cell.first + cell.pos + t0;
+    const int tok0 = cell.first + cell.pos + t0;
     const int left = cell.count - t0, row = min(w.t, left - 1);
     const int c0 = w.c0 + w.q * SH::EC, n0 = w.group * SH::N + w.q * SH::EN;
     x.load(row_at<T>(a.x, tok0, row, c0));

@@ -106,7 +106,10 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
     });
   // the lane's place among dB and dC of a token and tile: its values are dB of its NS states, then dC
   const int kept = halved_at<S, 2 * NS>(w.lane);
-  const uint32_t dbc_at = (uint32_t)((kept < NS ? 0 : N - NS) + n0 + kept);
+  const uint32_t dbc_at = 4 * (uint32_t)((kept < NS ? 0 : N - NS) + n0 + kept);
+  const uint32_t dbc_pitch = (uint32_t)tiles * (8 * N);  // bytes from token to token: tiles < 2^18
+  char* const dbc_tile = reinterpret_cast<char*>(a.w.dbc) + (uint32_t)tile * (8 * N);
+  char* const dbc_none = dbc_tile + (uint64_t)(uint32_t)a.plan.total * dbc_pitch;
   SelCell cell, ahead;
   bool more = prev_cell(a, grp.e1 - 1, grp.e0 - 1, cell);
   float g[NS];
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
       if (t0 > 0) next.load(a, w, cell, t0 - TB, my, n0);
       else if (more) next.load(a, w, ahead, (ahead.count - 1) / TB * TB, my, n0);
       const bool on = t0 + w.t < cell.count;
-      const int64_t tok0 = (int64_t)cell.first + cell.pos + t0;
+      const int tok0 = cell.first + cell.pos + t0;
       {
         float x[EC], raw[EC], delta[EC], bias[EC], z[EC], dy[EC], b[EN], c[EN];
         now.x.unpack(x);
@@ -160,6 +163,7 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
         Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], c);
       }
       wave_lds_sync();
+      char* const dbc = dbc_tile + (uint64_t)(uint32_t)tok0 * dbc_pitch;
       float h[TB / HB][NS];  // the states before each part
 #pragma unroll
       for (int i = 0; i < NS; ++i) h[0][i] = now.h0[i];
@@ -230,10 +234,10 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
           // each sum is stored as it is made, by every lane that has it; rows without a token (whose sums are
           // zero) go to a row behind the last
           channel_halve<S>(sums, w.lane);
-          const int64_t row = t0 + tb < cell.count ? tok0 + tb : (int64_t)a.plan.total;
-          float* to = a.w.dbc + (row * tiles + tile) * 2 * N;
+          char* row = t0 + tb < cell.count ? dbc + (uint32_t)tb * dbc_pitch : dbc_none;
 #pragma unroll
-          for (int i = 0; i < kHalved<S, 2 * NS>; ++i) to[dbc_at + i] = sums[i];
+          for (int i = 0; i < kHalved<S, 2 * NS>; ++i)
+            *reinterpret_cast<float*>(row + (dbc_at + 4 * (uint32_t)i)) = sums[i];
         }
 #pragma unroll
         for (int i = 0; i < KEEP; ++i)
