@@ -6,7 +6,7 @@ namespace ssm {
 namespace {
 
 // The main pass over a group. OUT: outputs and final states. Otherwise (the backward pass's second
-// kernel): the state before every block but the sequence's first.
+// kernel): the state before every HB tokens but the sequence's first.
 template <int S, int NS, typename T, bool OUT>
 __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const SelectiveArgs a) {
   using SH = SelShape<S, NS>;
@@ -58,11 +58,12 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
       const int tok0 = c.first + c.pos + t0;
       if (t0 + TB < c.count) next.load(a, w, c, t0 + TB);
       else if (more) next.load(a, w, ahead, 0);
+      const auto keep_state = [&](int t) {
+        const size_t part = (size_t)(c.first / HB + (c.pos + t0 + t) / HB - 1);
+        Vec<float, NS>::store(a.w.states + part * a.channels * N + (uint32_t)(my * N + n0), h);
+      };
       if constexpr (!OUT) {
-        if (c.pos + t0 > 0) {
-          const size_t block = (size_t)(c.first / TB + (c.pos + t0) / TB - 1);
-          Vec<float, NS>::store(a.w.states + block * a.channels * N + (uint32_t)(my * N + n0), h);
-        }
+        if (c.pos + t0 > 0) keep_state(0);
       }
       float x[EC], dt[EC], delta[EC], bias[EC], b[EN], cc[EN];
       now.x.unpack(x);
@@ -83,6 +84,8 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
       float y[(TB + S - 1) / S];  // lane sg keeps the tokens that are sg modulo S
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
+        if constexpr (!OUT)
+          if (t == HB && t0 + HB < c.count) keep_state(HB);
         const float2 v = sv[wave][t][w.ch];
         float bb[NS], ct[NS], yt = 0.f;
         Vec<float, NS>::load(&sb[wave][t][n0], bb);
@@ -351,7 +354,7 @@ SelectiveWork selective_work(const ssm_selective_dims& d, int total, bool backwa
   }
   if (backward) {
     if (g.groups > 1) w.back = take(g.groups * states);
-    w.states = take(((size_t)total / TB + 1) * states);
+    w.states = take(((size_t)total / HB + 1) * states);
     w.dbc = take(((size_t)total + 1) * selective_tiles(d) * 2 * d.d_state);
     w.partial = take((size_t)g.groups * d.channels * (d.d_state + 2));
   }

@@ -23,6 +23,7 @@
 namespace ssm {
 
 constexpr int TB = 16;     // tokens of a block
+constexpr int HB = 8;      // tokens between the states that the backward pass starts from
 constexpr int WAVES = 4;   // of a workgroup
 
 // log(1 + e^x) = max(x, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|x| <= 1, so small values keep their digits.
@@ -285,7 +286,7 @@ SelGroups selective_groups(const ssm_selective_dims& d, int cap);
 // The local pass; sets a's groups.
 hipError_t launch_selective_local(const ssm_selective_dims& d, SelectiveArgs& a, bool backward,
                                   hipStream_t stream);
-// The states before every block, for the backward pass.
+// The states before every HB tokens, for the backward pass.
 hipError_t launch_selective_states(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream);
 
 // Calls f(S, NS, type) for d.d_state: S lanes a channel, NS states a lane.

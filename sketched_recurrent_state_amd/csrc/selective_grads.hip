@@ -15,23 +15,22 @@ namespace ssm {
 namespace {
 
 template <typename T, int S, int NS>
-struct GradBlock : SelBlock<T, S, NS, true, true, true> {
-  using SH = SelShape<S, NS>;
-  float h0[NS];  // the state before the block
-  __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0,
-                                       int my, int n) {
-    SelBlock<T, S, NS, true, true, true>::load(a, w, cell, t0);
-    const uint32_t at = (uint32_t)(my * SH::N + n);
-    if (cell.pos + t0 > 0) {
-      const size_t block = (size_t)(cell.first / TB + (cell.pos + t0) / TB - 1);
-      Vec<float, NS>::load(a.w.states + block * a.channels * SH::N + at, h0);
-    } else if (a.state_in) {
-      Vec<float, NS>::load(a.state_in + (size_t)cell.slot * a.channels * SH::N + at, h0);
-    } else {
-      zero(h0);
-    }
-  }
-};
+using GradBlock = SelBlock<T, S, NS, true, true, true>;
+
+// The states before a block's two parts (of the later one, if it holds a token).
+template <int N, int NS>
+__device__ __forceinline__ void part_states(const SelectiveArgs& a, const SelCell& cell, int t0, int my, int n0,
+                                            float (&h)[TB / HB][NS]) {
+  static_assert(TB / HB == 2, "two parts");
+  const uint32_t at = (uint32_t)(my * N + n0);
+  const size_t step = (size_t)a.channels * N;
+  const float* kept = a.w.states + (size_t)(cell.first / HB + (cell.pos + t0) / HB) * step;
+  zero(h[0]);
+  zero(h[1]);
+  if (t0 + HB < cell.count) Vec<float, NS>::load(kept + at, h[1]);
+  if (cell.pos + t0 > 0) Vec<float, NS>::load(kept - step + at, h[0]);
+  else if (a.state_in) Vec<float, NS>::load(a.state_in + (size_t)cell.slot * step + at, h[0]);
+}
 
 // Sums of v[0 .. V) over the lanes that share lane % S, by halving: every step adds two lanes' values
 // and gives each half of the lanes half of the values. Afterwards v[0 .. kHalved) of a lane are
@@ -64,11 +63,8 @@ __device__ __forceinline__ void store3(float4* p, const float (&v)[3]) {
   *reinterpret_cast<float3*>(p) = make_float3(v[0], v[1], v[2]);
 }
 
-constexpr int HB = TB / 2;  // tokens whose states are in registers at once
-
-// A block's states are computed from the one before it: for its later half (through the first, whose
-// states are not kept), then for the first. 16 tokens' states and decays would take 128 registers and
-// leave one wave a SIMD.
+// A block's states are computed in two parts of HB tokens, the later first, each from the state kept before it:
+// 16 tokens' states and decays would take 128 registers and leave two waves a SIMD.
 template <int S, int NS, typename T>
 __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const SelectiveArgs a) {
   using SH = SelShape<S, NS>;
@@ -117,7 +113,7 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
   GradBlock<T, S, NS> next;
   if (more) {
     if (!cell.ends()) carry_back<N>(a, grp, cell, my, n0, A2, g);
-    next.load(a, w, cell, (cell.count - 1) / TB * TB, my, n0);
+    next.load(a, w, cell, (cell.count - 1) / TB * TB);
   }
   for (; more; cell = ahead) {
     more = prev_cell(a, cell.entry - 1, grp.e0 - 1, ahead);
@@ -128,8 +124,10 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
     }
     for (int t0 = (cell.count - 1) / TB * TB; t0 >= 0; t0 -= TB) {
       const GradBlock<T, S, NS> now = next;
-      if (t0 > 0) next.load(a, w, cell, t0 - TB, my, n0);
-      else if (more) next.load(a, w, ahead, (ahead.count - 1) / TB * TB, my, n0);
+      float h[TB / HB][NS];
+      part_states<N>(a, cell, t0, my, n0, h);
+      if (t0 > 0) next.load(a, w, cell, t0 - TB);
+      else if (more) next.load(a, w, ahead, (ahead.count - 1) / TB * TB);
       const bool on = t0 + w.t < cell.count;
       const int tok0 = cell.first + cell.pos + t0;
       {
@@ -164,23 +162,6 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
       }
       wave_lds_sync();
       char* const dbc = dbc_tile + (uint64_t)(uint32_t)tok0 * dbc_pitch;
-      float h[TB / HB][NS];  // the states before each part
-#pragma unroll
-      for (int i = 0; i < NS; ++i) h[0][i] = now.h0[i];
-#pragma unroll
-      for (int part = 1; part < TB / HB; ++part) {
-#pragma unroll
-        for (int i = 0; i < NS; ++i) h[part][i] = h[part - 1][i];
-#pragma unroll
-        for (int t = (part - 1) * HB; t < part * HB; ++t) {
-          const float2 v = *reinterpret_cast<const float2*>(&sv[wave][t][w.ch]);
-          float bb[NS];
-          Vec<float, NS>::load(&sb[wave][t][n0], bb);
-#pragma unroll
-          for (int i = 0; i < NS; ++i)
-            h[part][i] = fmaf(__builtin_amdgcn_exp2f(v.x * A2[i]), h[part][i], v.y * bb[i]);
-        }
-      }
 #pragma unroll
       for (int part = TB / HB - 1; part >= 0; --part) {
         float keep[KEEP][3];  // lane sg keeps the tokens that are sg modulo S
