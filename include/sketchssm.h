@@ -495,7 +495,8 @@ typedef struct {
  * where x before the sequence is the kept state's (zero without one), and
  *   y = a,  or with norm[p] = n > 0, over each run of n channels of part p:
  *   y = scale[p] * a / sqrt(sum a^2 + eps)
- * (the l2 norm of queries and keys per head, n = d_k).
+ * (the l2 norm of queries and keys per head, n = d_k; a run whose sum of squares passes fp32's range
+ * gives 0).
  *   x, y, dy, dx: parts arrays of rows, in_dtype;   weight fp32 [C][K], bias fp32 [C] or NULL;
  *   state: in_dtype [slots][K-1][C], a sequence's last K-1 inputs, oldest first.
  * A NaN or infinity in a token reaches the K tokens from it on (in the gradients the K-1 before them
@@ -567,7 +568,8 @@ ssm_status ssm_conv_step(const ssm_conv_dims* d, int32_t num_slots, const int32_
  * A NaN or infinity reaches what follows it in its own sequence (in the gradients all of its
  * sequence, and the sums over tokens); one in B or C every channel of its group.
  * d_state in {8, 16, 32, 64}; channels/groups a multiple of 16; channels <= 2^20; batch < 2^24;
- * (total_tokens/64 + batch) * channels/16 < 2^31; num_slots * channels < 2^38.
+ * (total_tokens/64 + batch) * channels/16 < 2^31; backward total_tokens * groups * d_state < 2^31;
+ * a step batch * channels * d_state < 2^34.
  */
 typedef struct {
   int32_t in_dtype; /* ssm_in_dtype of x, dt, z, B, C, out */

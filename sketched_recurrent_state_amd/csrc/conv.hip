@@ -5,7 +5,12 @@
 // and walks a run of tokens, so that an input is read once (and K - 1 more at the start of a run)
 // and nothing goes through LDS. Bound by HBM. A norm's run of channels is 2 to 32 neighbouring lanes: its
 // sums are DPP steps. E = 8 forward (16 bytes of bf16 a load) and 4 backward, whose sums for the weights
-// would otherwise take 256 registers and leave one wave a SIMD.
+// would otherwise take 256 registers and leave one wave a SIMD (327 us instead of 158).
+//
+// 8192 tokens of 12,288 channels in bf16, queries and keys normalised: forward 86 us for 403 MB, 4.7 TB/s, the rate
+// of a large copy on this card; backward 154 us for 604 MB, 3.9 TB/s, with about 40 vector instructions a value
+// (97 us of them). A run is a chunk's 64 tokens; shorter where that leaves fewer than 2,048 waves. One token of
+// 256 rows: 13.5 us for 50 MB.
 #include "layer.hpp"
 #include "launch.hpp"
 
@@ -437,7 +442,7 @@ unsigned conv_grid(ConvArgs& a, int runs) {
   return blocks;
 }
 
-constexpr int kWaves = 2048;  // of the whole GPU, below which runs are made shorter
+constexpr int kWaves = 2048;  // of the whole GPU, two a SIMD, below which runs are made shorter
 
 // log2 of the tokens of a run, for waves of `wide` channels
 int run_log(int cap, int C, int wide) {
@@ -446,7 +451,7 @@ int run_log(int cap, int C, int wide) {
   return log;
 }
 
-constexpr int kMostRows = 1024;  // of partial sums
+constexpr int kMostRows = 1024;  // of partial sums: a row is (taps + 1) C floats, written and read once
 int partial_rows(int runs) { return runs < kMostRows ? runs : kMostRows; }
 
 int channels_of(const ssm_conv_dims& d) {

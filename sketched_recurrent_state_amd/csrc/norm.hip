@@ -3,7 +3,9 @@
 //
 // One pass: a lane holds 8 channels of a group, which stay in registers between the group's statistics
 // and its result. A group of up to 512 channels is an aligned run of lanes of one wave, a wider one a
-// workgroup of as many waves as it needs. Bound by HBM.
+// workgroup of as many waves as it needs. Bound by HBM: 8192 rows of 32 groups of 128, fp32 in, bf16 gate and
+// result, 44 us for 268 MB (6.1 TB/s, half of it reads of what a caller has just written); backward of 4096 rows of
+// one group of 5,120 58 us for 294 MB (5.1 TB/s).
 #include "layer.hpp"
 #include "launch.hpp"
 

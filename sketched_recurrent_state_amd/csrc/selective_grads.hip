@@ -5,9 +5,14 @@
 //   dC = sum_channels dy h,  dB = sum_channels G delta x,
 //   e = sum_n G B,  dx = delta e + D dy,  ddelta = x e + sum_n G a h_{t-1} A,
 //   dA = sum_t delta G a h_{t-1},  dstate_in = a_0 G_0.
-// The states are computed again, a block of 16 tokens at a time, from those that a forward pass left
-// before every block. A wave's sums over channels are stored for each token and added up
-// afterwards in a fixed order; those over tokens stay in registers.
+// The states are computed again, from those that a forward pass left before every 8 tokens. A wave's
+// sums over channels are stored for each token and added up afterwards in a fixed order; those over tokens
+// stay in registers.
+//
+// Bound by the vector ALU: 2 x 2048 tokens, 5120 channels x 16 states, bf16, 302 us of 485 in all, 20 instructions a state
+// and token in the walk (4 to compute a state again, 10 for its gradients, 2 for the sums over a channel's lanes, 4 for
+// those over channels) and 4 around it; the vector ALU is busy nine tenths of the time at the clock it keeps.
+// Eight lanes a channel with two states each (168 registers without the parts) took 530 us.
 #include "selective.hpp"
 
 namespace ssm {

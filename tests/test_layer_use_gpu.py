@@ -142,6 +142,100 @@ def test_two_graphs_beside_eager_calls():
 
 
 # ---------------------------------------------------------------------------------
+# what a call may leave out, and where its outputs may go
+# ---------------------------------------------------------------------------------
+def test_optional_states():
+    """A kept state without a wanted one, a wanted one without a kept, and gradients of either alone."""
+    c = Conv("bf16", [20, 0, 2], [64, 32], [32, 0])
+    y, state = c.forward()
+    out = c.out()
+    ssm.conv_forward(c.d, c.T, c.plan, c.x, c.w, c.b, out, state_in=c.kept)
+    assert same(out, y)
+    whole = c.backward()
+    for end in (c.dend, None):
+        dx, dw, db, dk = c.out(), torch.empty_like(c.w), torch.empty_like(c.b), torch.empty_like(c.kept)
+        keep, c.dend = c.dend, end
+        ssm.conv_backward(c.d, c.T, c.plan, c.x, c.w, c.b, c.dy, dx, dw, db, state_in=c.kept, dstate=end)
+        assert end is None or (same(dx, whole["dx"]) and same(dw, whole["dw"]))
+        c.check_backward(c.backward())
+        c.dend = keep
+    s = Selective("f32", [20, 0, 2], 32, 16)
+    s.dend = None
+    s.check_backward(s.backward())
+    s.h0, s.dend = None, dev(np.random.default_rng(1).standard_normal((3, 32, 16)))
+    s.check_forward(*s.forward())
+    s.check_backward(s.backward())
+
+
+@pytest.mark.parametrize("without", ["gated", "skip", "bias", "soft"])
+def test_selective_step_without(without):
+    s = Selective("f32", [5], 48, 16, **{without: False}, pad=0)
+    pool, out = s.h0.clone(), s.rows()
+    d = ssm.SelectiveDims.make("f32", 1, 48, 16, softplus=s.soft)
+    for t in range(5):
+        at = slice(t, t + 1)
+        ssm.selective_step(d, s.x[at], s.dt[at], s.A, s.B[at], s.C[at], pool, out[at], D=s.D,
+                           z=None if s.z is None else s.z[at], dt_bias=s.bias)
+    s.check_forward(out, pool)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_outputs_in_wider_tensors(dtype):
+    """Every output of rows as a column range of a wider tensor whose other columns stay as they are."""
+    wide = []
+
+    def into(x):
+        w = torch.full((x.shape[0], x.shape[1] + 24), FILL, device="cuda", dtype=x.dtype)
+        wide.append((w, x.shape[1]))
+        return w[:, 8:8 + x.shape[1]]
+
+    c = Conv(dtype, [70, 3], [64, 40], [16, 0])
+    (y, state), back = c.forward(), c.backward()
+    out, dx = [into(v) for v in y], [into(v) for v in back["dx"]]
+    ssm.conv_forward(c.d, c.T, c.plan, c.x, c.w, c.b, out, torch.empty_like(state), state_in=c.kept)
+    ssm.conv_backward(c.d, c.T, c.plan, c.x, c.w, c.b, c.dy, dx, torch.empty_like(c.w), state_in=c.kept, dstate=c.dend)
+    assert same(out, y) and same(dx, back["dx"])
+    s = Selective(dtype, [70, 3], 48, 16)
+    (y, state), back = s.forward(), s.backward()
+    out = into(y)
+    ssm.selective_forward(s.d, s.T, s.plan, *s.inputs(), torch.empty_like(state), out, **s.more(), state_in=s.h0)
+    g = {k: into(back[k]) for k in ("dx", "ddt", "dB", "dC", "dz")}
+    ssm.selective_backward(s.d, s.T, s.plan, *s.inputs(), s.dout, g["dx"], g["ddt"], torch.empty_like(s.A), g["dB"],
+                           g["dC"], **s.more(), dD=torch.empty_like(s.D), dz=g["dz"],
+                           ddt_bias=torch.empty_like(s.bias), state_in=s.h0, dstate=s.dend)
+    assert same(out, y) and all(same(v, back[k]) for k, v in g.items())
+    for W, G in ((64, 3), (1032, 1)):
+        n = Norm("f32", dtype, 9, G, W)
+        y, back = n.forward(), n.backward()
+        out, dx, dz = into(y), into(back["dx"]), into(back["dz"])
+        ssm.gated_norm(n.d, 9, n.x, n.z, n.w, n.b, out)
+        ssm.gated_norm_backward(n.d, 9, n.x, n.z, n.w, n.b, n.dout, dx, dz, torch.empty_like(n.w))
+        assert same([out, dx, dz], [y, back["dx"], back["dz"]])
+    for w, width in wide:
+        assert (w[:, :8] == FILL).all() and (w[:, 8 + width:] == FILL).all()
+
+
+def test_norm_without_activation_in_the_convolution():
+    for norm in (16, 32, 64, 128):
+        c = Conv("f32", [40, 7], [norm, 3 * norm, 256], [norm, norm, 128], [2.0, 0.5, 1.0], silu=False, eps=0.5)
+        c.check_forward(*c.forward())
+        c.check_backward(c.backward())
+
+
+def test_large_and_tiny_values():
+    """Sums of squares that leave fp32's range above are 0 behind the norm; rows of zeros stay zeros."""
+    c = Conv("f32", [4], [32], [32], silu=False, bias=False, carried=False, pad=0)
+    c.w.zero_()
+    c.w[:, -1] = 1
+    c.x[0].copy_(torch.tensor([1e30, 0.0, 1e-30, 1.0], device="cuda")[:, None].expand(4, 32))
+    y, _ = c.forward()
+    assert (y[0][0] == 0).all() and (y[0][1] == 0).all() and (y[0][3] > 0.17).all()
+    assert (y[0][2] == y[0][2]).all() and (y[0][2] <= 1e-26).all()
+    o = c.backward()
+    assert all(torch.isfinite(v[1:]).all() for v in o["dx"])
+
+
+# ---------------------------------------------------------------------------------
 # the decoders with their convolution and norm
 # ---------------------------------------------------------------------------------
 class Layer:
