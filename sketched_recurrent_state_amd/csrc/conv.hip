@@ -5,11 +5,11 @@
 // and walks a run of tokens, so that an input is read once (and K - 1 more at the start of a run)
 // and nothing goes through LDS. Bound by HBM. A norm's run of channels is 2 to 32 neighbouring lanes: its
 // sums are DPP steps. E = 8 forward (16 bytes of bf16 a load) and 4 backward, whose sums for the weights
-// would otherwise take 256 registers and leave one wave a SIMD (327 us instead of 158).
+// would otherwise take 256 registers and leave one wave a SIMD (327 us instead of 158 for the case below).
 //
 // 8192 tokens of 12,288 channels in bf16, queries and keys normalised: forward 86 us for 403 MB, 4.7 TB/s, the rate
-// of a large copy on this card; backward 154 us for 604 MB, 3.9 TB/s, with about 40 vector instructions a value
-// (97 us of them). A run is a chunk's 64 tokens; shorter where that leaves fewer than 2,048 waves. One token of
+// of a large copy on this card; backward 140 us for 604 MB, 4.3 TB/s, its vector units issuing in 86 % of the cycles
+// (39 instructions a value). A run is a chunk's 64 tokens; shorter where that leaves fewer than 2,048 waves. One token of
 // 256 rows: 13.5 us for 50 MB.
 #include "layer.hpp"
 #include "launch.hpp"
@@ -53,6 +53,18 @@ __device__ __forceinline__ float run_sum(float x, int lanes) {
   if (lanes >= 32) x = xsum16(x);
   return x;
 }
+// The same of two values: as in the sum of one, but each test is made once.
+__device__ __forceinline__ void run_sums(float& x, float& y, int lanes) {
+  const auto both = [&](auto f) { x += f(x); y += f(y); };
+  both([](float v) { return dpp<DPP_QUAD_1032>(v); });
+  if (lanes >= 4) both([](float v) { return dpp<DPP_QUAD_2301>(v); });
+  if (lanes >= 8) both([](float v) { return dpp<DPP_HALF_MIRROR>(v); });
+  if (lanes >= 16) both([](float v) { return dpp<DPP_ROR8>(v); });
+  if (lanes >= 32) {
+    x = xsum16(x);
+    y = xsum16(y);
+  }
+}
 
 template <int K, int E>
 struct Taps {
@@ -91,9 +103,10 @@ template <int K, int E>
 __device__ __forceinline__ void conv_token(const ConvArgs& a, const ConvPart& P, const Taps<K, E>& taps,
                                            const float (*x)[E], float (&y)[E]) {
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const float u = taps.at(x, i);
-    y[i] = a.silu ? u * sigmoid(u) : u;
+  for (int i = 0; i < E; ++i) y[i] = taps.at(x, i);
+  if (a.silu) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) y[i] *= sigmoid(y[i]);
   }
   if (P.norm_lanes) {
     float s = 0.f;
@@ -225,10 +238,12 @@ __global__ void __launch_bounds__(NT) conv_forward_kernel(const ConvArgs a) {
 // Gradients. With g = dL/du, dx of a token is sum_j w_j g of the token K-1-j after it, so a run goes
 // on for K - 1 tokens behind its end (their g once more), and the first run of a sequence
 // makes the gradient of the kept inputs on the way.
-// Four waves a SIMD at the price of a few registers in memory: 151 us for 8192 tokens of 12,288 channels, 158
-// with three waves and none. (fp32, with twice the registers for what is read ahead, keeps three.)
+// The next four tokens' rows are on their way; a row's registers are filled again as soon as it is unpacked, and its
+// address is one step on from the row before (140 us for 8192 tokens of 12,288 channels; 152 with four rows unpacked,
+// then four fetched at products of their numbers). Three waves a SIMD: four would put 25 registers into memory
+// (190 us); eight tokens ahead 150 us.
 template <int K, typename T>
-__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 3) conv_backward_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(NT, 3) conv_backward_kernel(const ConvArgs a) {
   constexpr int E = EB, U = 4;
   const ConvLane l = conv_lane<E>(a);
   if (!l.active || l.run >= a.rows) return;
@@ -261,37 +276,39 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 3) conv_backward_kern
     const int steps = run.count + K - 1, with_g = min(steps, left);
     const int64_t t0 = (int64_t)run.first + run.pos;
     Packed<T, E> rx[U], ry[U];
-    const auto fetch = [&](int t) {  // rows behind the last are read again, and not used
+    const T *nx = P.x.row<T>(t0) + c, *ny = P.dy.row<T>(t0) + c;  // the row to be read next
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t at = t0 + min(t + i, with_g - 1);
-        rx[i].load(P.x.row<T>(at) + c);
-        ry[i].load(P.dy.row<T>(at) + c);
-      }
-    };
-    fetch(0);
+    for (int i = 0; i < U; ++i) {  // rows behind the last are read again, and not used
+      rx[i].load(nx);
+      ry[i].load(ny);
+      nx += i + 1 < with_g ? P.x.stride : 0;
+      ny += i + 1 < with_g ? P.dy.stride : 0;
+    }
+    T* px = P.dx.out<T>(t0) + c - (K - 1) * P.dx.stride;  // where dx of token t - (K - 1) goes
     for (int t = 0; t < steps; t += U) {
-      float dys[U][E];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        rx[i].unpack(x[K - 1 + i]);
-        ry[i].unpack(dys[i]);
-      }
-      if (t + U < steps) fetch(t + U);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         float(&gt)[E] = g[K - 1 + i];
-        float(&dy)[E] = dys[i];
+        float dy[E];
+        rx[i].unpack(x[K - 1 + i]);
+        ry[i].unpack(dy);
+        rx[i].load(nx);
+        ry[i].load(ny);
+        const bool more = t + i + U + 1 < with_g;
+        nx += more ? P.x.stride : 0;
+        ny += more ? P.dy.stride : 0;
         float act[E], slope[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float u = taps.at(x + i, e);
-          act[e] = u;
+          act[e] = taps.at(x + i, e);
           slope[e] = 1.f;
-          if (a.silu) {
-            const float s = sigmoid(u);
-            act[e] = u * s;
-            slope[e] = s * fmaf(u, 1.f - s, 1.f);
+        }
+        if (a.silu) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float s = sigmoid(act[e]);
+            act[e] *= s;
+            slope[e] = fmaf(act[e], 1.f - s, s);
           }
         }
         if (P.norm_lanes) {
@@ -301,10 +318,11 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 3) conv_backward_kern
             s = fmaf(act[e], act[e], s);
             d = fmaf(act[e], dy[e], d);
           }
-          const float r1 = __builtin_amdgcn_rsqf(run_sum(s, P.norm_lanes) + a.eps);
-          d = run_sum(d, P.norm_lanes) * r1 * r1;
+          run_sums(s, d, P.norm_lanes);
+          const float r1 = __builtin_amdgcn_rsqf(s + a.eps), f = P.scale * r1;
+          d *= -r1 * r1;
 #pragma unroll
-          for (int e = 0; e < E; ++e) dy[e] = P.scale * r1 * (dy[e] - act[e] * d);
+          for (int e = 0; e < E; ++e) dy[e] = f * fmaf(act[e], d, dy[e]);
         }
         const bool here = t + i < with_g;
 #pragma unroll
@@ -318,10 +336,10 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 3) conv_backward_kern
           }
         }
         // dx of the token K - 1 back
-        const int s = t + i - (K - 1), p = run.pos + s;
-        if (t + i < steps && (s >= 0 || (run.pos == 0 && a.dstate_in))) {
+        const int s = t + i - (K - 1);
+        if ((t + i < steps && (s >= 0 || (run.pos == 0 && a.dstate_in)))) {
           float dx[E];
-          const int end = p - (run.len - (K - 1));  // its row in the final state, if any
+          const int end = t + i - left;  // its row in the final state, if any
           if (a.dstate && end >= 0 && end < K - 1) {
             Vec<T, E>::load(static_cast<const T*>(a.dstate) +
                                 ((size_t)run.slot * (K - 1) + end) * a.C + P.offset + c,
@@ -334,7 +352,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 3) conv_backward_kern
 #pragma unroll
             for (int e = 0; e < E; ++e) dx[e] = fmaf(taps.w[e * K + j], g[K - 1 + i - j][e], dx[e]);
           if (s >= 0) {
-            store_channels(P.dx.out<T>(t0 + s) + c, dx);
+            store_channels(px + i * P.dx.stride, dx);
           } else {
             store_channels(static_cast<T*>(a.dstate_in) + ((size_t)run.slot * (K - 1) + t + i) * a.C +
                                P.offset + c,
@@ -342,6 +360,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 3) conv_backward_kern
           }
         }
       }
+      px += U * P.dx.stride;
 #pragma unroll
       for (int j = 0; j < K - 1; ++j)
 #pragma unroll
