@@ -515,7 +515,7 @@ typedef struct {
   int32_t channels[SSM_CONV_PARTS];
   int32_t norm[SSM_CONV_PARTS];
   float scale[SSM_CONV_PARTS];
-  float eps;          /* added to a run's sum of squares: > 0 with a norm   */
+  float eps;          /* added to a run's sum of squares: at least 2^-126 with a norm */
 } ssm_conv_dims;
 
 /* Bytes of the workspace of ssm_conv_backward. */
@@ -633,7 +633,8 @@ ssm_status ssm_selective_step(const ssm_selective_dims* d, int32_t num_slots, co
  *   o = n weight + bias,     out = o, or o s(z) (SSM_GATE_AFTER)
  *   x        x_dtype, rows of groups * width;   z, out  in_dtype, the same shape
  *   weight   fp32 [groups][width], or [width] for all groups (shared = 1);  bias the same or NULL
- * width a multiple of 8, at most 8192; groups * width <= 2^20; rows * groups < 2^31; eps > 0.
+ * width a multiple of 8, at most 8192; groups * width <= 2^20; rows * groups < 2^31;
+ * eps >= 2^-126. A group whose sum of squares passes fp32's range has n = 0.
  */
 typedef enum { SSM_GATE_NONE = 0, SSM_GATE_AFTER = 1, SSM_GATE_BEFORE = 2 } ssm_gate;
 typedef struct {

@@ -1,7 +1,7 @@
 // layer_abi.hip -- the extern "C" entry points of the short convolution, the selective recurrence and the
 // output norm: argument checks on the host, then the launches on the caller's stream. Nothing here
 // allocates, frees or synchronises. See include/sketchssm.h.
-#include <math.h>
+#include <float.h>
 
 #include "abi_checks.hpp"
 #include "layer.hpp"
@@ -55,6 +55,13 @@ ssm_status check_batch(int batch, int total, const char* fn) {
   return SSM_OK;
 }
 
+// The reciprocal root takes a smaller eps for 0, which would make NaN of a run of zeros.
+ssm_status check_eps(float eps, const char* fn) {
+  if (!(eps >= FLT_MIN))
+    return fail(SSM_E_RANGE, "%s: eps %g is not at least 2^-126", fn, (double)eps);
+  return SSM_OK;
+}
+
 ssm_status check_slots(int batch, int num_slots, const int32_t* slot, const char* fn) {
   if (num_slots < 1) return fail(SSM_E_SHAPE, "%s: num_slots %d < 1", fn, num_slots);
   if (slot == nullptr && batch > num_slots)
@@ -103,8 +110,7 @@ ssm_status check_conv(const ssm_conv_dims* d, int total, const char* fn, int& C)
     sum += c;
   }
   if (sum > kMaxChannels) return fail(SSM_E_SHAPE, "%s: %lld channels > 2^20", fn, sum);
-  if (normed && !(d->eps > 0.f))
-    return fail(SSM_E_RANGE, "%s: eps %g is not positive", fn, (double)d->eps);
+  if (normed && (st = check_eps(d->eps, fn)) != SSM_OK) return st;
   const long long tiles = (sum + 511) / 512;
   if (((long long)total / ssm::CT + d->batch) * tiles >= (1LL << 24))
     return fail(SSM_E_SHAPE, "%s: (total_tokens/64 + batch) * ceil(channels/512) >= 2^24", fn);
@@ -249,8 +255,7 @@ ssm_status check_norm(const ssm_norm_dims* d, int rows, const char* fn) {
     return fail(SSM_E_RANGE, "%s: activation %d is not 1 (silu) or 2 (sigmoid)", fn, d->activation);
   if ((d->shared != 0 && d->shared != 1) || (d->centred != 0 && d->centred != 1))
     return fail(SSM_E_RANGE, "%s: shared %d and centred %d are 0 or 1", fn, d->shared, d->centred);
-  if (!(d->eps > 0.f)) return fail(SSM_E_RANGE, "%s: eps %g is not positive", fn, (double)d->eps);
-  return SSM_OK;
+  return check_eps(d->eps, fn);
 }
 
 // The arrays of both directions.

@@ -377,6 +377,20 @@ def test_norm_refusals():
     assert norm_backward(d, nbytes=ssm.gated_norm_sizes(d, 10) - 1)[0] == 4
 
 
+@pytest.mark.parametrize("eps", [2.0 ** -149, 2.0 ** -127, -1e-6])
+def test_eps_below_the_normal_numbers(eps):
+    """The kernels' reciprocal root takes them for 0, and 0 / 0 is not the formula's 0."""
+    for f in (conv_forward, conv_backward, conv_step):
+        st, msg = f(conv_dims(eps=eps))
+        assert st == 4 and "eps" in msg
+    for f in (norm_forward, norm_backward):
+        st, msg = f(norm_dims(eps=eps))
+        assert st == 4 and "eps" in msg
+    assert ssm.conv_sizes(conv_dims(eps=eps, norm=[0, 0, 0]), 10) > 0  # not used without a norm
+    assert ssm.conv_sizes(conv_dims(eps=2.0 ** -126), 10) > 0
+    assert ssm.gated_norm_sizes(norm_dims(eps=2.0 ** -126), 10) > 0
+
+
 def test_binding_checks():
     torch = pytest.importorskip("torch")
     x = torch.zeros(3, 256, dtype=torch.bfloat16)
