@@ -31,7 +31,7 @@ from . import (ConvDims, Dims, IN_BF16, IN_F32, KDA, MAMBA2, NormDims, SKETCH_BF
                rank_offsets, recurrent_decode_step, scan_forward, scan_plan,
                selective_forward, selective_step, sketch_decode_step, sketch_decode_step_ls,
                sketch_decode_step_ranked, window_update_refresh, window_update_refresh_ls,
-               window_update_refresh_ranked)
+               window_update_refresh_ranked, _addr, _row_addr)
 
 
 def _in_type(in_dtype: int) -> torch.dtype:
@@ -118,6 +118,16 @@ class GatedNorm:
     def __init__(self, dims: NormDims, weight: torch.Tensor, bias: Optional[torch.Tensor] = None):
         self.d, self.weight, self.bias = dims, weight, bias
 
+    def check(self, rows: int, gate: Optional[torch.Tensor]) -> None:
+        """Raises where the norm would: a gate for `rows` rows that is missing, not wanted or not such rows,
+        weights that are not the dimensions'."""
+        if (gate is None) != (self.d.gate == 0):
+            raise ValueError("gate: " + ("the norm needs one" if gate is None else "the norm has none"))
+        wide = self.d.groups * self.d.width
+        _row_addr(gate, "gate", (_in_type(self.d.in_dtype),), rows, wide)
+        for w, name in ((self.weight, "weight"), (self.bias, "bias")):
+            _addr(w, name, (torch.float32,), self.d.width if self.d.shared else wide)
+
     def __call__(self, x: torch.Tensor, gate: Optional[torch.Tensor] = None) -> torch.Tensor:
         """x [rows][groups][width], gate rows of as many channels: a new tensor of x's shape."""
         out = torch.empty(x.shape, device=x.device, dtype=_in_type(self.d.in_dtype))
@@ -134,6 +144,24 @@ def _around(d: Dims, conv: Optional[ShortConv], norm: Optional[GatedNorm]) -> No
     if norm is not None:
         if (norm.d.groups, norm.d.width, norm.d.x_dtype) != (d.heads, d.d_v, IN_F32):
             raise ValueError(f"{norm.d} does not take the outputs of {d}")
+
+
+def _check_around(d: Dims, rows: int, conv, norm, decay, beta, gate, *ys) -> None:
+    """What the recurrence or the norm would refuse is refused before the convolution or the recurrence has
+    written its state: a call either does all of its work or none."""
+    if norm is not None:
+        norm.check(rows, gate)
+    elif gate is not None:
+        raise ValueError("gate: the decoder has no norm")
+    if conv is None:
+        return
+    if decay is None or (beta is None) != (d.rule == MAMBA2):
+        raise ValueError("decay and beta: every rule needs decay, all but Mamba-2 beta")
+    units, f32 = rows * d.heads, (torch.float32,)
+    _addr(decay, "decay", f32, units * d.d_k if d.rule == KDA else units)
+    _addr(beta, "beta", f32, units)
+    for y in ys:
+        _addr(y, "y", f32, units * d.d_v)
 
 
 def _heads(d: Dims, parts):
@@ -265,6 +293,7 @@ class WindowedDecoder:
         the device are not read back: prompts are cut where the token arrays end, and outputs
         behind the last prompt are zero."""
         lengths = _checked_lengths(self.d, lengths, q)
+        _check_around(self.d, q.shape[0], self.conv, self.norm, decay, beta, gate)
         with torch.cuda.device_of(self.state):  # the flush and the refresh on the scan's stream
             if self.tau:
                 self.flush()
@@ -278,6 +307,7 @@ class WindowedDecoder:
         norm what the norm makes of it."""
         d = self.d
         tau = self.tau + 1
+        _check_around(d, d.batch, self.conv, self.norm, decay, beta, gate, y, y_full)
         if self.conv is not None:
             q, k, v = _heads(d, self.conv.step(q, k, v))
         N, H, dv = d.batch, d.heads, d.d_v
@@ -318,6 +348,7 @@ class RecurrentDecoder:
 
     def step(self, q, k, v, decay, beta=None, *, gate=None, y=None):
         d = self.d
+        _check_around(d, d.batch, self.conv, self.norm, decay, beta, gate, y)
         if self.conv is not None:
             q, k, v = _heads(d, self.conv.step(q, k, v))
         if y is None:
@@ -329,6 +360,7 @@ class RecurrentDecoder:
         """Take a packed batch of prompts into the state; returns their outputs (lengths and
         outputs as in WindowedDecoder.prefill)."""
         lengths = _checked_lengths(self.d, lengths, q)
+        _check_around(self.d, q.shape[0], self.conv, self.norm, decay, beta, gate)
         with torch.cuda.device_of(self.state):
             return _prefill(self.d, self.state, lengths, q, k, v, decay, beta, self.conv, self.norm, gate)
 

@@ -353,6 +353,34 @@ def test_decoder_refusals():
         ShortConv(l.cd, l.w).prefill([3, 2], l.q, l.k, l.v)
 
 
+@pytest.mark.parametrize("which", ["recurrent", "full", "sketch"])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_refused_calls_leave_the_state(which, prefill):
+    """What the recurrence or the norm refuses is refused before the convolution has taken the token."""
+    l = Layer("gdn", "bf16", 2, 2, 32, 32, 2)
+    dec = l.decoder(which)
+    (q, k, v, decay, beta), z = l.tokens(slice(0, 2))
+    call = (lambda *a, **kw: dec.prefill([1, 1], *a, **kw)) if prefill else dec.step
+    call(q, k, v, decay, beta, gate=z)
+    held = [dec.conv.state, dec.state] + ([] if which == "recurrent" else [dec.k_buf, dec.v_buf])
+    before = [x.clone() for x in held]
+    bad = torch.zeros(3, device="cuda")
+    for args, kw in [((decay, beta), {}), ((decay, beta), dict(gate=z[:1])), ((decay, beta), dict(gate=z.float())),
+                     ((decay,), dict(gate=z)), ((bad, beta), dict(gate=z)), ((decay, bad), dict(gate=z)),
+                     ((None, beta), dict(gate=z)), ((decay.double(), beta), dict(gate=z))]:
+        with pytest.raises((ValueError, TypeError)):
+            call(q, k, v, *args, **kw)
+    weight, dec.norm.weight = dec.norm.weight, bad
+    with pytest.raises(ValueError, match="weight"):
+        call(q, k, v, decay, beta, gate=z)
+    norm, dec.norm = dec.norm, None
+    with pytest.raises(ValueError, match="no norm"):
+        call(q, k, v, decay, beta, gate=z)
+    dec.norm, norm.weight = norm, weight
+    assert all(torch.equal(x, y) for x, y in zip(held, before))
+    assert call(q, k, v, decay, beta, gate=z).shape == (2, 2, 32)
+
+
 def test_lengths_on_the_device():
     """Prompts that fill the arrays in part: rows behind them are zero, also behind a norm with a bias."""
     T = 64
