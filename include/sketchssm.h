@@ -568,8 +568,8 @@ ssm_status ssm_conv_step(const ssm_conv_dims* d, int32_t num_slots, const int32_
  * A NaN or infinity reaches what follows it in its own sequence (in the gradients all of its
  * sequence, and the sums over tokens); one in B or C every channel of its group.
  * d_state in {8, 16, 32, 64}; channels/groups a multiple of 16; channels <= 2^20; batch < 2^24;
- * (total_tokens/64 + batch) * channels/16 < 2^31; backward total_tokens * groups * d_state < 2^31;
- * a step batch * channels * d_state < 2^34.
+ * (total_tokens/64 + batch) * channels/16 < 2^31; backward total_tokens * groups * d_state <= 2^31 - 128;
+ * a step batch * channels * max(d_state, 16) < 2^34.
  */
 typedef struct {
   int32_t in_dtype; /* ssm_in_dtype of x, dt, z, B, C, out */

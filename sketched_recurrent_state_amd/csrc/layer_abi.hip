@@ -482,8 +482,8 @@ ssm_status ssm_selective_backward(const ssm_selective_dims* d, int32_t total_tok
   static const char* fn = "ssm_selective_backward";
   ssm_status st = check_selective(d, total_tokens, fn);
   if (st != SSM_OK) return st;
-  if ((long long)total_tokens * d->groups * d->d_state >= (1LL << 31))
-    return fail(SSM_E_SHAPE, "%s: total_tokens * groups * d_state >= 2^31", fn);
+  if ((long long)total_tokens * d->groups * d->d_state > (1LL << 31) - 128)  // twice that: threads of a grid
+    return fail(SSM_E_SHAPE, "%s: total_tokens * groups * d_state > 2^31 - 128", fn);
   if (d->batch > 0 && plan == nullptr) return fail(SSM_E_NULL, "%s: plan is NULL", fn);
   if (grads == nullptr) return fail(SSM_E_NULL, "%s: grads is NULL", fn);
   const ssm::SelectiveWork w = ssm::selective_work(*d, total_tokens, true, workspace);
@@ -554,8 +554,8 @@ ssm_status ssm_selective_step(const ssm_selective_dims* d, int32_t num_slots, co
   ssm_status st = check_selective(d, 0, fn);
   if (st != SSM_OK) return st;
   if (d->batch == 0) return ok();
-  if ((long long)d->batch * d->channels * d->d_state >= (1LL << 34))
-    return fail(SSM_E_SHAPE, "%s: batch * channels * d_state >= 2^34", fn);
+  if ((long long)d->batch * d->channels * (d->d_state > 16 ? d->d_state : 16) >= (1LL << 34))
+    return fail(SSM_E_SHAPE, "%s: batch * channels * max(d_state, 16) >= 2^34", fn);
   if (state == nullptr) return fail(SSM_E_NULL, "%s: state is NULL", fn);
   if ((st = check_slots(d->batch, num_slots, slot, fn)) != SSM_OK) return st;
   Arrays arrs;

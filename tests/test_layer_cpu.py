@@ -391,6 +391,15 @@ def test_eps_below_the_normal_numbers(eps):
     assert ssm.gated_norm_sizes(norm_dims(eps=2.0 ** -126), 10) > 0
 
 
+def test_selective_grids_below_32_bits():
+    """Calls whose launches would have 2^32 threads: a token of 2047 rows of 2^20 channels x 8 states (a lane has 2 of
+    them, for two rows), and dB and dC (a thread each) of 2^27 - 1 tokens x 16 states."""
+    st, msg = sel_step(sel_dims(batch=2047, channels=1 << 20, d_state=8, groups=1), num_slots=2047)
+    assert st == 2 and "batch * channels" in msg
+    st, msg = sel_backward(sel_dims(groups=1), total=(1 << 27) - 1)
+    assert st == 2 and "total_tokens" in msg
+
+
 def test_binding_checks():
     torch = pytest.importorskip("torch")
     x = torch.zeros(3, 256, dtype=torch.bfloat16)
