@@ -72,7 +72,8 @@ struct SelectiveWork {
   float* local;    // [groups][channels][d_state]  the state it leaves, from zero (or the sequence's start)
   float* sums;     // [groups][channels]           the sum of its deltas
   float* back;     // backward: [groups][channels][d_state]  the gradient that leaves it at its start
-  float* states;   // backward: the state before every 8 tokens of a sequence but its first
+  float* states;   // backward: the state before every 8 tokens of a sequence but its first, from the group's zero
+  float* until;    // backward: [those places][channels]  the sum of delta from the group's start
   float* dbc;      // [tokens + 1][tiles][2][d_state]  dB and dC of a wave's channels
   float* partial;  // [groups][channels][d_state + 2]  dA, dD, ddt_bias of a group's tokens
   size_t bytes;

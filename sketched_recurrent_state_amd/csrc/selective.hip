@@ -5,17 +5,16 @@ namespace ssm {
 
 namespace {
 
-// The main pass over a group. OUT: outputs and final states. Otherwise (the backward pass's second
-// kernel): the state before every HB tokens but the sequence's first.
-template <int S, int NS, typename T, bool OUT>
+// The main pass over a group: outputs and final states.
+template <int S, int NS, typename T>
 __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const SelectiveArgs a) {
   using SH = SelShape<S, NS>;
-  using Block = SelBlock<T, S, NS, OUT, OUT, false>;
+  using Block = SelBlock<T, S, NS, true, true, false>;
   constexpr int N = SH::N, CH = SH::CH, EC = SH::EC, EN = SH::EN;
   __shared__ __align__(16) float2 sv[WAVES][TB][CH + 1];  // delta, delta x; a row of 16 channels more would
                                                           // start in the same bank again
-  __shared__ __align__(16) float sb[WAVES][TB][N], sc[WAVES][OUT ? TB : 1][N];
-  __shared__ float sy[WAVES][OUT ? TB : 1][CH];
+  __shared__ __align__(16) float sb[WAVES][TB][N], sc[WAVES][TB][N];
+  __shared__ float sy[WAVES][TB][CH];
   __shared__ __align__(16) float sbias[WAVES][CH], sskip[WAVES][CH];
   const int wave = scalar(threadIdx.x >> 6), tiles = a.channels / CH;
   const int tile_blocks = (tiles + WAVES - 1) / WAVES;
@@ -31,7 +30,7 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
   stage_channels(sbias[wave], a.dt_bias, w);
   stage_channels(sskip[wave], a.D, w);
   wave_lds_sync();
-  if (OUT && a.state != a.state_in)
+  if (a.state != a.state_in)
     for_empty_sequences(a, grp, [&](int, int slot) {
       const size_t at = ((size_t)slot * a.channels + my) * N + n0;
       float v[NS];
@@ -58,13 +57,6 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
       const int tok0 = c.first + c.pos + t0;
       if (t0 + TB < c.count) next.load(a, w, c, t0 + TB);
       else if (more) next.load(a, w, ahead, 0);
-      const auto keep_state = [&](int t) {
-        const size_t part = (size_t)(c.first / HB + (c.pos + t0 + t) / HB - 1);
-        Vec<float, NS>::store(a.w.states + part * a.channels * N + (uint32_t)(my * N + n0), h);
-      };
-      if constexpr (!OUT) {
-        if (c.pos + t0 > 0) keep_state(0);
-      }
       float x[EC], dt[EC], delta[EC], bias[EC], b[EN], cc[EN];
       now.x.unpack(x);
       now.dt.unpack(dt);
@@ -76,61 +68,50 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
 #pragma unroll
       for (int i = 0; i < EC; ++i) sv[wave][w.t][w.q * EC + i] = make_float2(delta[i], delta[i] * x[i]);
       Vec<float, EN>::store(&sb[wave][w.t][w.q * EN], b);
-      if constexpr (OUT) {
-        now.c.unpack(cc);
-        Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], cc);
-      }
+      now.c.unpack(cc);
+      Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], cc);
       wave_lds_sync();
       float y[(TB + S - 1) / S];  // lane sg keeps the tokens that are sg modulo S
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
-        if constexpr (!OUT)
-          if (t == HB && t0 + HB < c.count) keep_state(HB);
         const float2 v = sv[wave][t][w.ch];
         float bb[NS], ct[NS], yt = 0.f;
         Vec<float, NS>::load(&sb[wave][t][n0], bb);
-        if constexpr (OUT) Vec<float, NS>::load(&sc[wave][t][n0], ct);
+        Vec<float, NS>::load(&sc[wave][t][n0], ct);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           h[i] = fmaf(__builtin_amdgcn_exp2f(v.x * A[i]), h[i], v.y * bb[i]);
-          if constexpr (OUT) yt = fmaf(ct[i], h[i], yt);
+          yt = fmaf(ct[i], h[i], yt);
         }
-        if constexpr (OUT) {
-          yt = state_sum<S>(yt);
-          y[t / S] = t % S == 0 ? yt : w.sg == t % S ? yt : y[t / S];
-        }
+        yt = state_sum<S>(yt);
+        y[t / S] = t % S == 0 ? yt : w.sg == t % S ? yt : y[t / S];
       }
-      if constexpr (OUT) {
 #pragma unroll
-        for (int i = 0; i < TB / S; ++i) sy[wave][i * S + w.sg][w.ch] = y[i];
-        wave_lds_sync();
-        if (on) {
-          float z[EC], o[EC], skip[EC];
-          now.z.unpack(z);
-          Vec<float, EC>::load(&sskip[wave][w.q * EC], skip);
+      for (int i = 0; i < TB / S; ++i) sy[wave][i * S + w.sg][w.ch] = y[i];
+      wave_lds_sync();
+      if (on) {
+        float z[EC], o[EC], skip[EC];
+        now.z.unpack(z);
+        Vec<float, EC>::load(&sskip[wave][w.q * EC], skip);
 #pragma unroll
-          for (int i = 0; i < EC; ++i) o[i] = fmaf(skip[i], x[i], sy[wave][w.t][w.q * EC + i]);
-          apply_gate(a, z, o);
-          store_row<T, EC>(row_at<T>(a.out, tok0, w.t, w.c0 + w.q * EC), o);
-        }
+        for (int i = 0; i < EC; ++i) o[i] = fmaf(skip[i], x[i], sy[wave][w.t][w.q * EC + i]);
+        apply_gate(a, z, o);
+        store_row<T, EC>(row_at<T>(a.out, tok0, w.t, w.c0 + w.q * EC), o);
       }
       wave_lds_sync();
     }
-    if (OUT && c.ends()) Vec<float, NS>::store(a.state + at, h);
+    if (c.ends()) Vec<float, NS>::store(a.state + at, h);
   }
 }
 
-// The local pass. Forward: the state that the group's last sequence leaves, if it goes on behind the
-// group. BWD: also the gradient that the group's first sequence leaves at the group's start, if it began
-// before. A group inside one sequence makes both in one walk.
-template <int S, int NS, typename T, bool BWD>
+// The local pass: the state that the group's last sequence leaves, if it goes on behind the group.
+template <int S, int NS, typename T>
 __global__ void __launch_bounds__(64 * WAVES) selective_local_kernel(const SelectiveArgs a) {
   using SH = SelShape<S, NS>;
-  using Block = SelBlock<T, S, NS, BWD, BWD, BWD>;
+  using Block = SelBlock<T, S, NS, false, false, false>;
   constexpr int N = SH::N, CH = SH::CH, EC = SH::EC, EN = SH::EN;
-  using V = std::conditional_t<BWD, float4, float2>;
-  __shared__ __align__(16) V sv[WAVES][TB][CH + 1];  // delta, delta x, and backwards dL/dy
-  __shared__ __align__(16) float sb[WAVES][TB][N], sc[WAVES][BWD ? TB : 1][N];
+  __shared__ __align__(16) float2 sv[WAVES][TB][CH + 1];  // delta, delta x
+  __shared__ __align__(16) float sb[WAVES][TB][N];
   __shared__ __align__(16) float sbias[WAVES][CH];
   const int wave = scalar(threadIdx.x >> 6), tiles = a.channels / CH;
   const int tile_blocks = (tiles + WAVES - 1) / WAVES;
@@ -138,109 +119,55 @@ __global__ void __launch_bounds__(64 * WAVES) selective_local_kernel(const Selec
   if (tile >= tiles) return;
   const SelTile w = sel_tile<S>(a, tile);
   const SelGroup grp = sel_group(a, blockIdx.x / tile_blocks);
-  SelCell first, last;
-  if (!next_cell(a, grp.e0, grp.e1, first) || !prev_cell(a, grp.e1 - 1, grp.e0 - 1, last)) return;
-  const bool goes_on = !last.ends();                     // the last sequence, behind the group
-  const bool began = BWD && !first.starts();             // the first sequence, before it
-  if (!goes_on && !began) return;
+  SelCell c, last;
+  if (!prev_cell(a, grp.e1 - 1, grp.e0 - 1, last) || last.ends()) return;
+  if (!next_cell(a, max(seq_entry(a, last.seq), grp.e0), grp.e1, c) || c.seq != last.seq) return;
   const int my = w.c0 + w.ch, n0 = w.sg * NS;
-  float A[NS];
+  float A[NS], h[NS], sum = 0.f;
   Vec<float, NS>::load(a.A + (size_t)my * N + n0, A);
 #pragma unroll
   for (int i = 0; i < NS; ++i) A[i] *= kLog2e;
   stage_channels(sbias[wave], a.dt_bias, w);
   wave_lds_sync();
-
-  // Walks from chunk c to the end of its sequence or of the group. leaves: the gradient is wanted.
-  auto walk = [&](SelCell c, bool leaves) {
-    const int seq = c.seq;
-    float h[NS], g[NS], p[NS], sum = 0.f;
-    zero(h);
-    zero(g);
+  zero(h);
+  if (c.starts() && a.state_in)
+    Vec<float, NS>::load(a.state_in + (size_t)c.slot * a.channels * N + (uint32_t)(my * N + n0), h);
+  Block next;
+  next.load(a, w, c, 0);
+  SelCell ahead;
+  for (bool more = true; more; c = ahead) {
+    more = next_cell(a, c.entry + 1, grp.e1, ahead);
+    for (int t0 = 0; t0 < c.count; t0 += TB) {
+      const Block now = next;
+      const bool on = t0 + w.t < c.count;
+      if (t0 + TB < c.count) next.load(a, w, c, t0 + TB);
+      else if (more) next.load(a, w, ahead, 0);
+      float x[EC], dt[EC], delta[EC], bias[EC], b[EN];
+      now.x.unpack(x);
+      now.dt.unpack(dt);
+      now.b.unpack(b);
+      Vec<float, EC>::load(&sbias[wave][w.q * EC], bias);
 #pragma unroll
-    for (int i = 0; i < NS; ++i) p[i] = 1.f;
-    if (c.starts() && a.state_in)
-      Vec<float, NS>::load(a.state_in + (size_t)c.slot * a.channels * N + (uint32_t)(my * N + n0), h);
-    Block next;
-    next.load(a, w, c, 0);
-    SelCell ahead, end = c;
-    for (bool more = true; more; c = ahead) {
-      end = c;
-      more = next_cell(a, c.entry + 1, grp.e1, ahead) && ahead.seq == seq;
-      for (int t0 = 0; t0 < c.count; t0 += TB) {
-        const Block now = next;
-        const bool on = t0 + w.t < c.count;
-        if (t0 + TB < c.count) next.load(a, w, c, t0 + TB);
-        else if (more) next.load(a, w, ahead, 0);
-        float x[EC], dt[EC], delta[EC], bias[EC], b[EN], cc[EN], z[EC], dy[EC];
-        now.x.unpack(x);
-        now.dt.unpack(dt);
-        now.b.unpack(b);
-        if constexpr (BWD) {
-          now.z.unpack(z);
-          now.dy.unpack(dy);
-          now.c.unpack(cc);
-        }
-        Vec<float, EC>::load(&sbias[wave][w.q * EC], bias);
+      for (int i = 0; i < EC; ++i) dt[i] += bias[i];
+      steps(a, dt, t0 + TB <= c.count, on, delta);
 #pragma unroll
-        for (int i = 0; i < EC; ++i) dt[i] += bias[i];
-        steps(a, dt, t0 + TB <= c.count, on, delta);
-        if constexpr (BWD) apply_gate(a, z, dy);
+      for (int i = 0; i < EC; ++i) sv[wave][w.t][w.q * EC + i] = make_float2(delta[i], delta[i] * x[i]);
+      Vec<float, EN>::store(&sb[wave][w.t][w.q * EN], b);
+      wave_lds_sync();
 #pragma unroll
-        for (int i = 0; i < EC; ++i) {
-          if constexpr (BWD)
-            sv[wave][w.t][w.q * EC + i] = make_float4(delta[i], delta[i] * x[i], dy[i], 0.f);
-          else
-            sv[wave][w.t][w.q * EC + i] = make_float2(delta[i], delta[i] * x[i]);
-        }
-        Vec<float, EN>::store(&sb[wave][w.t][w.q * EN], b);
-        if constexpr (BWD) Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], cc);
-        wave_lds_sync();
+      for (int t = 0; t < TB; ++t) {
+        const float2 v = sv[wave][t][w.ch];
+        float bb[NS];
+        Vec<float, NS>::load(&sb[wave][t][n0], bb);
+        sum += v.x;
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-          const V v = sv[wave][t][w.ch];
-          float bb[NS], ct[NS], d = 0.f;
-          Vec<float, NS>::load(&sb[wave][t][n0], bb);
-          if constexpr (BWD) {
-            Vec<float, NS>::load(&sc[wave][t][n0], ct);
-            d = v.z;
-          }
-          sum += v.x;
-#pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            const float decay = __builtin_amdgcn_exp2f(v.x * A[i]);
-            h[i] = fmaf(decay, h[i], v.y * bb[i]);
-            if constexpr (BWD) {
-              p[i] *= decay;
-              g[i] = fmaf(p[i], ct[i] * d, g[i]);
-            }
-          }
-        }
-        wave_lds_sync();
+        for (int i = 0; i < NS; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(v.x * A[i]), h[i], v.y * bb[i]);
       }
+      wave_lds_sync();
     }
-    const size_t at = ((size_t)grp.g * a.channels + my) * N + n0;
-    if (!end.ends()) {
-      Vec<float, NS>::store(a.w.local + at, h);
-      if (w.sg == 0) a.w.sums[(size_t)grp.g * a.channels + my] = sum;
-    }
-    if constexpr (BWD) {
-      if (leaves) {
-        if (end.ends() && a.dstate) {
-          float l[NS];
-          Vec<float, NS>::load(a.dstate + ((size_t)end.slot * a.channels + my) * N + n0, l);
-#pragma unroll
-          for (int i = 0; i < NS; ++i) g[i] = fmaf(p[i], l[i], g[i]);
-        }
-        Vec<float, NS>::store(a.w.back + at, g);
-      }
-    }
-  };
-  if (began) walk(first, true);
-  if (goes_on && !(began && last.seq == first.seq)) {
-    const int e = max(seq_entry(a, last.seq), grp.e0);
-    if (next_cell(a, e, grp.e1, first) && first.seq == last.seq) walk(first, false);
   }
+  Vec<float, NS>::store(a.w.local + ((size_t)grp.g * a.channels + my) * N + n0, h);
+  if (w.sg == 0) a.w.sums[(size_t)grp.g * a.channels + my] = sum;
 }
 
 // Single tokens: a lane holds 4 states of a channel (2 where d_state = 8), so that a wave's state is
@@ -308,25 +235,6 @@ __global__ void __launch_bounds__(256) selective_step_kernel(const SelectiveArgs
   }
 }
 
-// Launches a pass over the groups: f(S, NS, type, grid).
-template <typename F>
-hipError_t over_groups(const ssm_selective_dims& d, const SelectiveArgs& a, F&& f) {
-  const unsigned tile_blocks = (unsigned)(selective_tiles(d) + WAVES - 1) / WAVES;
-  return selective_dispatch(d, [&](auto S, auto NS, auto T) {
-    f(S, NS, T, dim3(tile_blocks * (unsigned)a.time_groups));
-    return hipGetLastError();
-  });
-}
-
-template <bool OUT>
-hipError_t launch_scan_pass(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream) {
-  return over_groups(d, a, [&](auto S, auto NS, auto T, dim3 grid) {
-    hipLaunchKernelGGL((selective_scan_kernel<decltype(S)::value, decltype(NS)::value,
-                                              typename decltype(T)::type, OUT>),
-                       grid, dim3(64 * WAVES), 0, stream, a);
-  });
-}
-
 }  // namespace
 
 // Ten waves a SIMD of the whole GPU in all (5 of the forward pass's and 3 of the gradients' are resident at
@@ -345,26 +253,6 @@ SelGroups selective_groups(const ssm_selective_dims& d, int cap) {
   return SelGroups{chunks, (cap + chunks - 1) / chunks};
 }
 
-hipError_t launch_selective_local(const ssm_selective_dims& d, SelectiveArgs& a, bool backward,
-                                  hipStream_t stream) {
-  const SelGroups g = selective_groups(d, a.plan.cap);
-  a.time_groups = g.groups;
-  a.group_chunks = g.chunks;
-  if (g.groups == 1) return hipSuccess;
-  return over_groups(d, a, [&](auto S, auto NS, auto T, dim3 grid) {
-    constexpr int s = decltype(S)::value, ns = decltype(NS)::value;
-    using TI = typename decltype(T)::type;
-    if (backward)
-      hipLaunchKernelGGL((selective_local_kernel<s, ns, TI, true>), grid, dim3(64 * WAVES), 0, stream, a);
-    else
-      hipLaunchKernelGGL((selective_local_kernel<s, ns, TI, false>), grid, dim3(64 * WAVES), 0, stream, a);
-  });
-}
-
-hipError_t launch_selective_states(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream) {
-  return launch_scan_pass<false>(d, a, stream);
-}
-
 SelectiveWork selective_work(const ssm_selective_dims& d, int total, bool backward, void* base) {
   SelectiveWork w{};
   const SelGroups g = selective_groups(d, d.batch > 0 ? scan_capacity(total, d.batch) : 0);
@@ -375,13 +263,14 @@ SelectiveWork selective_work(const ssm_selective_dims& d, int total, bool backwa
     at += floats * sizeof(float);  // channels are a multiple of 16, so every part is one of 64 bytes
     return p;
   };
-  if (g.groups > 1) {
+  if (g.groups > 1 || backward) {  // backwards a wrong plan's only group may claim to go on
     w.local = take(g.groups * states);
     w.sums = take((size_t)g.groups * d.channels);
   }
   if (backward) {
-    if (g.groups > 1) w.back = take(g.groups * states);
+    w.back = take(g.groups * states);
     w.states = take(((size_t)total / HB + 1) * states);
+    w.until = take(((size_t)total / HB + 1) * d.channels);
     w.dbc = take(((size_t)total + 1) * selective_tiles(d) * 2 * d.d_state);
     w.partial = take((size_t)g.groups * d.channels * (d.d_state + 2));
   }
@@ -390,8 +279,16 @@ SelectiveWork selective_work(const ssm_selective_dims& d, int total, bool backwa
 }
 
 hipError_t launch_selective_forward(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream) {
-  const hipError_t e = launch_selective_local(d, a, false, stream);
-  return e == hipSuccess ? launch_scan_pass<true>(d, a, stream) : e;
+  const SelGroups g = selective_groups(d, a.plan.cap);
+  a.time_groups = g.groups;
+  a.group_chunks = g.chunks;
+  return over_groups(d, a, [&](auto S, auto NS, auto T, dim3 grid) {
+    constexpr int s = decltype(S)::value, ns = decltype(NS)::value;
+    using TI = typename decltype(T)::type;
+    if (g.groups > 1)
+      hipLaunchKernelGGL((selective_local_kernel<s, ns, TI>), grid, dim3(64 * WAVES), 0, stream, a);
+    hipLaunchKernelGGL((selective_scan_kernel<s, ns, TI>), grid, dim3(64 * WAVES), 0, stream, a);
+  });
 }
 
 hipError_t launch_selective_step(const ssm_selective_dims& d, const SelectiveArgs& a,

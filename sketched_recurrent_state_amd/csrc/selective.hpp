@@ -17,7 +17,7 @@
 //   h <- exp(A sum delta) h + local,
 // which costs a few exps a group. Likewise backwards, where the gradient that leaves a group at its start
 // is sum_t P_t C_t dy_t with P_t the product of the decays up to t: taken in the same forward
-// walk.
+// walk, which also keeps the states that the walk back starts from (selective_grads.hip).
 #pragma once
 
 #include "layer.hpp"
@@ -50,30 +50,28 @@ struct SelShape {
 // Sum over the S lanes of a channel.
 template <int S>
 __device__ __forceinline__ float state_sum(float x) {
-  if constexpr (S >= 2) x += dpp<DPP_QUAD_1032>(x);
-  if constexpr (S >= 4) x += dpp<DPP_QUAD_2301>(x);
+  x += dpp<DPP_QUAD_1032>(x);
+  x += dpp<DPP_QUAD_2301>(x);
   if constexpr (S >= 8) x += dpp<DPP_HALF_MIRROR>(x);
   if constexpr (S >= 16) x += dpp<DPP_ROR8>(x);
   return x;
 }
-// Sum over the lanes of a wave that share lane % S.
-template <int S>
-__device__ __forceinline__ float channel_sum(float x) {
-  if constexpr (S <= 4) x += dpp<DPP_ROR4>(x);
-  if constexpr (S <= 8) x += dpp<DPP_ROR8>(x);
+// Sum over a block's tokens of what a lane has read: the lanes with the same quarter.
+__device__ __forceinline__ float token_sum(float x) {
+  x += dpp<DPP_ROR4>(x);
+  x += dpp<DPP_ROR8>(x);
   return xsum32(xsum16(x));
 }
 
 // The wave's tile of channels, and the lane's place in it.
 struct SelTile {
-  int tile, c0, group;   // first channel, and the group of B and C
+  int c0, group;         // first channel, and the group of B and C
   int lane, t, q;        // reading: token t of a block, quarter q
   int ch, sg;            // computing: channel ch of the tile, states sg * NS ..
 };
 template <int S>
 __device__ __forceinline__ SelTile sel_tile(const SelectiveArgs& a, int tile) {
   SelTile w;
-  w.tile = tile;
   w.c0 = tile * (64 / S);
   w.group = w.c0 / (a.channels / a.groups);
   w.lane = threadIdx.x & 63;
@@ -193,25 +191,39 @@ struct SelBlock {
   using SH = SelShape<S, NS>;
   Packed<T, SH::EC> x, dt, z, dy;
   Packed<T, SH::EN> b, c;
-  __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0) {
+  // what the state is made of
+  __device__ __forceinline__ void load_state(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0) {
     const int tok0 = cell.first + cell.pos + t0;
     const int left = cell.count - t0, row = min(w.t, left - 1);
     const int c0 = w.c0 + w.q * SH::EC, n0 = w.group * SH::N + w.q * SH::EN;
     x.load(row_at<T>(a.x, tok0, row, c0));
     dt.load(row_at<T>(a.dt, tok0, row, c0));
     b.load(row_at<T>(a.B, tok0, row, n0));
-    if constexpr (Z) z.load(row_at<T>(a.z, tok0, row, c0));  // x where there is no gate
-    if constexpr (C) c.load(row_at<T>(a.C, tok0, row, n0));
-    if constexpr (DY) dy.load(row_at<T>(a.dout, tok0, row, c0));
     if (left < TB) {
       const uint32_t mask = w.t < left ? 0xFFFFFFFFu : 0u;
       mask_out(x, mask);
       mask_out(dt, mask);
       mask_out(b, mask);
+    }
+  }
+  // and the rest
+  __device__ __forceinline__ void load_more(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0) {
+    const int tok0 = cell.first + cell.pos + t0;
+    const int left = cell.count - t0, row = min(w.t, left - 1);
+    const int c0 = w.c0 + w.q * SH::EC, n0 = w.group * SH::N + w.q * SH::EN;
+    if constexpr (Z) z.load(row_at<T>(a.z, tok0, row, c0));  // x where there is no gate
+    if constexpr (C) c.load(row_at<T>(a.C, tok0, row, n0));
+    if constexpr (DY) dy.load(row_at<T>(a.dout, tok0, row, c0));
+    if (left < TB) {
+      const uint32_t mask = w.t < left ? 0xFFFFFFFFu : 0u;
       if constexpr (Z) mask_out(z, mask);
       if constexpr (C) mask_out(c, mask);
       if constexpr (DY) mask_out(dy, mask);
     }
+  }
+  __device__ __forceinline__ void load(const SelectiveArgs& a, const SelTile& w, const SelCell& cell, int t0) {
+    load_state(a, w, cell, t0);
+    load_more(a, w, cell, t0);
   }
 };
 
@@ -286,11 +298,10 @@ struct SelGroups {
 };
 SelGroups selective_groups(const ssm_selective_dims& d, int cap);
 
-// The local pass; sets a's groups.
-hipError_t launch_selective_local(const ssm_selective_dims& d, SelectiveArgs& a, bool backward,
-                                  hipStream_t stream);
-// The states before every HB tokens, for the backward pass.
-hipError_t launch_selective_states(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream);
+inline int selective_tiles(const ssm_selective_dims& d) {  // of selective_dispatch's mapping
+  const int S = d.d_state <= 16 ? 4 : d.d_state / 4;
+  return d.channels * S / 64;
+}
 
 // Calls f(S, NS, type) for d.d_state: S lanes a channel, NS states a lane.
 template <typename F>
@@ -308,9 +319,14 @@ hipError_t selective_dispatch(const ssm_selective_dims& d, F&& f) {
   return hipErrorInvalidValue;
 }
 
-inline int selective_tiles(const ssm_selective_dims& d) {  // of selective_dispatch's mapping
-  const int S = d.d_state <= 16 ? 4 : d.d_state / 4;
-  return d.channels * S / 64;
+// Launches a pass over the groups: f(S, NS, type, grid).
+template <typename F>
+hipError_t over_groups(const ssm_selective_dims& d, const SelectiveArgs& a, F&& f) {
+  const unsigned tile_blocks = (unsigned)(selective_tiles(d) + WAVES - 1) / WAVES;
+  return selective_dispatch(d, [&](auto S, auto NS, auto T) {
+    f(S, NS, T, dim3(tile_blocks * (unsigned)a.time_groups));
+    return hipGetLastError();
+  });
 }
 
 }  // namespace ssm

@@ -5,14 +5,15 @@
 //   dC = sum_channels dy h,  dB = sum_channels G delta x,
 //   e = sum_n G B,  dx = delta e + D dy,  ddelta = x e + sum_n G a h_{t-1} A,
 //   dA = sum_t delta G a h_{t-1},  dstate_in = a_0 G_0.
-// The states are computed again, from those that a forward pass left before every 8 tokens. A wave's
-// sums over channels are stored for each token and added up afterwards in a fixed order; those over tokens
-// stay in registers.
+// The first pass keeps the state before every 8 tokens as it is from the group's zero, so it need not know the groups
+// before; the walk back adds to each exp(A sum delta) h of the group's start (4 exps a lane for 8 tokens, where a pass of its
+// own for the true states took 79 us), and computes the states between from it. A wave's sums over channels are stored for each
+// token and added up afterwards in a fixed order; those over tokens stay in registers.
 //
-// Bound by the vector ALU: 2 x 2048 tokens, 5120 channels x 16 states, bf16, 302 us of 485 in all, 20 instructions a state
+// Bound by the vector ALU: 2 x 2048 tokens, 5120 channels x 16 states, bf16, 303 us of 450 in all, 20 instructions a state
 // and token in the walk (4 to compute a state again, 10 for its gradients, 2 for the sums over a channel's lanes, 4 for
-// those over channels) and 4 around it; the vector ALU is busy nine tenths of the time at the clock it keeps.
-// Eight lanes a channel with two states each (168 registers without the parts) took 530 us.
+// those over channels) and 4 around it; the vector ALU is busy nine tenths of the time at the clock it keeps. The first pass
+// 132 us, the sums over channels 34. Eight lanes a channel with two states each (168 registers without the parts) took 530 us.
 #include "selective.hpp"
 
 namespace ssm {
@@ -22,14 +23,149 @@ namespace {
 template <typename T, int S, int NS>
 using GradBlock = SelBlock<T, S, NS, true, true, true>;
 
-// The states before a block's two parts (of the later one, if it holds a token).
+// The first pass over a group: of every sequence the state before each HB tokens but its first, from zero (or the
+// sequence's start), with the sum of delta since the group's start where the sequence began before it; the state
+// that the last sequence leaves, if it goes on behind the group; the gradient that the first sequence leaves
+// at the group's start, if it began before.
+template <int S, int NS, typename T>
+__global__ void __launch_bounds__(64 * WAVES) selective_states_kernel(const SelectiveArgs a) {
+  using SH = SelShape<S, NS>;
+  using Block = SelBlock<T, S, NS, true, true, true>;
+  constexpr int N = SH::N, CH = SH::CH, EC = SH::EC, EN = SH::EN;
+  __shared__ __align__(16) float4 sv[WAVES][TB][CH + 1];  // delta, delta x, dL/dy
+  __shared__ __align__(16) float sb[WAVES][TB][N], sc[WAVES][TB][N];
+  __shared__ __align__(16) float sbias[WAVES][CH];
+  const int wave = scalar(threadIdx.x >> 6), tiles = a.channels / CH;
+  const int tile_blocks = (tiles + WAVES - 1) / WAVES;
+  const int tile = blockIdx.x % tile_blocks * WAVES + wave;
+  if (tile >= tiles) return;
+  const SelTile w = sel_tile<S>(a, tile);
+  const SelGroup grp = sel_group(a, blockIdx.x / tile_blocks);
+  SelCell c, ahead;
+  if (!next_cell(a, grp.e0, grp.e1, c)) return;
+  const int began = c.starts() ? -1 : c.seq;  // the sequence that began before the group
+  const int my = w.c0 + w.ch, n0 = w.sg * NS;
+  const size_t at = ((size_t)grp.g * a.channels + my) * N + n0;
+  float A[NS], h[NS], g[NS], p[NS], sum = 0.f;
+  Vec<float, NS>::load(a.A + (size_t)my * N + n0, A);
+  zero(h);
+  zero(g);
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    A[i] *= kLog2e;
+    p[i] = 1.f;
+  }
+  stage_channels(sbias[wave], a.dt_bias, w);
+  wave_lds_sync();
+  Block next{};
+  const auto fetch = [&](const SelCell& c, int t0) {
+    next.load_state(a, w, c, t0);
+    if (c.seq == began) next.load_more(a, w, c, t0);
+  };
+  fetch(c, 0);
+  for (bool more = true; more; c = ahead) {
+    more = next_cell(a, c.entry + 1, grp.e1, ahead);
+    const bool leaves = c.seq == began;
+    if (c.starts()) {
+      zero(h);
+      sum = 0.f;
+      if (a.state_in)
+        Vec<float, NS>::load(a.state_in + (size_t)c.slot * a.channels * N + (uint32_t)(my * N + n0), h);
+    }
+    for (int t0 = 0; t0 < c.count; t0 += TB) {
+      const Block now = next;
+      const bool on = t0 + w.t < c.count;
+      if (t0 + TB < c.count) fetch(c, t0 + TB);
+      else if (more) fetch(ahead, 0);
+      const auto keep_state = [&](int t) {
+        const size_t part = (size_t)(c.first / HB + (c.pos + t0 + t) / HB - 1) * a.channels;
+        Vec<float, NS>::store(a.w.states + part * N + (uint32_t)(my * N + n0), h);
+        if (leaves && w.sg == 0) a.w.until[part + my] = sum;
+      };
+      float x[EC], dt[EC], delta[EC], bias[EC], b[EN], dy[EC];
+      now.x.unpack(x);
+      now.dt.unpack(dt);
+      now.b.unpack(b);
+      zero(dy);
+      if (leaves) {
+        float z[EC], cc[EN];
+        now.z.unpack(z);
+        now.dy.unpack(dy);
+        now.c.unpack(cc);
+        apply_gate(a, z, dy);
+        Vec<float, EN>::store(&sc[wave][w.t][w.q * EN], cc);
+      }
+      Vec<float, EC>::load(&sbias[wave][w.q * EC], bias);
+#pragma unroll
+      for (int i = 0; i < EC; ++i) dt[i] += bias[i];
+      steps(a, dt, t0 + TB <= c.count, on, delta);
+#pragma unroll
+      for (int i = 0; i < EC; ++i)
+        sv[wave][w.t][w.q * EC + i] = make_float4(delta[i], delta[i] * x[i], dy[i], 0.f);
+      Vec<float, EN>::store(&sb[wave][w.t][w.q * EN], b);
+      wave_lds_sync();
+      if (c.pos + t0 > 0) keep_state(0);
+      const auto tokens = [&](auto with) {
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          if (t == HB && t0 + HB < c.count) keep_state(HB);
+          const float4 v = sv[wave][t][w.ch];
+          float bb[NS], ct[NS];
+          Vec<float, NS>::load(&sb[wave][t][n0], bb);
+          if constexpr (with) Vec<float, NS>::load(&sc[wave][t][n0], ct);
+          sum += v.x;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            const float decay = __builtin_amdgcn_exp2f(v.x * A[i]);
+            h[i] = fmaf(decay, h[i], v.y * bb[i]);
+            if constexpr (with) {
+              p[i] *= decay;
+              g[i] = fmaf(p[i], ct[i] * v.z, g[i]);
+            }
+          }
+          // keeps the additions here: moved behind the block, their operands took 155 registers instead of 103
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            asm volatile("" : "+v"(h[i]));
+            if constexpr (with) asm volatile("" : "+v"(g[i]));
+          }
+        }
+      };
+      if (leaves) tokens(std::true_type{});
+      else tokens(std::false_type{});
+      wave_lds_sync();
+    }
+    if (leaves && !(more && ahead.seq == began)) {
+      if (c.ends() && a.dstate) {
+        float l[NS];
+        Vec<float, NS>::load(a.dstate + ((size_t)c.slot * a.channels + my) * N + n0, l);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) g[i] = fmaf(p[i], l[i], g[i]);
+      }
+      Vec<float, NS>::store(a.w.back + at, g);
+    }
+    if (!more && !c.ends()) {
+      Vec<float, NS>::store(a.w.local + at, h);
+      if (w.sg == 0) a.w.sums[(size_t)grp.g * a.channels + my] = sum;
+    }
+  }
+}
+
+// What was kept of the states before a block's two parts (of the later one, if it holds a token), and the sums of
+// delta until there where the sequence began before the group.
 template <int N, int NS>
 __device__ __forceinline__ void part_states(const SelectiveArgs& a, const SelCell& cell, int t0, int my, int n0,
-                                            float (&h)[TB / HB][NS]) {
+                                            bool began, float (&h)[TB / HB][NS], float (&until)[TB / HB]) {
   static_assert(TB / HB == 2, "two parts");
   const uint32_t at = (uint32_t)(my * N + n0);
-  const size_t step = (size_t)a.channels * N;
-  const float* kept = a.w.states + (size_t)(cell.first / HB + (cell.pos + t0) / HB) * step;
+  const size_t step = (size_t)a.channels * N, part = (size_t)(cell.first / HB + (cell.pos + t0) / HB);
+  const float* kept = a.w.states + part * step;
+  until[0] = until[1] = 0.f;
+  if (began) {
+    const float* u = a.w.until + part * a.channels + my;
+    until[0] = *(u - a.channels);
+    if (t0 + HB < cell.count) until[1] = *u;
+  }
   zero(h[0]);
   zero(h[1]);
   if (t0 + HB < cell.count) Vec<float, NS>::load(kept + at, h[1]);
@@ -111,7 +247,16 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
   const uint32_t dbc_pitch = (uint32_t)tiles * (8 * N);  // bytes from token to token: tiles < 2^18
   char* const dbc_tile = reinterpret_cast<char*>(a.w.dbc) + (uint32_t)tile * (8 * N);
   char* const dbc_none = dbc_tile + (uint64_t)(uint32_t)a.plan.total * dbc_pitch;
+  // the state that the group's first sequence had before the group
+  __shared__ __align__(16) float sh[WAVES][64][NS];
   SelCell cell, ahead;
+  int began = -1;
+  if (next_cell(a, grp.e0, grp.e1, cell) && !cell.starts()) {
+    float h[NS];
+    carry_in<N>(a, grp, cell, my, n0, A2, h);
+    Vec<float, NS>::store(sh[wave][w.lane], h);
+    began = cell.seq;
+  }
   bool more = prev_cell(a, grp.e1 - 1, grp.e0 - 1, cell);
   float g[NS];
   zero(g);
@@ -129,8 +274,8 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
     }
     for (int t0 = (cell.count - 1) / TB * TB; t0 >= 0; t0 -= TB) {
       const GradBlock<T, S, NS> now = next;
-      float h[TB / HB][NS];
-      part_states<N>(a, cell, t0, my, n0, h);
+      float h[TB / HB][NS], until[TB / HB];
+      part_states<N>(a, cell, t0, my, n0, cell.seq == began, h, until);
       if (t0 > 0) next.load(a, w, cell, t0 - TB);
       else if (more) next.load(a, w, ahead, (ahead.count - 1) / TB * TB);
       const bool on = t0 + w.t < cell.count;
@@ -173,6 +318,13 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
         float hs[HB + 1][NS], d[HB][NS];  // states before each token and after the last, decays
 #pragma unroll
         for (int i = 0; i < NS; ++i) hs[0][i] = h[part][i];
+        if (cell.seq == began) {
+          float h0[NS];
+          Vec<float, NS>::load(sh[wave][w.lane], h0);
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+            hs[0][i] = fmaf(__builtin_amdgcn_exp2f(A2[i] * until[part]), h0[i], hs[0][i]);
+        }
 #pragma unroll
         for (int t = 0; t < HB; ++t) {
           const float2 v = *reinterpret_cast<const float2*>(&sv[wave][part * HB + t][w.ch]);
@@ -264,8 +416,8 @@ __global__ void __launch_bounds__(64 * WAVES, 3) selective_grads_kernel(const Se
   Vec<float, NS>::store(sums + (size_t)my * N + n0, dA);
 #pragma unroll
   for (int i = 0; i < EC; ++i) {
-    dD[i] = channel_sum<4>(dD[i]);  // over the 16 tokens of a block: lanes with the same quarter
-    dbias[i] = channel_sum<4>(dbias[i]);
+    dD[i] = token_sum(dD[i]);  // over the 16 tokens of a block: lanes with the same quarter
+    dbias[i] = token_sum(dbias[i]);
   }
   if (w.t == 0) {
     float* p = sums + (size_t)a.channels * N + w.c0 + w.q * EC;
@@ -312,17 +464,21 @@ selective_sum_groups_kernel(const SelectiveArgs a, int N) {
 }  // namespace
 
 hipError_t launch_selective_backward(const ssm_selective_dims& d, SelectiveArgs& a, hipStream_t stream) {
-  hipError_t e = launch_selective_local(d, a, true, stream);
-  if (e == hipSuccess) e = launch_selective_states(d, a, stream);
+  const SelGroups g = selective_groups(d, a.plan.cap);
+  a.time_groups = g.groups;
+  a.group_chunks = g.chunks;
+  hipError_t e = over_groups(d, a, [&](auto S, auto NS, auto T, dim3 grid) {
+    constexpr int s = decltype(S)::value, ns = decltype(NS)::value;
+    using TI = typename decltype(T)::type;
+    hipLaunchKernelGGL((selective_states_kernel<s, ns, TI>), grid, dim3(64 * WAVES), 0, stream, a);
+    hipLaunchKernelGGL((selective_grads_kernel<s, ns, TI>), grid, dim3(64 * WAVES), 0, stream, a);
+  });
   if (e != hipSuccess) return e;
   return selective_dispatch(d, [&](auto S, auto NS, auto T) {
     constexpr int s = decltype(S)::value, ns = decltype(NS)::value;
     using TI = typename decltype(T)::type;
-    const int tiles = d.channels * s / 64, tb = (tiles + WAVES - 1) / WAVES;
-    hipLaunchKernelGGL((selective_grads_kernel<s, ns, TI>), dim3((unsigned)tb * (unsigned)a.time_groups),
-                       dim3(64 * WAVES), 0, stream, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    const int tiles = selective_tiles(d);
+    hipError_t e = hipSuccess;
     const long long sums = (long long)a.plan.total * a.groups * 2 * s * ns;
     if (sums > 0) {
       hipLaunchKernelGGL((selective_sum_tiles_kernel<s * ns, TI>), dim3((unsigned)((sums + 255) / 256)),
