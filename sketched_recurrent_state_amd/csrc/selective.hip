@@ -237,10 +237,10 @@ __global__ void __launch_bounds__(256) selective_step_kernel(const SelectiveArgs
 
 }  // namespace
 
-// Ten waves a SIMD of the whole GPU in all (5 of the forward pass's and 3 of the gradients' are resident at
+// Ten waves a SIMD of the whole GPU in all (6 of the forward pass's and 3 of the gradients' are resident at
 // a time): with fewer, longer groups the last ones leave SIMDs without work. A prompt of 8192 tokens
-// x 5120 channels, by chunks of a group: 3: 342 us, 4: 330, 6: 352, 8: 349, 11: 391, 16: 448;
-// the gradients of 2 x 2048 tokens: 2: 487 us, 4: 491, 6: 579, 8: 582, 11: 617. Joining the groups before costs a
+// x 5120 channels, by chunks of a group: 3: 342 us, 4: 330, 6: 352, 8: 349, 11: 391, 16: 448; the first pass and the
+// walk back of the gradients of 2 x 2048 tokens: 1: 437 us, 3: 439, 5: 465, 9: 532, 17: 632. Joining the groups before costs a
 // group about a fiftieth of a chunk each, so long prompts of few channels get longer groups.
 constexpr int kWaves = 10240;
 SelGroups selective_groups(const ssm_selective_dims& d, int cap) {
