@@ -595,9 +595,9 @@ ssm_status ssm_selective_sizes(const ssm_selective_dims* d, int32_t total_tokens
                                int64_t* forward_bytes, int64_t* backward_bytes);
 
 /*
- * A packed batch; plan, slots and states as in ssm_conv_forward, but the final states are always
- * written. The workspace holds nothing between calls; calls that may run at the same time need one
- * each. Outputs: state, out, workspace.
+ * A packed batch; plan, slots and states as in ssm_conv_forward (state_in may be state itself), but the
+ * final states are always written. The workspace holds nothing between calls; calls that may run at the
+ * same time need one each. Outputs: state, out, workspace.
  */
 ssm_status ssm_selective_forward(const ssm_selective_dims* d, int32_t total_tokens,
                                  const int32_t* plan, int32_t num_slots, const int32_t* slot,

@@ -49,6 +49,11 @@ struct ScanPlan {
   }
 };
 
+// Whether a sequence of len > 0 tokens whose first chunk is entry c goes on behind its group, the entries before e1.
+__host__ __device__ __forceinline__ bool goes_on(int c, int len, int e1, int cap) {
+  return e1 < cap && c + (len - 1) / CT >= e1;
+}
+
 inline int scan_capacity(int total, int seqs) { return total / CT + seqs; }
 
 }  // namespace ssm

@@ -49,7 +49,10 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
     const size_t at = (size_t)c.slot * a.channels * N + (uint32_t)(my * N + n0);
     if (c.starts()) {
       zero(h);
-      if (a.state_in) Vec<float, NS>::load(a.state_in + at, h);
+      // in place, the group where the sequence ends may have written its state by now
+      const bool copied = a.state == a.state_in && goes_on(c.entry, c.len, grp.e1, a.plan.cap);
+      const float* from = copied ? a.w.start + (size_t)grp.g * a.channels * N : a.state_in + (size_t)c.slot * a.channels * N;
+      if (a.state_in) Vec<float, NS>::load(from + (uint32_t)(my * N + n0), h);
     }
     for (int t0 = 0; t0 < c.count; t0 += TB) {
       const Block now = next;
@@ -104,7 +107,9 @@ __global__ void __launch_bounds__(64 * WAVES) selective_scan_kernel(const Select
   }
 }
 
-// The local pass: the state that the group's last sequence leaves, if it goes on behind the group.
+// The local pass: the state that the group's last sequence leaves, if it goes on behind the group. Where states are
+// continued in place it also copies the one that such a sequence begins with: the main pass reads it in this group
+// and writes the final state in a later one, in no order.
 template <int S, int NS, typename T>
 __global__ void __launch_bounds__(64 * WAVES) selective_local_kernel(const SelectiveArgs a) {
   using SH = SelShape<S, NS>;
@@ -130,8 +135,11 @@ __global__ void __launch_bounds__(64 * WAVES) selective_local_kernel(const Selec
   stage_channels(sbias[wave], a.dt_bias, w);
   wave_lds_sync();
   zero(h);
-  if (c.starts() && a.state_in)
+  if (c.starts() && a.state_in) {
     Vec<float, NS>::load(a.state_in + (size_t)c.slot * a.channels * N + (uint32_t)(my * N + n0), h);
+    if (a.state == a.state_in)
+      Vec<float, NS>::store(a.w.start + ((size_t)grp.g * a.channels + my) * N + n0, h);
+  }
   Block next;
   next.load(a, w, c, 0);
   SelCell ahead;
@@ -267,6 +275,7 @@ SelectiveWork selective_work(const ssm_selective_dims& d, int total, bool backwa
     w.local = take(g.groups * states);
     w.sums = take((size_t)g.groups * d.channels);
   }
+  if (g.groups > 1 && !backward) w.start = take(g.groups * states);
   if (backward) {
     w.back = take(g.groups * states);
     w.states = take(((size_t)total / HB + 1) * states);
