@@ -28,7 +28,7 @@ import torch
 
 from . import (ConvDims, Dims, IN_BF16, IN_F32, KDA, MAMBA2, NormDims, SKETCH_BF16, SelectiveDims,
                buffer_append, conv_forward, conv_step, full_read_decode_step, gated_norm,
-               rank_offsets, recurrent_decode_step, scan_forward, scan_plan,
+               rank_offsets, recurrent_decode_step, scan_forward, scan_plan, scan_sizes,
                selective_forward, selective_step, sketch_decode_step, sketch_decode_step_ls,
                sketch_decode_step_ranked, window_update_refresh, window_update_refresh_ls,
                window_update_refresh_ranked, _addr, _row_addr)
@@ -118,15 +118,28 @@ class GatedNorm:
     def __init__(self, dims: NormDims, weight: torch.Tensor, bias: Optional[torch.Tensor] = None):
         self.d, self.weight, self.bias = dims, weight, bias
 
-    def check(self, rows: int, gate: Optional[torch.Tensor]) -> None:
+    def check(self, rows: int, gate: Optional[torch.Tensor], device: Optional[int] = None) -> list:
         """Raises where the norm would: a gate for `rows` rows that is missing, not wanted or not such rows,
-        weights that are not the dimensions'."""
+        weights that are not the dimensions', any of them on another device than `device` (a number, or None). Returns
+        the places of the gate and the weights (first byte, and the one behind the last)."""
         if (gate is None) != (self.d.gate == 0):
             raise ValueError("gate: " + ("the norm needs one" if gate is None else "the norm has none"))
-        wide = self.d.groups * self.d.width
-        _row_addr(gate, "gate", (_in_type(self.d.in_dtype),), rows, wide)
-        for w, name in ((self.weight, "weight"), (self.bias, "bias")):
-            _addr(w, name, (torch.float32,), self.d.width if self.d.shared else wide)
+        d = self.d
+        wide, own, places = d.groups * d.width, d.width if d.shared else d.groups * d.width, []
+        if gate is not None:
+            tin = _in_type(d.in_dtype)
+            at, stride = _row_addr(gate, "gate", (tin,), rows, wide)
+            if stride < wide or stride % 8 or stride >= 1 << 26:
+                raise ValueError(f"gate: a stride of {stride}, not a multiple of 8 in [{wide}, 2^26)")
+            if at % 16:
+                raise ValueError("gate: not 16-byte aligned")
+            if device is not None and not isinstance(gate, int) and gate.get_device() != device:
+                raise ValueError(f"gate: on device {gate.get_device()}, the state is on {device}")
+            places.append((at, at + (max(rows - 1, 0) * stride + wide) * tin.itemsize))
+        places.append(_place(self.weight, "weight", own, 16, device))
+        if self.bias is not None:
+            places.append(_place(self.bias, "bias", own, 16, device))
+        return places
 
     def __call__(self, x: torch.Tensor, gate: Optional[torch.Tensor] = None) -> torch.Tensor:
         """x [rows][groups][width], gate rows of as many channels: a new tensor of x's shape."""
@@ -146,29 +159,68 @@ def _around(d: Dims, conv: Optional[ShortConv], norm: Optional[GatedNorm]) -> No
             raise ValueError(f"{norm.d} does not take the outputs of {d}")
 
 
-def _check_around(d: Dims, rows: int, conv, norm, decay, beta, gate, *ys) -> None:
-    """What the recurrence or the norm would refuse is refused before the convolution or the recurrence has
-    written its state: a call either does all of its work or none."""
-    if norm is not None:
-        norm.check(rows, gate)
-    elif gate is not None:
-        raise ValueError("gate: the decoder has no norm")
-    if conv is None:
-        return
-    if decay is None or (beta is None) != (d.rule == MAMBA2):
-        raise ValueError("decay and beta: every rule needs decay, all but Mamba-2 beta")
-    units, f32 = rows * d.heads, (torch.float32,)
-    _addr(decay, "decay", f32, units * d.d_k if d.rule == KDA else units)
-    _addr(beta, "beta", f32, units)
+_F32 = (torch.float32,)
+
+
+def _place(x, name: str, count: int, align: int, device: Optional[int]) -> tuple:
+    """First byte of a contiguous fp32 argument of `count` elements and the byte behind its last ((0, 0) for None); raises
+    where the library would refuse it, or where it is on another device."""
+    at = _addr(x, name, _F32, count)
+    if at is None:
+        return 0, 0
+    if at % align:
+        raise ValueError(f"{name}: not {align}-byte aligned")
+    if device is not None and not isinstance(x, int) and x.get_device() != device:
+        raise ValueError(f"{name}: on device {x.get_device()}, the state is on {device}")
+    return at, at + 4 * count
+
+
+def _whole(x: torch.Tensor) -> tuple:
+    at = x.data_ptr()
+    return at, at + x.numel() * x.element_size()
+
+
+def _check_around(d: Dims, rows: int, conv, norm, decay, beta, gate, state, *, align=(16, 16), written=(),
+                  kept=(), ys=()) -> None:
+    """What the recurrence or the norm would refuse of a call's arguments is refused before the convolution or
+    the recurrence has written its state: a call that raises for its arguments has done none of its work.
+    align: of decay's and beta's addresses; written: what the recurrence writes besides the state; kept: what else
+    of the decoder's the caller's outputs ys must not lie over."""
+    if norm is None:
+        if gate is not None:
+            raise ValueError("gate: the decoder has no norm")
+        if conv is None:
+            return
+    device, units = state.get_device(), rows * d.heads
+    read = [] if norm is None else norm.check(rows, gate, device)
+    own = [_whole(state)]
+    if conv is not None:
+        if decay is None or (beta is None) != (d.rule == MAMBA2):
+            raise ValueError("decay and beta: every rule needs decay, all but Mamba-2 beta")
+        read.append(_place(decay, "decay", units * d.d_k if d.rule == KDA else units, align[0], device))
+        if beta is not None:
+            read.append(_place(beta, "beta", units, align[1], device))
+        own.append(_whole(conv.state))
+    own += written
+    for lo, hi in own:
+        for at, end in read:
+            if at < hi and lo < end:
+                raise ValueError("an array that the call reads overlaps one that it writes")
     for y in ys:
-        _addr(y, "y", f32, units * d.d_v)
+        if y is None:
+            continue
+        y = _place(y, "y", units * d.d_v, 16, device)
+        for at, end in read + own + [_whole(t) for t in kept if t is not None]:
+            if at < y[1] and y[0] < end:
+                raise ValueError("y overlaps an array that the call reads or that the decoder keeps")
+        read.append(y)
 
 
-def _heads(d: Dims, parts):
-    """Convolved parts as queries, keys and values by head."""
-    q, k, v = parts
-    rows = q.shape[0]
-    return q.view(rows, d.heads, d.d_k), k.view(rows, d.heads, d.d_k), v.view(rows, d.heads, d.d_v)
+def _prefill_check(d: Dims, rows: int, conv, norm, decay, beta, gate, state) -> None:
+    """_check_around for a packed batch, which asks less of its gates' addresses."""
+    if conv is not None:
+        scan_sizes(d, rows)  # more tokens than the recurrence takes
+    _check_around(d, rows, conv, norm, decay, beta, gate, state, align=(16 if d.rule == KDA else 4, 4))
 
 
 def _prefill(d: Dims, state: torch.Tensor, lengths, q, k, v, decay, beta, conv=None, norm=None,
@@ -178,7 +230,7 @@ def _prefill(d: Dims, state: torch.Tensor, lengths, q, k, v, decay, beta, conv=N
     total, make = q.shape[0], _new_rows(lengths)
     plan = _plan(lengths, total, state.device)
     if conv is not None:
-        q, k, v = _heads(d, conv._prefill(plan, torch.empty, (q, k, v)))
+        q, k, v = conv._prefill(plan, torch.empty, (q, k, v))
     y = make((total, d.heads, d.d_v), device=state.device, dtype=torch.float32)
     scan_forward(d, total, plan, q, k, v, decay, beta, state, y, state_in=state)
     if norm is not None:
@@ -247,6 +299,7 @@ class WindowedDecoder:
         self.decay_buf = torch.zeros(dshape, device=dev, dtype=torch.float32)
         self.beta_buf = (torch.zeros((N, H, W), device=dev, dtype=torch.float32)
                          if dims.rule != MAMBA2 else None)
+        self._buf_places = [_whole(t) for t in (self.k_buf, self.v_buf, self.decay_buf, self.beta_buf) if t is not None]
         self.tau = 0  # tokens already in the window buffer
 
     # -- library calls, uniform or per-head ranks --------------------------------
@@ -293,7 +346,7 @@ class WindowedDecoder:
         the device are not read back: prompts are cut where the token arrays end, and outputs
         behind the last prompt are zero."""
         lengths = _checked_lengths(self.d, lengths, q)
-        _check_around(self.d, q.shape[0], self.conv, self.norm, decay, beta, gate)
+        _prefill_check(self.d, q.shape[0], self.conv, self.norm, decay, beta, gate, self.state)
         with torch.cuda.device_of(self.state):  # the flush and the refresh on the scan's stream
             if self.tau:
                 self.flush()
@@ -307,9 +360,11 @@ class WindowedDecoder:
         norm what the norm makes of it."""
         d = self.d
         tau = self.tau + 1
-        _check_around(d, d.batch, self.conv, self.norm, decay, beta, gate, y, y_full)
+        bufs = (self.k_buf, self.v_buf, self.decay_buf, self.beta_buf)
+        _check_around(d, d.batch, self.conv, self.norm, decay, beta, gate, self.state, written=self._buf_places,
+                      kept=(self.sketch, self.basis, self.read_map), ys=(y, y_full))
         if self.conv is not None:
-            q, k, v = _heads(d, self.conv.step(q, k, v))
+            q, k, v = self.conv.step(q, k, v)
         N, H, dv = d.batch, d.heads, d.d_v
         if y is None and self.read != "full":
             y = torch.empty((N, H, dv), device=q.device, dtype=torch.float32)
@@ -320,7 +375,6 @@ class WindowedDecoder:
             buffer_append(d, k, v, decay, beta, self.k_buf, self.v_buf, self.decay_buf,
                           self.beta_buf, tau - 1)
             tok = {}
-        bufs = (self.k_buf, self.v_buf, self.decay_buf, self.beta_buf)
         if self.read != "full":
             self._sketch_read(q, tau, y, tok)
             tok = {}  # the token is in the buffer now
@@ -348,9 +402,9 @@ class RecurrentDecoder:
 
     def step(self, q, k, v, decay, beta=None, *, gate=None, y=None):
         d = self.d
-        _check_around(d, d.batch, self.conv, self.norm, decay, beta, gate, y)
+        _check_around(d, d.batch, self.conv, self.norm, decay, beta, gate, self.state, ys=(y,))
         if self.conv is not None:
-            q, k, v = _heads(d, self.conv.step(q, k, v))
+            q, k, v = self.conv.step(q, k, v)
         if y is None:
             y = torch.empty((d.batch, d.heads, d.d_v), device=q.device, dtype=torch.float32)
         recurrent_decode_step(d, self.state, q, k, v, decay, beta, y)
@@ -360,7 +414,7 @@ class RecurrentDecoder:
         """Take a packed batch of prompts into the state; returns their outputs (lengths and
         outputs as in WindowedDecoder.prefill)."""
         lengths = _checked_lengths(self.d, lengths, q)
-        _check_around(self.d, q.shape[0], self.conv, self.norm, decay, beta, gate)
+        _prefill_check(self.d, q.shape[0], self.conv, self.norm, decay, beta, gate, self.state)
         with torch.cuda.device_of(self.state):
             return _prefill(self.d, self.state, lengths, q, k, v, decay, beta, self.conv, self.norm, gate)
 

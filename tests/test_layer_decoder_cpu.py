@@ -1,0 +1,80 @@
+"""The decoders' checks of a call's arguments, with stand-ins for device tensors: an array on another device than the
+state, arrays that overlap, addresses that the library cannot read."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import sketched_recurrent_state_amd as ssm  # noqa: E402
+from sketched_recurrent_state_amd import decoder  # noqa: E402
+
+
+class Stub:
+    """A contiguous device tensor's description; nothing is behind its address."""
+
+    is_cuda = True
+
+    def __init__(self, at, shape, dtype=torch.float32, device=0):
+        self.at, self.shape, self.dtype, self.device = at, torch.Size(shape), dtype, device
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return self.at
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+    def dim(self):
+        return len(self.shape)
+
+
+D = ssm.Dims.make("gdn", "bf16", 2, 2, 32, 32, 4, 4)
+NORM = ssm.NormDims.make("f32", "bf16", 2, 32, shared=True)
+MB = 1 << 20
+
+
+def call(**kw):
+    a = dict(decay=Stub(1 * MB, (2, 2)), beta=Stub(2 * MB, (2, 2)), gate=Stub(3 * MB, (2, 64), torch.bfloat16),
+             weight=Stub(4 * MB, (32,)), state=Stub(5 * MB, (2, 2, 32, 32)), y=Stub(6 * MB, (2, 2, 32)),
+             conv_state=Stub(7 * MB, (2, 3, 192), torch.bfloat16), sketch=Stub(8 * MB, (2, 2, 4, 32)))
+    a.update(kw)
+    conv = type("Conv", (), {"state": a["conv_state"]})
+    norm = decoder.GatedNorm(NORM, a["weight"])
+    decoder._check_around(D, 2, conv, norm, a["decay"], a["beta"], a["gate"], a["state"], kept=(a["sketch"],),
+                          ys=(a["y"],))
+
+
+def test_arguments_that_fit():
+    call()
+    call(y=None)
+
+
+@pytest.mark.parametrize("name,shape,dtype", [("decay", (2, 2), torch.float32), ("beta", (2, 2), torch.float32),
+                                              ("gate", (2, 64), torch.bfloat16), ("weight", (32,), torch.float32),
+                                              ("y", (2, 2, 32), torch.float32)])
+def test_one_argument(name, shape, dtype):
+    with pytest.raises(ValueError, match=f"{name}: on device 1"):
+        call(**{name: Stub(20 * MB, shape, dtype, device=1)})
+    with pytest.raises(ValueError, match=f"{name}: not 16-byte aligned"):
+        call(**{name: Stub(20 * MB + 8, shape, dtype)})
+    for at, own in ((5, "state"), (7, "conv_state")):
+        with pytest.raises(ValueError, match="overlaps"):
+            call(**{name: Stub(at * MB + 16, shape, dtype)})
+
+
+@pytest.mark.parametrize("at", [1, 2, 3, 4, 8])
+def test_the_output_over_what_the_call_reads(at):
+    with pytest.raises(ValueError, match="y overlaps"):
+        call(y=Stub(at * MB, (2, 2, 32)))
+
+
+def test_neighbours_do_not_overlap():
+    call(y=Stub(1 * MB + 16, (2, 2, 32)))
+    call(y=Stub(5 * MB - 512, (2, 2, 32)))
