@@ -94,3 +94,37 @@ def test_in_place_without_a_state():
     s.h0 = torch.zeros(41, 16, 8, device="cuda")
     out2, state2 = s.forward(in_place=True)
     assert torch.equal(out, out2) and torch.equal(state, state2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("batch", BATCHES)
+def test_gradients(batch, shape, dtype):
+    """The switch from the sequence that began before a group to later ones, kept states completed over several chunks,
+    joins forwards and backwards over such groups."""
+    s = Selective(dtype, BATCHES[batch], *shape, spare=3)
+    o = s.backward()
+    s.check_backward(o)
+    again = s.backward()
+    assert all(v is None or torch.equal(v, again[k]) for k, v in o.items())
+
+
+@pytest.mark.parametrize("without", ["gated", "soft", "carried"])
+def test_without(without):
+    s = Selective("f32", BATCHES["unlike"], 32, 16, 2, **{without: False}, pad=0)
+    out, state = s.forward()
+    s.check_forward(out, state)
+    s.check_backward(s.backward())
+    if s.h0 is not None:
+        assert all(torch.equal(a, b) for a, b in zip(s.forward(in_place=True), (out, state)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_slow_decays(dtype):
+    """Decays near 1, so that a state of the first tokens is still there groups later and joins count."""
+    s = Selective(dtype, [64, 0, 900, 31] + [300] * 8, 16, 16)
+    s.A.mul_(1e-3)
+    out, state = s.forward()
+    s.check_forward(out, state)
+    assert all(torch.equal(a, b) for a, b in zip(s.forward(in_place=True), (out, state)))
+    s.check_backward(s.backward())
