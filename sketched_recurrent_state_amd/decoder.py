@@ -142,7 +142,8 @@ class GatedNorm:
         return places
 
     def __call__(self, x: torch.Tensor, gate: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """x [rows][groups][width], gate rows of as many channels: a new tensor of x's shape."""
+        """x: rows of groups * width channels, whatever its further dimensions; gate: rows of as many: a new tensor of
+        x's shape."""
         out = torch.empty(x.shape, device=x.device, dtype=_in_type(self.d.in_dtype))
         gated_norm(self.d, x.shape[0], x, gate, self.weight, self.bias, out)
         return out
@@ -154,8 +155,8 @@ def _around(d: Dims, conv: Optional[ShortConv], norm: Optional[GatedNorm]) -> No
         want = [d.heads * d.d_k, d.heads * d.d_k, d.heads * d.d_v]
         if conv.widths != want or conv.d.batch != d.batch or conv.d.in_dtype != d.in_dtype:
             raise ValueError(f"{conv.d} does not make the queries, keys and values of {d}")
-    if norm is not None:
-        if (norm.d.groups, norm.d.width, norm.d.x_dtype) != (d.heads, d.d_v, IN_F32):
+    if norm is not None:  # groups of any channels of a row: heads, runs of heads (Mamba-2), all of them
+        if norm.d.groups * norm.d.width != d.heads * d.d_v or norm.d.x_dtype != IN_F32:
             raise ValueError(f"{norm.d} does not take the outputs of {d}")
 
 
@@ -257,7 +258,8 @@ class WindowedDecoder:
             [N, H, r, d_k] the per-unit map q~ -> c; uniform rank and fp32 sketch only)
     conv, norm: the layer's short convolution and output norm, or None. With a convolution q, k, v are the
             projections that go into it (rows of H d_k, H d_k and H d_v channels; they may be column ranges of
-            one tensor); with a norm the outputs are normalised and gated by `gate`, in its in_dtype.
+            one tensor); with a norm the outputs are normalised and gated by `gate`, in its in_dtype. The norm's groups
+            divide the H d_v channels of a token as they like: heads, runs of heads, all of them.
     The sketch is kept in dims.sketch_dtype (fp32, or bf16 rounded to nearest).
     """
 
