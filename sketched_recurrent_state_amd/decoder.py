@@ -28,8 +28,8 @@ import torch
 
 from . import (ConvDims, Dims, IN_BF16, IN_F32, KDA, MAMBA2, NormDims, SKETCH_BF16, SelectiveDims,
                buffer_append, conv_forward, conv_step, full_read_decode_step, gated_norm,
-               rank_offsets, recurrent_decode_step, scan_forward, scan_plan, scan_sizes,
-               selective_forward, selective_step, sketch_decode_step, sketch_decode_step_ls,
+               gated_norm_sizes, rank_offsets, recurrent_decode_step, scan_forward, scan_plan,
+               scan_sizes, selective_forward, selective_step, sketch_decode_step, sketch_decode_step_ls,
                sketch_decode_step_ranked, window_update_refresh, window_update_refresh_ls,
                window_update_refresh_ranked, _addr, _row_addr)
 
@@ -158,6 +158,7 @@ def _around(d: Dims, conv: Optional[ShortConv], norm: Optional[GatedNorm]) -> No
     if norm is not None:  # groups of any channels of a row: heads, runs of heads (Mamba-2), all of them
         if norm.d.groups * norm.d.width != d.heads * d.d_v or norm.d.x_dtype != IN_F32:
             raise ValueError(f"{norm.d} does not take the outputs of {d}")
+        gated_norm_sizes(norm.d, 0)  # raises for dimensions that the norm refuses: not after a state is written
 
 
 _F32 = (torch.float32,)

@@ -78,3 +78,13 @@ def test_the_output_over_what_the_call_reads(at):
 def test_neighbours_do_not_overlap():
     call(y=Stub(1 * MB + 16, (2, 2, 32)))
     call(y=Stub(5 * MB - 512, (2, 2, 32)))
+
+
+@pytest.mark.parametrize("norm", [dict(eps=0.0), dict(eps=float("nan")), dict(gate=3), dict(activation="none")])
+def test_a_norm_that_every_call_would_refuse(norm):
+    d = ssm.NormDims.make("f32", "bf16", 2, 32, **norm)
+    with pytest.raises(ssm.SSMError):
+        decoder.RecurrentDecoder(D, None, norm=decoder.GatedNorm(d, None))
+    with pytest.raises(ssm.SSMError):
+        decoder.WindowedDecoder(D, None, read="full", norm=decoder.GatedNorm(d, None))
+    decoder.RecurrentDecoder(D, None, norm=decoder.GatedNorm(NORM, None))
