@@ -218,6 +218,13 @@ def _check_around(d: Dims, rows: int, conv, norm, decay, beta, gate, state, *, a
         read.append(y)
 
 
+def _elsewhere(dec) -> bool:
+    """Whether a step of a decoder with a convolution or a norm has to change the current device: the calls of the
+    recurrence go to its stream, those of the convolution and the norm to that of their tensors' device."""
+    return ((dec.conv is not None or dec.norm is not None)
+            and dec.state.get_device() != torch.cuda.current_device())
+
+
 def _prefill_check(d: Dims, rows: int, conv, norm, decay, beta, gate, state) -> None:
     """_check_around for a packed batch, which asks less of its gates' addresses."""
     if conv is not None:
@@ -361,6 +368,9 @@ class WindowedDecoder:
     def step(self, q, k, v, decay, beta=None, *, gate=None, y=None, y_full=None):
         """Read the output for the current token; returns y (or (y, y_full) for read="both"), or with a
         norm what the norm makes of it."""
+        if _elsewhere(self):
+            with torch.cuda.device_of(self.state):
+                return self.step(q, k, v, decay, beta, gate=gate, y=y, y_full=y_full)
         d = self.d
         tau = self.tau + 1
         bufs = (self.k_buf, self.v_buf, self.decay_buf, self.beta_buf)
@@ -404,6 +414,9 @@ class RecurrentDecoder:
         self.d, self.state, self.conv, self.norm = dims, state, conv, norm
 
     def step(self, q, k, v, decay, beta=None, *, gate=None, y=None):
+        if _elsewhere(self):
+            with torch.cuda.device_of(self.state):
+                return self.step(q, k, v, decay, beta, gate=gate, y=y)
         d = self.d
         _check_around(d, d.batch, self.conv, self.norm, decay, beta, gate, self.state, ys=(y,))
         if self.conv is not None:

@@ -88,3 +88,43 @@ def test_a_norm_that_every_call_would_refuse(norm):
     with pytest.raises(ssm.SSMError):
         decoder.WindowedDecoder(D, None, read="full", norm=decoder.GatedNorm(d, None))
     decoder.RecurrentDecoder(D, None, norm=decoder.GatedNorm(NORM, None))
+
+
+@pytest.mark.parametrize("which", ["recurrent", "windowed"])
+def test_steps_on_another_device_than_the_current_one(which, monkeypatch):
+    """Every call of a step is made with the state's device current, and the old one is back afterwards."""
+    now, calls = [0], []
+
+    class On:
+        def __init__(self, x):
+            self.to = x.get_device()
+
+        def __enter__(self):
+            self.back, now[0] = now[0], self.to
+
+        def __exit__(self, *_):
+            now[0] = self.back
+
+    def note(name, result=None):
+        return lambda *a, **kw: (calls.append((name, now[0])), result)[1]
+
+    monkeypatch.setattr(decoder.torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(decoder.torch.cuda, "device_of", On)
+    for name in ("recurrent_decode_step", "full_read_decode_step", "window_update_refresh"):
+        monkeypatch.setattr(decoder, name, note(name))
+    cls = decoder.RecurrentDecoder if which == "recurrent" else decoder.WindowedDecoder
+    dec = cls.__new__(cls)
+    x = torch.zeros(2, 64)
+    conv = type("Conv", (), {"state": Stub(7 * MB, (2, 3, 192), torch.bfloat16, 1), "step": note("conv", (x, x, x))})
+
+    class Norm(decoder.GatedNorm):
+        __call__ = note("norm", x)
+
+    dec.__dict__.update(d=D, conv=conv, norm=Norm(NORM, Stub(4 * MB, (32,), device=1)), read="full", fused=True, tau=3,
+                        state=Stub(5 * MB, (2, 2, 32, 32), device=1), sketch=None, basis=None, read_map=None,
+                        offsets=None, k_buf=None, v_buf=None, decay_buf=None, beta_buf=None, _buf_places=[])
+    gate = Stub(3 * MB, (2, 64), torch.bfloat16, 1)
+    assert dec.step(x, x, x, Stub(1 * MB, (2, 2), device=1), Stub(2 * MB, (2, 2), device=1), gate=gate) is x
+    want = ["conv"] + (["recurrent_decode_step"] if which == "recurrent" else
+                       ["full_read_decode_step", "window_update_refresh"]) + ["norm"]
+    assert calls == [(name, 1) for name in want] and now == [0]
