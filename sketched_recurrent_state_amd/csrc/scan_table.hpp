@@ -54,6 +54,13 @@ __host__ __device__ __forceinline__ bool goes_on(int c, int len, int e1, int cap
   return e1 < cap && c + (len - 1) / CT >= e1;
 }
 
+// The gradients of the selective recurrence keep the state before every KT tokens of a sequence but its first. The
+// place of that before token pos (a multiple of KT, not 0) of the sequence whose first token is `first`: no two
+// sequences' meet, whatever their lengths, and all are below kept_places(tokens of the batch).
+constexpr int KT = 8;
+__host__ __device__ __forceinline__ int kept_place(int first, int pos) { return first / KT + pos / KT - 1; }
+inline int kept_places(int total) { return total / KT + 1; }
+
 inline int scan_capacity(int total, int seqs) { return total / CT + seqs; }
 
 }  // namespace ssm

@@ -278,8 +278,8 @@ SelectiveWork selective_work(const ssm_selective_dims& d, int total, bool backwa
   if (g.groups > 1 && !backward) w.start = take(g.groups * states);
   if (backward) {
     w.back = take(g.groups * states);
-    w.states = take(((size_t)total / HB + 1) * states);
-    w.until = take(((size_t)total / HB + 1) * d.channels);
+    w.states = take((size_t)kept_places(total) * states);
+    w.until = take((size_t)kept_places(total) * d.channels);
     w.dbc = take(((size_t)total + 1) * selective_tiles(d) * 2 * d.d_state);
     w.partial = take((size_t)g.groups * d.channels * (d.d_state + 2));
   }

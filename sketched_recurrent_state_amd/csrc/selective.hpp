@@ -26,7 +26,7 @@
 namespace ssm {
 
 constexpr int TB = 16;     // tokens of a block
-constexpr int HB = 8;      // tokens between the states that the backward pass starts from
+constexpr int HB = KT;     // tokens between the states that the backward pass starts from
 constexpr int WAVES = 4;   // of a workgroup
 
 // log(1 + e^x) = max(x, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|x| <= 1, so small values keep their digits.

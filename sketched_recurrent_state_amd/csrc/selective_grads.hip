@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(64 * WAVES) selective_states_kernel(const Sele
       if (t0 + TB < c.count) fetch(c, t0 + TB);
       else if (more) fetch(ahead, 0);
       const auto keep_state = [&](int t) {
-        const size_t part = (size_t)(c.first / HB + (c.pos + t0 + t) / HB - 1) * a.channels;
+        const size_t part = (size_t)kept_place(c.first, c.pos + t0 + t) * a.channels;
         Vec<float, NS>::store(a.w.states + part * N + (uint32_t)(my * N + n0), h);
         if (leaves && w.sg == 0) a.w.until[part + my] = sum;
       };
@@ -158,7 +158,7 @@ __device__ __forceinline__ void part_states(const SelectiveArgs& a, const SelCel
                                             bool began, float (&h)[TB / HB][NS], float (&until)[TB / HB]) {
   static_assert(TB / HB == 2, "two parts");
   const uint32_t at = (uint32_t)(my * N + n0);
-  const size_t step = (size_t)a.channels * N, part = (size_t)(cell.first / HB + (cell.pos + t0) / HB);
+  const size_t step = (size_t)a.channels * N, part = (size_t)kept_place(cell.first, cell.pos + t0 + HB);
   const float* kept = a.w.states + part * step;
   until[0] = until[1] = 0.f;
   if (began) {
