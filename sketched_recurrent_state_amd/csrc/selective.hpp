@@ -30,7 +30,7 @@ constexpr int HB = KT;     // tokens between the states that the backward pass s
 constexpr int WAVES = 4;   // of a workgroup
 
 // log(1 + e^x) = max(x, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|x| <= 1, so small values keep their digits.
-// atanh(s) / s as a polynomial in q = s^2 <= 1/9 whose largest relative error is the least (2^-28). x = +inf
+// atanh(s) / s as a polynomial in q = s^2 <= 1/9 whose largest relative error is the least (7.8e-9, 2^-26.9). x = +inf
 // and NaN pass through.
 __device__ __forceinline__ float softplus(float x) {
   const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(x));
