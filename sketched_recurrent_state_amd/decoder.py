@@ -309,7 +309,7 @@ class WindowedDecoder:
         self.decay_buf = torch.zeros(dshape, device=dev, dtype=torch.float32)
         self.beta_buf = (torch.zeros((N, H, W), device=dev, dtype=torch.float32)
                          if dims.rule != MAMBA2 else None)
-        self._buf_places = [_whole(t) for t in (self.k_buf, self.v_buf, self.decay_buf, self.beta_buf) if t is not None]
+        self._placed = (), []  # the buffers, and where they lie
         self.tau = 0  # tokens already in the window buffer
 
     # -- library calls, uniform or per-head ranks --------------------------------
@@ -374,7 +374,10 @@ class WindowedDecoder:
         d = self.d
         tau = self.tau + 1
         bufs = (self.k_buf, self.v_buf, self.decay_buf, self.beta_buf)
-        _check_around(d, d.batch, self.conv, self.norm, decay, beta, gate, self.state, written=self._buf_places,
+        if ((self.conv is not None or self.norm is not None)
+                and (len(self._placed[0]) != 4 or not all(map(operator.is_, bufs, self._placed[0])))):
+            self._placed = bufs, [_whole(t) for t in bufs if t is not None]
+        _check_around(d, d.batch, self.conv, self.norm, decay, beta, gate, self.state, written=self._placed[1],
                       kept=(self.sketch, self.basis, self.read_map), ys=(y, y_full))
         if self.conv is not None:
             q, k, v = self.conv.step(q, k, v)

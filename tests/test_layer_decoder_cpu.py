@@ -122,9 +122,30 @@ def test_steps_on_another_device_than_the_current_one(which, monkeypatch):
 
     dec.__dict__.update(d=D, conv=conv, norm=Norm(NORM, Stub(4 * MB, (32,), device=1)), read="full", fused=True, tau=3,
                         state=Stub(5 * MB, (2, 2, 32, 32), device=1), sketch=None, basis=None, read_map=None,
-                        offsets=None, k_buf=None, v_buf=None, decay_buf=None, beta_buf=None, _buf_places=[])
+                        offsets=None, k_buf=None, v_buf=None, decay_buf=None, beta_buf=None, _placed=((), []))
     gate = Stub(3 * MB, (2, 64), torch.bfloat16, 1)
     assert dec.step(x, x, x, Stub(1 * MB, (2, 2), device=1), Stub(2 * MB, (2, 2), device=1), gate=gate) is x
     want = ["conv"] + (["recurrent_decode_step"] if which == "recurrent" else
                        ["full_read_decode_step", "window_update_refresh"]) + ["norm"]
     assert calls == [(name, 1) for name in want] and now == [0]
+
+
+def test_buffers_that_were_replaced(monkeypatch):
+    """What a step must not lie over are the window buffers of now."""
+    dec = decoder.WindowedDecoder.__new__(decoder.WindowedDecoder)
+    x = torch.zeros(2, 64)
+    conv = type("Conv", (), {"state": Stub(7 * MB, (2, 3, 192), torch.bfloat16), "step": lambda *a: (x, x, x)})
+    bufs = [Stub((30 + i) * MB, (2, 2, 4, 32)) for i in range(4)]
+    monkeypatch.setattr(decoder, "full_read_decode_step", lambda *a, **kw: None)
+    monkeypatch.setattr(decoder.torch.cuda, "current_device", lambda: 0)
+    dec.__dict__.update(d=D, conv=conv, norm=None, read="full", fused=True, tau=0, state=Stub(5 * MB, (2, 2, 32, 32)),
+                        sketch=None, basis=None, read_map=None, offsets=None, k_buf=bufs[0], v_buf=bufs[1],
+                        decay_buf=bufs[2], beta_buf=bufs[3], _placed=((), []))
+    step = lambda at: dec.step(x, x, x, Stub(at, (2, 2)), Stub(2 * MB, (2, 2)))
+    for _ in range(2):
+        with pytest.raises(ValueError, match="overlaps"):
+            step(31 * MB)
+    dec.v_buf = Stub(40 * MB, (2, 2, 4, 32))
+    step(31 * MB)
+    with pytest.raises(ValueError, match="overlaps"):
+        step(40 * MB)
