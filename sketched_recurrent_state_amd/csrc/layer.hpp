@@ -71,12 +71,13 @@ struct SelectiveWork {
   // for every group of chunks, of the sequences that go on behind it:
   float* local;    // [groups][channels][d_state]  the state it leaves, from zero (or the sequence's start)
   float* sums;     // [groups][channels]           the sum of its deltas
-  float* start;    // forward: [groups][channels][d_state]  the kept state such a sequence begins with in the group
   float* back;     // backward: [groups][channels][d_state]  the gradient that leaves it at its start
   float* states;   // backward: the state before every 8 tokens of a sequence but its first, from the group's zero
   float* until;    // backward: [those places][channels]  the sum of delta from the group's start
   float* dbc;      // [tokens + 1][tiles][2][d_state]  dB and dC of a wave's channels
   float* partial;  // [groups][channels][d_state + 2]  dA, dD, ddt_bias of a group's tokens
+  float* start;    // forward: [groups][channels][d_state]  the kept state such a sequence begins with in the group
+                   // (behind what the gradients read: among it, their calls took 1 % longer)
   size_t bytes;
 };
 

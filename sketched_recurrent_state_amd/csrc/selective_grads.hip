@@ -158,7 +158,7 @@ __device__ __forceinline__ void part_states(const SelectiveArgs& a, const SelCel
                                             bool began, float (&h)[TB / HB][NS], float (&until)[TB / HB]) {
   static_assert(TB / HB == 2, "two parts");
   const uint32_t at = (uint32_t)(my * N + n0);
-  const size_t step = (size_t)a.channels * N, part = (size_t)kept_place(cell.first, cell.pos + t0 + HB);
+  const size_t step = (size_t)a.channels * N, part = (size_t)(kept_place(cell.first, cell.pos + t0) + 1);
   const float* kept = a.w.states + part * step;
   until[0] = until[1] = 0.f;
   if (began) {
