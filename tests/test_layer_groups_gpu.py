@@ -13,6 +13,7 @@ torch = pytest.importorskip("torch")
 import sketched_recurrent_state_amd as ssm  # noqa: E402
 from sketched_recurrent_state_amd.decoder import SelectiveDecoder  # noqa: E402
 from tests.test_layer_gpu import FILL, Selective, spans  # noqa: E402
+from tests.test_layer_use_gpu import Banded  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +129,53 @@ def test_slow_decays(dtype):
     s.check_forward(out, state)
     assert all(torch.equal(a, b) for a, b in zip(s.forward(in_place=True), (out, state)))
     s.check_backward(s.backward())
+
+
+@pytest.mark.parametrize("index,value", [(1, 0), (1, 5000), (2, 5185), (41, 2 ** 31 - 1), (1, -5), (42 + 1, 2 ** 31 - 1),
+                                         (42 + 1, -1), (42 + 5, 0), (42 + 41, 2 ** 31 - 1), (42 + 2, 121), (84 + 2, 40),
+                                         (84 + 3, -2 ** 31), (84 + 1, 0), (84 + 121, 40), (0, 64), (30, 60)])
+def test_wrong_plans_in_place(index, value):
+    s = Selective("bf16", BATCHES["a chunk then pairs"], 16, 16, pad=0)
+    s.plan[index] = value
+    new = Banded()
+    state = new(s.h0)
+    state.copy_(s.h0)
+    need = torch.empty(ssm.selective_sizes(s.d, s.T)[0], dtype=torch.uint8, device="cuda")
+    ssm.selective_forward(s.d, s.T, s.plan, *s.inputs(), state, new(s.x), **s.more(), state_in=state, workspace=new(need))
+    torch.cuda.synchronize()
+    assert new.intact()
+
+
+def test_captured_in_place():
+    """A prompt continued in place in a graph, replayed: each replay goes on from the last one's states."""
+    s = Selective("bf16", BATCHES["a chunk then pairs"], 48, 16)
+    state, eager = s.h0.clone(), s.h0.clone()
+    out, want = s.rows(), s.rows()
+    call = lambda h, o: ssm.selective_forward(s.d, s.T, s.plan, *s.inputs(), h, o, **s.more(), state_in=h)
+    graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=st):
+        call(state, out)
+    for _ in range(3):
+        before = eager.clone()
+        graph.replay()
+        call(eager, want)
+        apart, end = s.rows(), torch.empty_like(before)
+        ssm.selective_forward(s.d, s.T, s.plan, *s.inputs(), end, apart, **s.more(), state_in=before)
+        torch.randn(1 << 16, device="cuda").sum().item()
+        assert torch.equal(out, want) and torch.equal(state, eager)
+        assert torch.equal(apart, want) and torch.equal(end, eager)
+
+
+def test_two_calls_at_once_in_place():
+    ss = [Selective("bf16", BATCHES["unlike"], 128, 16, seed=k) for k in range(2)]
+    want = [s.forward() for s in ss]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for s, st in zip(ss, streams):
+            with torch.cuda.stream(st):
+                got.append(s.forward(in_place=True))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
