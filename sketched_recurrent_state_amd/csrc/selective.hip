@@ -246,9 +246,10 @@ __global__ void __launch_bounds__(256) selective_step_kernel(const SelectiveArgs
 }  // namespace
 
 // Ten waves a SIMD of the whole GPU in all (6 of the forward pass's and 3 of the gradients' are resident at
-// a time): with fewer, longer groups the last ones leave SIMDs without work. A prompt of 8192 tokens
-// x 5120 channels, by chunks of a group: 3: 342 us, 4: 330, 6: 352, 8: 349, 11: 391, 16: 448; the first pass and the
-// walk back of the gradients of 2 x 2048 tokens: 1: 437 us, 3: 439, 5: 465, 9: 532, 17: 632. Joining the groups before costs a
+// a time): with fewer, longer groups the last ones leave SIMDs without work. By chunks of a group, on a busy GPU, the
+// rule's choice in brackets: a prompt of 8192 tokens x 5120 channels 3: 305 us, 4: 292, [5]: 295, 6: 311, 8: 310, 11: 351,
+// 16: 413; 41 unlike prompts of 8003 tokens 3: 263, 4: 248, 5: 264, [6]: 271, 8: 260, 11: 269, 16: 330; gradients of
+// 2 x 2048 tokens 1: 501, 2: 458, [3]: 464, 5: 484, 9: 549, 17: 654. Joining the groups before costs a
 // group about a fiftieth of a chunk each, so long prompts of few channels get longer groups.
 constexpr int kWaves = 10240;
 SelGroups selective_groups(const ssm_selective_dims& d, int cap) {

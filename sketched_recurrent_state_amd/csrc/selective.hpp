@@ -6,9 +6,10 @@
 // token and channel, and passed through LDS of the wave's own: no workgroup barrier. Per state and
 // token the recurrence is a product, an exp2, a product and two fused ones, so prompts are bound by the
 // vector ALU, not by HBM. (exp2 takes two issue slots here: six a state and token at the least. One prompt of 8192 tokens,
-// 5120 channels x 16 states: the main pass 197 us, 8.3 instructions a state and token, of which 5 are the recurrence,
+// 5120 channels x 16 states: the main pass 169 us, 8.3 instructions a state and token, of which 5 are the recurrence,
 // 0.75 the sum over lanes, the rest softplus, gate, conversions and LDS, all once for 16 states; its vector units
-// issue all the time. The local pass 138 us, 5.6 instructions.)
+// issue all the time. The local pass 122 us, 5.6 instructions. Times are of a GPU that has been busy for 30 ms; its clock
+// rises over them, and the first passes after a pause take 204 and 147 us.)
 //
 // Time is divided too: the plan's 64-token chunks go to `groups` of equal size, whatever sequences
 // they belong to, and a wave walks one group. A sequence that crosses groups needs its state

@@ -10,10 +10,13 @@
 // own for the true states took 79 us), and computes the states between from it. A wave's sums over channels are stored for each
 // token and added up afterwards in a fixed order; those over tokens stay in registers.
 //
-// Bound by the vector ALU: 2 x 2048 tokens, 5120 channels x 16 states, bf16, 303 us of 450 in all, 20 instructions a state
-// and token in the walk (4 to compute a state again, 10 for its gradients, 2 for the sums over a channel's lanes, 4 for
-// those over channels) and 4 around it; the vector ALU is busy nine tenths of the time at the clock it keeps. The first pass
-// 132 us, the sums over channels 34. Eight lanes a channel with two states each (168 registers without the parts) took 530 us.
+// Bound by the vector ALU: 2 x 2048 tokens, 5120 channels x 16 states, bf16, on a busy GPU 292 us of 461 in all, 20
+// instructions a state and token in the walk (4 to compute a state again, 10 for its gradients, 2 for the sums over a
+// channel's lanes, 4 for those over channels) and 4 around it; the vector ALU is busy nine tenths of the time at the clock it
+// keeps. The first pass 127 us, the sums over channels 36, over groups 5 (the first passes after a pause: 337, 145, 36, 5).
+// Eight lanes a channel with two states each (168 registers without the parts) took 530 us at the time, against 370.
+// With 32 and 64 states a wave has 8 and 4 channels, and the sums over them that it stores for every token are 4 and 16 times
+// as many a channel as with 16: 64 prompts of 100 tokens, 5120 channels x 64 states, 3.8 ms.
 #include "selective.hpp"
 
 namespace ssm {
